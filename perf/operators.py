@@ -129,7 +129,7 @@ def prepare(case, seed):
         s["x"] = _normal(gen, rows, d, DTYPES[case["x"]], 1)
         # the weight as a program keeps it: symmetric 8 bits with a scale for each output channel
         w = torch.randn(N, d, device="cuda", generator=gen) * (2.0 * d ** -0.5)
-        s["ws"] = w.abs().amax(1) / 127
+        s["ws"] = _step(w)
         s["wq"] = _padded(N, d, torch.int8, 16)
         s["wq"].copy_(torch.round(w / s["ws"][:, None]).to(torch.int8))
         s["xq"], s["xs"] = _padded(rows, d, torch.int8, 16), torch.empty(rows, device="cuda")
@@ -174,6 +174,12 @@ def _run_own(s):
     return {"lse": s["lse"], "slice": s["slice"]}
 
 
+def _step(x):
+    """Each row's quantisation step: an IEEE quotient (by a tensor: a division by a number multiplies by its reciprocal)."""
+    m = x.abs().amax(1)
+    return m / torch.full_like(m, 127.0)
+
+
 def _row_lse(x):
     m = x.amax(1)
     return m + (x - m[:, None]).exp_().sum(1).log()
@@ -201,14 +207,16 @@ def run(s):
         x = h @ w.T
         lse = _row_lse(x)
         loss = torch.where(live, lse - x.gather(1, at[:, None])[:, 0], 0.0)
+        if op == "loss_grad":
+            x.sub_(lse[:, None]).exp_()
+        lse = torch.where(live, lse, 0.0)  # rows that do not count
         if op == "loss":
             return {"loss": loss, "lse": lse}
-        x.sub_(lse[:, None]).exp_()
         x.scatter_add_(1, at[:, None], torch.full((len(t), 1), -1.0, device="cuda"))
         x.mul_(torch.where(live, s["grad_loss"], 0.0)[:, None])
         return {"loss": loss, "lse": lse, "grad_hidden": (x @ w).bfloat16(), "grad_weight": (x.T @ h).bfloat16()}
     x = s["x"].float()
-    xs = x.abs().amax(1) / 127
+    xs = _step(x)
     q = torch.round(x / torch.where(xs > 0, xs, 1.0)[:, None])
     y = q @ s["wq"].float().T
     y *= xs[:, None]
@@ -229,7 +237,7 @@ def work(case):
         table = V * d * size[case["table"]]
         return {"bytes": n * 4 + live * d * size[case["grad"]] + table * (2 if case["add"] else 1), "flops": live * d}
     if op in ("loss", "loss_grad"):
-        rows, V, d = case["rows"], case["V"], case["d"]
+        rows, V, d = case["rows"] * (1 - case["ignored"]), case["V"], case["d"]  # the rows that count
         inputs, product = 2 * d * (rows + V) + 4 * rows, 2 * rows * V * d
         if op == "loss":
             return {"bytes": inputs + 8 * rows, "flops": product}
@@ -264,6 +272,7 @@ def exact(case, seed):
         logp = torch.mm(h, w.t())
         lse = torch.logsumexp(logp, dim=1)
         logp -= lse[:, None]
+        lse *= keep
         rows = torch.nonzero(keep)[:, 0]
         cols = s["targets"][rows].long()
         loss = torch.zeros(len(h), dtype=f64, device="cuda")
@@ -277,7 +286,7 @@ def exact(case, seed):
         return {"loss": loss, "lse": lse, "grad_hidden": torch.mm(g, w), "grad_weight": torch.mm(g.t(), h)}
     # the quantised values are a definition in 32 bits: x / (amax / 127), each rounded to nearest even
     x = s["x"].float()
-    step = x.abs().max(dim=1, keepdim=True).values / 127
+    step = (x.abs().max(dim=1, keepdim=True).values.to(f64) / 127).float()
     q = torch.where(step == 0, torch.zeros_like(x), torch.round(x / step))
     y = torch.mm(q.to(f64), s["wq"].to(f64).t()) * step.to(f64) * s["ws"].to(f64)[None, :]
     if op == "int8":
