@@ -291,6 +291,132 @@ fr_status fr_beam_read_timing(fr_beam* beam, float* stream_ms, float* select_ms,
 void fr_beam_destroy(fr_beam* beam);
 
 /* ------------------------------------------------------------------------ */
+/* The vocabulary table's two ends around the beam step: the embedding of the
+ * chosen tokens, the training loss of the lm_head projection, and the lm_head
+ * product in 8-bit integers.  No counterpart in the pages, which run the model
+ * itself elsewhere: these are the operators next to the step that read or
+ * write the [V, d] table.
+ *
+ * Common to the three handles (fr_embed, fr_ce, fr_i8): a handle belongs to the
+ * device that was current at its init, and a run with another current device
+ * returns FR_ERR_INVALID_ARG.  Its workspace is shared by all its runs, so runs
+ * of one handle (captured graphs included) must be ordered one after another,
+ * by one stream or by events; use one handle per stream for runs that may
+ * overlap.  Runs allocate nothing, never synchronise and can be captured into a
+ * CUDA graph.  Inputs, outputs and workspace may not overlap, except where an
+ * output is said to be added to.  The status calls are as fr_beam_status:
+ * sticky, first error first, read with a synchronisation of the last run's
+ * stream (not while that stream is being captured). */
+
+/* Token embedding.  V x d table, up to max_tokens tokens per call (< 2^30).
+ * Tokens are int32 in [0, V) or -1 (a dead beam or padding); any other value
+ * is treated as -1 and recorded as FR_ERR_CODE_RANGE.
+ *
+ * fr_embed_lookup:  out[i][j] = scale * table[tokens[i]][j], a row of zeros for
+ * token -1.  One fp32 product, rounded once to the output type.
+ *   table_dev   [V, ldt] of table_dtype, ldt >= d elements
+ *   tokens_dev  int32 [n], n >= 0 (n == 0 does nothing)
+ *   out_dev     [n, ldo] of out_dtype, ldo >= d; columns d.. are left as they are
+ *
+ * fr_embed_grad:  the lookup's gradient,
+ *   grad_table[v][j] = [accumulate] grad_table[v][j] + scale * sum_{i: tokens[i] = v} grad_out[i][j].
+ * The sum is fp32 in an order that depends on the tokens alone (no
+ * floating-point atomics; the tokens are sorted first, so repeated tokens are
+ * neighbours); it is scaled, added and rounded once.
+ * accumulate = 0 writes every row of the table (zeros where no token fell);
+ * accumulate = 1 adds to the rows that tokens fell on and leaves the others
+ * untouched, e.g. to add to a tied lm_head's gradient.
+ * Any pointer aligned to its element size and any row pitch is taken; rows that
+ * start on 16 bytes move in 16-byte pieces. */
+typedef struct fr_embed fr_embed;
+fr_status fr_embed_init(int32_t V, int32_t d, int32_t max_tokens, fr_embed** out);
+fr_status fr_embed_lookup(fr_embed* embed, const void* table_dev, int64_t ldt, fr_dtype table_dtype,
+                          const int32_t* tokens_dev, int32_t n, float scale, void* out_dev, int64_t ldo,
+                          fr_dtype out_dtype, fr_stream stream);
+fr_status fr_embed_grad(fr_embed* embed, const void* grad_out_dev, int64_t ldg, fr_dtype grad_dtype,
+                        const int32_t* tokens_dev, int32_t n, float scale, void* grad_table_dev, int64_t ldt,
+                        fr_dtype table_dtype, int32_t accumulate, fr_stream stream);
+fr_status fr_embed_status(fr_embed* embed);
+fr_status fr_embed_clear_status(fr_embed* embed, fr_stream stream);
+void fr_embed_destroy(fr_embed* embed);
+
+/* Softmax cross entropy of the lm_head projection, in pieces of the vocabulary:
+ * the [rows, V] logits x = h W^T are never written.  Up to max_rows rows
+ * (<= 2^24) of bf16 hidden states h [rows, ldh] against the bf16 weight
+ * W [V, ldw], fp32 accumulation.  targets: int32 [rows] in [0, V), or -1 for a
+ * row that does not count; any other value is recorded as FR_ERR_CODE_RANGE,
+ * its row's loss and lse are NaN, and it takes no part in the gradients.
+ *
+ * fr_ce_loss:  lse[r] = log sum_v e^x[r][v], loss[r] = lse[r] - x[r][targets[r]]
+ * (fp32 [rows]); both are 0 for rows that do not count, whose hidden states are
+ * not read (they may hold NaN).  A row whose lse is not finite is recorded as
+ * FR_ERR_NAN_LOGIT.
+ *
+ * fr_ce_grad:  with G[r][v] = grad_loss[r] * (e^(x[r][v] - lse[r]) - [v == targets[r]]),
+ *   grad_hidden [rows, ldgh] = G W     (bf16; rows that do not count: zeros)
+ *   grad_weight [V, ldgw]    = G^T h   (bf16; every row is written)
+ * from the lse that fr_ce_loss gave for the same inputs and grad_loss fp32
+ * [rows] (for a mean, 1 / the rows that count).  The logits are computed again,
+ * a piece of the vocabulary at a time; G is rounded to bf16 (the products'
+ * operand type), all sums are fp32, each output is rounded once.  Either output
+ * may be NULL and is then not computed; rows == 0 writes zeros to grad_weight.
+ *
+ * h and W: base 16-byte aligned, pitches multiples of 8 elements (else
+ * FR_ERR_INVALID_ARG).  The gradients' base and pitch only need the element's
+ * alignment; 16-byte aligned ones are written faster.  init allocates about
+ * max_rows * (32 KB + 6 d) bytes.  The kernels take one CTA per SM and all of
+ * its tensor memory while they run, as fr_lmhead_run does. */
+typedef struct fr_ce fr_ce;
+fr_status fr_ce_init(int32_t V, int32_t d, int32_t max_rows, fr_ce** out);
+fr_status fr_ce_loss(fr_ce* ce, const void* hidden_dev, int64_t ldh, const void* weight_dev, int64_t ldw,
+                     const int32_t* targets_dev, int32_t rows, float* loss_dev, float* lse_dev, fr_stream stream);
+fr_status fr_ce_grad(fr_ce* ce, const void* hidden_dev, int64_t ldh, const void* weight_dev, int64_t ldw,
+                     const int32_t* targets_dev, const float* lse_dev, const float* grad_loss_dev, int32_t rows,
+                     void* grad_hidden_dev, int64_t ldgh, void* grad_weight_dev, int64_t ldgw, fr_stream stream);
+fr_status fr_ce_status(fr_ce* ce);
+fr_status fr_ce_clear_status(fr_ce* ce, fr_stream stream);
+void fr_ce_destroy(fr_ce* ce);
+
+/* The lm_head product (or any [N, d] weight's) in 8-bit integers, with a scale
+ * for each token and each output channel.
+ *
+ * fr_i8_quantize:  for each row r of x [rows, ldx] (FR_F32 or FR_BF16),
+ *   scale[r] = max_j |x[r][j]| / 127,  q[r][j] = x[r][j] / scale[r] rounded to
+ *   nearest even (IEEE fp32 quotients, clamped to [-127, 127]),
+ * for tokens before a product, or once for a weight's output channels.  A row
+ * of zeros has scale 0 and zeros; a row with a NaN or an infinity keeps it as
+ * its scale with zeros, so its products are NaN.  q: int8 [rows, ldq], columns
+ * d.. left as they are.  It needs no handle.
+ *
+ * fr_i8_init keeps the weight: int8 [N, ldw] and fp32 channel scales [N]
+ * (caller-owned, valid and unchanged for the handle's lifetime), d <= 131,071
+ * (the int32 sums cannot overflow), and the SID range for fr_i8_lse.
+ *
+ * fr_i8_matmul:  out[r][n] = (sum_j xq[r][j] * wq[n][j]) * xscale[r] * wscale[n]
+ *   into out [rows, ldo] of FR_F32 or FR_BF16, ldo >= N: with the lm_head as the
+ *   weight, logits rows for fr_beam_step.  Exact int32 sums, two fp32 products,
+ *   one rounding to the output type.
+ * fr_i8_lse:  the same product reduced to lse [rows] and the SID slice
+ *   [rows, sid_span] for fr_beam_step_lse, without writing the [rows, N]
+ *   product; a row whose lse is not finite is recorded as FR_ERR_NAN_LOGIT.
+ *
+ * xq and wq: base 16-byte aligned, pitches multiples of 16 (else
+ * FR_ERR_INVALID_ARG); out needs its element's alignment.  The tile kernels take
+ * one CTA per SM and its tensor memory while they run. */
+typedef struct fr_i8 fr_i8;
+fr_status fr_i8_quantize(const void* x_dev, int64_t ldx, fr_dtype dtype, int32_t rows, int32_t d, int8_t* q_dev,
+                         int64_t ldq, float* scale_dev, fr_stream stream);
+fr_status fr_i8_init(const int8_t* weight_dev, int64_t ldw, const float* wscale_dev, int32_t N, int32_t d,
+                     int32_t max_rows, int32_t sid_base, int32_t sid_span, fr_i8** out);
+fr_status fr_i8_matmul(fr_i8* i8, const int8_t* xq_dev, int64_t ldx, const float* xscale_dev, int32_t rows,
+                       void* out_dev, int64_t ldo, fr_dtype out_dtype, fr_stream stream);
+fr_status fr_i8_lse(fr_i8* i8, const int8_t* xq_dev, int64_t ldx, const float* xscale_dev, int32_t rows,
+                    float* lse_dev, float* slice_dev, fr_stream stream);
+fr_status fr_i8_status(fr_i8* i8);
+fr_status fr_i8_clear_status(fr_i8* i8, fr_stream stream);
+void fr_i8_destroy(fr_i8* i8);
+
+/* ------------------------------------------------------------------------ */
 /* Test hooks for the failure path (no counterpart in the pages).  Every wait
  * a kernel makes on an mbarrier or on a flag set by another warp is bounded:
  * when the limit passes, the kernel records FR_ERR_DEVICE in the handle's
@@ -301,7 +427,7 @@ void fr_beam_destroy(fr_beam* beam);
  *   wait_limit_ns  limit of those waits, 1,000 .. 60,000,000,000 ns, or 0 for
  *                  the default (2 s)
  *   starve_copies  1: the producer warp of the streaming kernel (for a beam)
- *                  or of the lm_head kernel issues no copies at all, so the
+ *                  or of the tensor-core kernels issues no copies at all, so the
  *                  consumers' first wait cannot complete and expires after
  *                  wait_limit_ns; 0: normal operation
  * Host-side settings that apply from the next fr_beam_step /
@@ -311,6 +437,8 @@ void fr_beam_destroy(fr_beam* beam);
  * operation. */
 fr_status fr_beam_set_wait_test(fr_beam* beam, uint64_t wait_limit_ns, int32_t starve_copies);
 fr_status fr_lmhead_set_wait_test(fr_lmhead* lmhead, uint64_t wait_limit_ns, int32_t starve_copies);
+fr_status fr_ce_set_wait_test(fr_ce* ce, uint64_t wait_limit_ns, int32_t starve_copies);
+fr_status fr_i8_set_wait_test(fr_i8* i8, uint64_t wait_limit_ns, int32_t starve_copies);
 
 /* ------------------------------------------------------------------------ */
 /* Allocation-free row log-sum-exp.  No counterpart in the pages: this is a

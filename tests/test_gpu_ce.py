@@ -1,0 +1,316 @@
+"""Cross entropy of the lm_head projection and its gradients vs the formulas
+in double.
+
+Tolerances, from the arithmetic.  A logit is a d-term dot product of bf16
+values (exact products) accumulated in fp32: its error is at most
+D = d * 2^-23 * sum |h w|.  The log-sum-exp moves by at most the largest D of
+its row, plus the fp32 sum of exponentials: at most 256 sequential terms per
+tile and one per 32 tiles (2^-24 each), exponentials of 2^-22, and the
+rounding of their arguments and of the result (2^-23 of the values' size).
+The gradient's G = g (p - [v = t]) has the error of x and lse in p (relative),
+and is rounded to bf16 (half a step, 2^-8); the sums over V or over the rows
+add (terms) * 2^-23 of the sum of magnitudes, and the output is rounded to
+bf16 once more."""
+import pytest
+import torch
+
+from trie_constrained_beam_fr_b200 import fr
+
+pytestmark = pytest.mark.gpu
+BF16 = torch.bfloat16
+
+
+def _padded(rows, cols, extra=0):
+    """bf16 [rows, cols] whose pitch is a multiple of 8 elements; NaN between the rows."""
+    t = torch.full((rows, -(-cols // 8) * 8 + extra), float("nan"), dtype=BF16, device="cuda")
+    return t[:, :cols]
+
+
+def _inputs(rows, V, d, seed, gain=2.0, ignored=0.2, extra=0):
+    g = torch.Generator().manual_seed(seed)
+    h, w = _padded(rows, d, extra), _padded(V, d, extra)
+    h.copy_(torch.randn(rows, d, generator=g))
+    w.copy_(torch.randn(V, d, generator=g) * gain / d ** 0.5)
+    t = torch.randint(0, V, (rows,), generator=g, dtype=torch.int32)
+    t[torch.rand(rows, generator=g) < ignored] = -1
+    gl = torch.rand(rows, generator=g) * 2 - 0.5
+    return h, w, t.cuda(), gl.cuda()
+
+
+def _reference(h, w, t, gl):
+    h, w, t, gl = h.double().cpu(), w.double().cpu(), t.long().cpu(), gl.double().cpu()
+    live = t >= 0
+    h = torch.where(live[:, None], h, 0.0)
+    d, V, n = h.shape[1], w.shape[0], max(1, int(live.sum()))
+    x = h @ w.T
+    D = d * 2.0 ** -23 * (h.abs() @ w.abs().T)
+    big = x.abs().amax(1)
+    lse = torch.logsumexp(x, 1)
+    b_lse = D.amax(1) + (256 + V / 8192 + 8) * 2.0 ** -24 + 2.0 ** -22 + 2.0 ** -23 * (lse.abs() + 3 * big)
+    at = t.clamp(min=0)[:, None]
+    loss = lse - x.gather(1, at)[:, 0]
+    b_loss = b_lse + D.gather(1, at)[:, 0] + 2.0 ** -24 * loss.abs()
+    p = torch.exp(x - lse[:, None])
+    hot = torch.zeros_like(p).scatter_(1, at, 1.0)
+    gl = torch.where(live, gl, 0.0)
+    G = (p - hot) * gl[:, None]
+    b_p = p * torch.expm1(D + (b_lse + 2.0 ** -22 + 2.0 ** -23 * (lse.abs() + big))[:, None])
+    b_G = (b_p + 2.0 ** -23 * (p + hot)) * gl.abs()[:, None]
+    b_G = b_G + 2.0 ** -8 * (G.abs() + b_G)
+    m = G.abs() + b_G
+    dh, dw = G @ w, G.T @ h
+    b_dh = b_G @ w.abs() + V * 2.0 ** -23 * (m @ w.abs())
+    b_dw = b_G.T @ h.abs() + n * 2.0 ** -23 * (m.T @ h.abs())
+    zero = torch.zeros_like(lse)
+    return dict(lse=(torch.where(live, lse, zero), b_lse), loss=(torch.where(live, loss, zero), b_loss),
+                dh=(dh, b_dh + 2.0 ** -8 * (dh.abs() + b_dh)), dw=(dw, b_dw + 2.0 ** -8 * (dw.abs() + b_dw)))
+
+
+def _close(got, ref):
+    want, bound = ref
+    err = (got.double().cpu() - want).abs()
+    assert torch.all(err <= bound), "largest error over its bound: %.3g" % float((err / bound.clamp(min=1e-300)).max())
+
+
+@pytest.fixture
+def handle():
+    made = []
+
+    def make(*a):
+        made.append(fr.fr_ce_init(*a))
+        return made[-1]
+
+    yield make
+    for h in made:
+        fr.fr_ce_destroy(h)
+
+
+def _loss(ce, h, w, t):
+    loss, lse = torch.full((len(t),), 7.0, device="cuda"), torch.full((len(t),), 7.0, device="cuda")
+    fr.fr_ce_loss(ce, h, w, t, loss, lse)
+    return loss, lse
+
+
+def _grad(ce, h, w, t, lse, gl, pad=0, offset=0):
+    """Gradients into tensors whose rows start `offset` elements into their
+    storage, `pad` elements apart; checks that nothing else was written."""
+    outs = []
+    for rows in (h.shape[0], w.shape[0]):
+        d = h.shape[1]
+        flat = torch.full((rows * (d + pad) + offset + 8,), 5.0, dtype=BF16, device="cuda")
+        outs.append(flat[offset:offset + rows * (d + pad)].view(rows, d + pad)[:, :d])
+    fr.fr_ce_grad(ce, h, w, t, lse, gl, *outs)
+    for o in outs:
+        mask = torch.ones_like(o._base, dtype=torch.bool)
+        mask[offset:offset + o.shape[0] * (o.shape[1] + pad)].view(o.shape[0], o.shape[1] + pad)[:, :o.shape[1]] = False
+        assert torch.all(o._base[mask] == 5.0)
+    return outs
+
+
+@pytest.mark.parametrize("rows,V,d,ignored,gain,pad,offset", [
+    (1, 1, 1, 0.0, 1.0, 0, 0),
+    (1, 300, 64, 0.0, 2.0, 0, 0),
+    (5, 64, 8, 0.2, 2.0, 0, 0),
+    (130, 257, 72, 0.3, 2.0, 3, 1),
+    (300, 1000, 200, 0.5, 2.0, 8, 8),
+    (128, 256, 256, 0.0, 2.0, 0, 0),
+    (129, 8500, 64, 0.0, 2.0, 0, 0),     # two pieces of the vocabulary
+    (64, 20000, 137, 0.1, 2.0, 0, 0),    # three pieces, an odd hidden size, few rows
+    (700, 3000, 520, 0.1, 30.0, 0, 0),   # peaked rows: probabilities near 0 and 1
+    (260, 16400, 264, 0.9, 2.0, 5, 0),   # most rows do not count; last piece of 16 tokens
+])
+def test_loss_and_gradients(handle, rows, V, d, ignored, gain, pad, offset):
+    h, w, t, gl = _inputs(rows, V, d, rows + V + d, gain, ignored, extra=8 if pad else 0)
+    ce = handle(V, d, rows)
+    loss, lse = _loss(ce, h, w, t)
+    dh, dw = _grad(ce, h, w, t, lse, gl, pad, offset)
+    assert fr.fr_ce_status(ce) == fr.FR_OK
+    ref = _reference(h, w, t, gl)
+    _close(lse, ref["lse"])
+    _close(loss, ref["loss"])
+    _close(dh, ref["dh"])
+    _close(dw, ref["dw"])
+    # the same again, bit for bit, and each gradient alone
+    a, b = _grad(ce, h, w, t, lse, gl, pad, offset)
+    assert torch.equal(a, dh) and torch.equal(b, dw)
+    a, b = torch.empty_like(dh), torch.empty_like(dw)
+    fr.fr_ce_grad(ce, h, w, t, lse, gl, a, None)
+    fr.fr_ce_grad(ce, h, w, t, lse, gl, None, b)
+    assert torch.equal(a, dh) and torch.equal(b, dw)
+
+
+def test_gradients_against_differences(handle):
+    """The loss along a direction: (L(h + e) - L(h - e)) / 2 in double, from
+    losses of bf16 inputs moved by one exact step, against the gradients.  The
+    central difference is off by a third derivative (|x| moved by at most
+    2^-4: under 2^-12 of the magnitude sum) and each gradient by its bound."""
+    rows, V, d = 40, 90, 24
+    h, w, t, gl = _inputs(rows, V, d, 3)
+    ce = handle(V, d, rows)
+    loss, lse = _loss(ce, h, w, t)
+    dh, dw = _grad(ce, h, w, t, lse, gl)
+    ref = _reference(h, w, t, gl)
+
+    def total(hh, ww):
+        x = hh @ ww.T
+        live = t.cpu() >= 0
+        each = torch.logsumexp(x, 1) - x.gather(1, t.long().cpu().clamp(min=0)[:, None])[:, 0]
+        return (each * gl.double().cpu())[live].sum()
+
+    hd, wd = h.double().cpu(), w.double().cpu()
+    e = 2.0 ** -10
+    g = torch.Generator().manual_seed(1)
+    for _ in range(4):
+        sh, sw = torch.randn(rows, d, generator=g).double().sign(), torch.randn(V, d, generator=g).double().sign()
+        diff = (total(hd + e * sh, wd + e * sw) - total(hd - e * sh, wd - e * sw)) / (2 * e)
+        along = (dh.double().cpu() * sh).sum() + (dw.double().cpu() * sw).sum()
+        slack = ref["dh"][1].sum() + ref["dw"][1].sum()
+        third = 2.0 ** -12 * gl.double().abs().sum().cpu()
+        assert abs(diff - along) <= slack + third
+
+
+def test_rows_that_do_not_count_reach_nothing(handle):
+    rows, V, d = 200, 500, 64
+    h, w, t, gl = _inputs(rows, V, d, 11, ignored=0.4)
+    ref = _reference(h, w, t, gl)
+    dead = t < 0
+    h[dead] = float("nan")
+    h[int(torch.nonzero(dead)[0, 0])] = float("inf")
+    gl[dead] = float("nan")
+    ce = handle(V, d, rows)
+    loss, lse = _loss(ce, h, w, t)
+    dh, dw = _grad(ce, h, w, t, lse, gl)
+    assert fr.fr_ce_status(ce) == fr.FR_OK
+    for got, name in ((loss, "loss"), (lse, "lse"), (dh, "dh"), (dw, "dw")):
+        _close(got, ref[name])
+    assert torch.all(loss[dead] == 0) and torch.all(lse[dead] == 0) and torch.all(dh[dead] == 0)
+
+
+@pytest.mark.parametrize("rows", [0, 1, 150])
+def test_no_row_counts(handle, rows):
+    V, d = 300, 40
+    h, w, t, gl = _inputs(rows, V, d, 1, ignored=2.0)
+    ce = handle(V, d, 150)
+    h.fill_(float("nan"))
+    loss, lse = _loss(ce, h, w, t)
+    dh, dw = _grad(ce, h, w, t, lse, gl)
+    assert fr.fr_ce_status(ce) == fr.FR_OK
+    for x in (loss, lse, dh, dw):
+        assert torch.all(x == 0)
+
+
+def test_fewer_rows_than_the_handle_holds(handle):
+    V, d = 700, 96
+    h, w, t, gl = _inputs(400, V, d, 21)
+    ce = handle(V, d, 400)
+    for n in (400, 3, 129):
+        loss, lse = _loss(ce, h[:n], w, t[:n])
+        dh, dw = _grad(ce, h[:n], w, t[:n], lse, gl[:n])
+        ref = _reference(h[:n], w, t[:n], gl[:n])
+        for got, name in ((loss, "loss"), (lse, "lse"), (dh, "dh"), (dw, "dw")):
+            _close(got, ref[name])
+
+
+def test_targets_out_of_range_are_recorded(handle):
+    h, w, t, gl = _inputs(6, 50, 16, 2, ignored=0.0)
+    ref = _reference(h, w, torch.where(torch.arange(6).cuda() % 3 == 1, -1, t).int(), gl)
+    t[1], t[4] = 50, -2
+    ce = handle(50, 16, 6)
+    loss, lse = _loss(ce, h, w, t)
+    assert fr.fr_ce_status(ce) == fr.FR_ERR_CODE_RANGE
+    fr.fr_ce_clear_status(ce)
+    assert fr.fr_ce_status(ce) == fr.FR_OK
+    assert torch.all(torch.isnan(loss[[1, 4]])) and torch.all(torch.isnan(lse[[1, 4]]))
+    keep = [0, 2, 3, 5]
+    _close(loss[keep], tuple(x[keep] for x in ref["loss"]))
+    dh, dw = _grad(ce, h, w, t, lse, gl)
+    assert fr.fr_ce_status(ce) == fr.FR_ERR_CODE_RANGE
+    _close(dh, ref["dh"])
+    _close(dw, ref["dw"])
+
+
+def test_a_row_that_is_not_finite_is_recorded(handle):
+    h, w, t, gl = _inputs(5, 40, 16, 4, ignored=0.0)
+    h[3, 2] = float("nan")
+    ce = handle(40, 16, 5)
+    loss, lse = _loss(ce, h, w, t)
+    assert fr.fr_ce_status(ce) == fr.FR_ERR_NAN_LOGIT
+    assert torch.isnan(loss[3]) and torch.all(torch.isfinite(loss[[0, 1, 2, 4]]))
+
+
+def test_graph_and_another_stream(handle):
+    rows, V, d = 150, 9000, 72
+    sets = [_inputs(rows, V, d, s, ignored=i) for s, i in ((1, 0.1), (2, 0.7))]
+    ce = handle(V, d, rows)
+    want = []
+    for h, w, t, gl in sets:
+        loss, lse = _loss(ce, h, w, t)
+        want.append((loss, *_grad(ce, h, w, t, lse, gl)))
+    h, w, t, gl = (x.clone(memory_format=torch.preserve_format) for x in sets[0])
+    h, w = _padded(rows, d), _padded(V, d)
+    loss, lse = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    dh, dw = torch.empty(rows, d, dtype=BF16, device="cuda"), torch.empty(V, d, dtype=BF16, device="cuda")
+
+    def run():
+        fr.fr_ce_loss(ce, h, w, t, loss, lse)
+        fr.fr_ce_grad(ce, h, w, t, lse, gl, dh, dw)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        run()
+    for (a, b, c, e), (x, y, z) in list(zip(sets, want)) * 2:  # the number of rows that count changes between replays
+        h.copy_(a), w.copy_(b), t.copy_(c), gl.copy_(e)
+        graph.replay()
+        assert torch.equal(loss, x) and torch.equal(dh, y) and torch.equal(dw, z)
+    with torch.cuda.stream(s):
+        s.wait_stream(torch.cuda.default_stream())
+        dw.fill_(4.0)
+        run()
+    s.synchronize()
+    assert torch.equal(dw, want[1][2])
+
+
+def test_a_wait_that_expires(handle):
+    """The producer issues no copies: loss and gradient give up after 1 ms,
+    record it, and the handle works again afterwards."""
+    h, w, t, gl = _inputs(60, 700, 64, 8)
+    ref = _reference(h, w, t, gl)
+    ce = handle(700, 64, 60)
+    loss, lse = _loss(ce, h, w, t)
+    dh, dw = torch.empty(60, 64, dtype=BF16, device="cuda"), torch.empty(700, 64, dtype=BF16, device="cuda")
+    for call in (lambda: fr.fr_ce_loss(ce, h, w, t, loss.clone(), lse.clone()),
+                 lambda: fr.fr_ce_grad(ce, h, w, t, lse, gl, dh, dw)):
+        fr.fr_ce_set_wait_test(ce, 1_000_000, True)
+        call()
+        assert fr.fr_ce_status(ce) == fr.FR_ERR_DEVICE
+        fr.fr_ce_set_wait_test(ce, 0, False)
+        fr.fr_ce_clear_status(ce)
+    dh, dw = _grad(ce, h, w, t, lse, gl)
+    assert fr.fr_ce_status(ce) == fr.FR_OK
+    _close(dh, ref["dh"])
+    _close(dw, ref["dw"])
+
+
+def test_refusals(handle):
+    h, w, t, gl = _inputs(8, 40, 32, 0)
+    ce = handle(40, 32, 8)
+    loss, lse = torch.empty(8, device="cuda"), torch.empty(8, device="cuda")
+    dh, dw = torch.empty(8, 32, dtype=BF16, device="cuda"), torch.empty(40, 32, dtype=BF16, device="cuda")
+    for bad in (lambda: fr.fr_ce_loss(ce, h.float(), w, t, loss, lse), lambda: fr.fr_ce_loss(ce, h[:, :31], w, t, loss, lse),
+                lambda: fr.fr_ce_loss(ce, h, w[:39], t, loss, lse), lambda: fr.fr_ce_loss(ce, h, w, t.long(), loss, lse),
+                lambda: fr.fr_ce_loss(ce, h, w, t, loss[:7], lse), lambda: fr.fr_ce_loss(ce, h, w, t.cpu(), loss, lse),
+                lambda: fr.fr_ce_grad(ce, h, w, t, lse, gl[:7], dh, dw), lambda: fr.fr_ce_grad(ce, h, w, t, lse, gl, dh.float(), dw),
+                lambda: fr.fr_ce_grad(ce, h, w, t, lse, gl, dh, dw[:39])):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(fr.FrError):  # neither gradient
+        fr.fr_ce_grad(ce, h, w, t, lse, gl, None, None)
+    with pytest.raises(fr.FrError):  # more rows than the handle holds
+        fr.fr_ce_loss(ce, *_inputs(9, 40, 32, 0)[:3], torch.empty(9, device="cuda"), torch.empty(9, device="cuda"))
+    odd = torch.zeros(8, 33, dtype=BF16, device="cuda")[:, :32]
+    with pytest.raises(fr.FrError):  # pitch not a multiple of 8
+        fr.fr_ce_loss(ce, odd, w, t, loss, lse)
+    with pytest.raises(fr.FrError):  # base not on 16 bytes
+        fr.fr_ce_loss(ce, torch.zeros(8 * 32 + 8, dtype=BF16, device="cuda")[1:257].view(8, 32), w, t, loss, lse)

@@ -25,10 +25,11 @@ ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 
 TARGETS = {
-    "libfr.so": ["fr_trie.cu", "fr_step.cu", "fr_select.cu", "fr_beam.cu", "fr_noalloc.cu", "fr_lmhead.cu"],
+    "libfr.so": ["fr_trie.cu", "fr_step.cu", "fr_select.cu", "fr_beam.cu", "fr_noalloc.cu", "fr_lmhead.cu",
+                 "fr_i8.cu", "fr_ce.cu", "fr_embed.cu"],
     "libfr_gen.so": ["fr_gen.cu"],
 }
-HEADERS = ["fr_internal.cuh", "fr_handles.h", "fr_step.cuh", "fr_topk.cuh"]
+HEADERS = ["fr_internal.cuh", "fr_handles.h", "fr_step.cuh", "fr_topk.cuh", "fr_tc.cuh", "fr_gemm.cuh"]
 
 
 def lib_path(name: str) -> str:

@@ -1,0 +1,642 @@
+// fr_ce.cu -- softmax cross entropy of the lm_head projection, and its
+// gradients, without keeping the [rows, V] logits.
+//
+//   x = h W^T,  lse_r = log sum_v e^(x_rv),  loss_r = lse_r - x_{r, t_r}
+//   G_rv = g_r (e^(x_rv - lse_r) - [v = t_r]),  dh = G W,  dW = G^T h
+//
+// Rows whose target is -1 take no part: they are left out of the products
+// altogether (the other rows are packed together first), so a NaN in an
+// ignored row's hidden state reaches nothing and a batch that is mostly
+// prompt costs only its counted rows.
+//
+//   k_ce_gather   packs the counted rows: hidden states, targets, (gradients:
+//                 lse and g) and their row numbers; zero rows up to the next
+//                 multiple of 128.
+//   k_ce_loss     tcgen05 tiles of x (128 rows x 256 tokens); the epilogue
+//                 keeps a (max, scaled sum) partial per row and tile and the
+//                 target's logit.  k_ce_combine: lse and loss.
+//   k_ce_grad     works through the vocabulary in pieces: for a piece, tiles
+//                 of x are computed again and turned into G (bf16, the only
+//                 piece that is kept), then dh += G W_piece (fp32 partials
+//                 over the pieces) and dW_piece = G^T h.  One launch runs the
+//                 products of one piece and the G tiles of the next, so that
+//                 no tile type leaves SMs idle at its end.  The transposed
+//                 operands are read in place: their shared-memory tiles are
+//                 MN-major.
+//   k_ce_finish   dh = sum of the fp32 partials, rounded, at the original rows.
+//
+// G is rounded to bf16, the operand type of the products: half a step (2^-8)
+// of each entry, the same as one rounding of the inputs.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <new>
+
+#include "fr.h"
+#include "fr_gemm.cuh"
+#include "fr_handles.h"
+#include "fr_internal.cuh"
+
+namespace fr {
+namespace {
+
+constexpr int CE_BN = 256;
+constexpr int CE_STAGES = 4;
+constexpr int CE_PIECE = 8192;  // tokens per piece of the gradient
+constexpr float CE_L2E = 1.4426950408889634f;
+
+// The packed rows and what belongs to them.
+struct CeRows {
+    __nv_bfloat16* h;  // [cap, pitch]
+    int64_t pitch;
+    int32_t* tgt;      // [cap]
+    float* lse;        // [cap]
+    float* g;          // [cap]
+    int32_t* idx;      // [cap] original row
+    int32_t* n;        // [1] counted rows
+};
+
+// A CTA packs 64 consecutive rows: it counts the counted rows before its own
+// (reading the targets up to there), so no CTA waits for another.
+constexpr int CE_GATHER_ROWS = 64;
+constexpr int CE_GATHER_THREADS = 256;
+__global__ void __launch_bounds__(CE_GATHER_THREADS)
+    k_ce_gather(const __nv_bfloat16* __restrict__ hidden, int64_t ldh, const int32_t* __restrict__ targets,
+                const float* __restrict__ lse, const float* __restrict__ grad_loss, int32_t rows, int32_t V, int32_t d,
+                CeRows out, float* __restrict__ loss_out, float* __restrict__ lse_out,
+                __nv_bfloat16* __restrict__ grad_hidden, int64_t ldgh, int32_t* __restrict__ err) {
+    __shared__ int32_t before_s, pos_s[CE_GATHER_ROWS], total_s;
+    griddep_wait();
+    griddep_launch_dependents();
+    const int32_t r0 = blockIdx.x * CE_GATHER_ROWS, tid = threadIdx.x;
+    if (tid == 0) before_s = 0;
+    __syncthreads();
+    int32_t c = 0;
+#pragma unroll 4
+    for (int32_t i = tid; i < r0; i += CE_GATHER_THREADS) {
+        const int32_t t = targets[i];
+        c += t >= 0 && t < V;
+    }
+    c = __reduce_add_sync(0xffffffffu, c);
+    if ((tid & 31) == 0 && c) atomicAdd(&before_s, c);
+    __syncthreads();
+    if (tid < 32) {
+        int32_t at = before_s;
+        for (int k = 0; k < CE_GATHER_ROWS; k += 32) {
+            const int32_t r = r0 + k + tid;
+            const int32_t t = r < rows ? targets[r] : -1;
+            const bool live = t >= 0 && t < V;
+            const uint32_t m = __ballot_sync(0xffffffffu, live);
+            const int32_t pos = at + __popc(m & ((1u << tid) - 1u));
+            pos_s[k + tid] = live ? pos : -1;
+            if (live) {
+                out.tgt[pos] = t;
+                out.idx[pos] = r;
+                if (lse) {
+                    out.lse[pos] = lse[r];
+                    out.g[pos] = grad_loss[r];
+                }
+            } else if (r < rows) {
+                const bool bad = t != -1;
+                if (bad) set_error(err, FR_ERR_CODE_RANGE);
+                if (loss_out) {
+                    loss_out[r] = bad ? NAN : 0.f;
+                    lse_out[r] = bad ? NAN : 0.f;
+                }
+            }
+            at += __popc(m);
+        }
+        if (tid == 0) total_s = at;
+    }
+    __syncthreads();
+    const bool hvec = (d & 7) == 0;  // rows start on 16 bytes (checked by the caller)
+    const int32_t vecs = d >> 3;
+    for (int k = tid >> 5; k < CE_GATHER_ROWS; k += CE_GATHER_THREADS / 32) {
+        const int32_t r = r0 + k, lane = tid & 31;
+        if (r >= rows) break;
+        const int32_t pos = pos_s[k];
+        if (pos >= 0) {
+            const uint4* src = reinterpret_cast<const uint4*>(hidden + r * ldh);
+            uint4* dst = reinterpret_cast<uint4*>(out.h + pos * out.pitch);
+#pragma unroll 4
+            for (int32_t i = lane; i < vecs; i += 32) dst[i] = src[i];
+            if (!hvec)
+                for (int32_t j = (vecs << 3) + lane; j < d; j += 32) out.h[pos * out.pitch + j] = hidden[r * ldh + j];
+        } else if (grad_hidden) {
+            for (int32_t j = lane; j < d; j += 32) grad_hidden[r * ldgh + j] = __float2bfloat16_rn(0.f);
+        }
+    }
+    if (blockIdx.x == gridDim.x - 1) {
+        const int32_t n = total_s, end = max((n + GM_BM - 1) / GM_BM, 1) * GM_BM;
+        for (int32_t r = n + (tid >> 5); r < end; r += CE_GATHER_THREADS / 32)
+            for (int32_t j = tid & 31; j < out.pitch; j += 32) out.h[r * out.pitch + j] = __float2bfloat16_rn(0.f);
+        if (tid == 0) *out.n = n;
+    }
+}
+
+__device__ __forceinline__ int32_t ce_m_tiles(int32_t n) { return max((n + GM_BM - 1) / GM_BM, 1); }
+
+struct CeLoss {
+    static constexpr bool I8 = false;
+    static constexpr int BN = CE_BN, STAGES = CE_STAGES;
+    struct Tile {
+        int nk, m0, n0;
+        uint32_t idesc;
+    };
+    struct State {
+        int32_t n, m_tiles;
+    };
+    CUtensorMap map_h, map_w;
+    CeRows rows;
+    int32_t V, k_blocks, n_tiles;
+    float2* partial;  // [cap, n_tiles]
+    float* xt;        // [cap] the target's logit
+
+    __device__ __forceinline__ State begin() const {
+        const int32_t n = *rows.n;
+        return {n, n ? ce_m_tiles(n) : 0};
+    }
+    __device__ __forceinline__ bool tile(const State& st, int i, Tile& t) const {
+        const int64_t g = blockIdx.x + (int64_t)i * gridDim.x;
+        if (g >= (int64_t)st.m_tiles * n_tiles) return false;
+        t.m0 = (int)(g % st.m_tiles) * GM_BM;
+        t.n0 = (int)(g / st.m_tiles) * BN;
+        t.nk = k_blocks;
+        t.idesc = gm_idesc(false, BN);
+        return true;
+    }
+    __device__ __forceinline__ bool a_mn(const Tile&) const { return false; }
+    __device__ __forceinline__ bool b_mn(const Tile&) const { return false; }
+    __device__ __forceinline__ void load(const Tile& t, int kb, uint8_t* a, uint8_t* b, uint64_t* bar) const {
+        tc_tma_load_2d(&map_h, a, bar, kb * 64, t.m0);
+        tc_tma_load_2d(&map_w, b, bar, kb * 64, t.n0);
+    }
+    __device__ __forceinline__ void epilogue(const State& st, const Tile& t, uint32_t taddr, int r) const {
+        const int row = t.m0 + r;
+        const int32_t tgt = row < st.n ? rows.tgt[row] : -1;
+        float m = -INFINITY, s = 0.f;
+#pragma unroll 1
+        for (int c = 0; c < BN && t.n0 + c < V; c += 32) {
+            const int n = t.n0 + c;
+            float v[32];
+            tc_tmem_ld32(taddr + (uint32_t)c, v);
+            if ((uint32_t)(tgt - n) < 32u) {
+                float x = 0.f;
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (n + i == tgt) x = v[i];
+                xt[row] = x;
+            }
+            if (n + 32 > V) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (n + i >= V) v[i] = -INFINITY;
+            }
+            gm_lse_fold(v, m, s);
+        }
+        if (row < st.n) partial[(int64_t)row * n_tiles + t.n0 / BN] = make_float2(m, s);
+    }
+};
+
+__global__ void __launch_bounds__(GM_THREADS, 1) k_ce_loss(const __grid_constant__ CeLoss p, const GmCtl ctl) {
+    gm_run(p, ctl);
+}
+
+__global__ void __launch_bounds__(256) k_ce_combine(const float2* __restrict__ partial, int32_t n_tiles, CeRows rows,
+                                                    const float* __restrict__ xt, float* __restrict__ loss,
+                                                    float* __restrict__ lse, int32_t* __restrict__ err) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t c = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (c >= *rows.n) return;
+    const float v = gm_lse_combine(partial + c * n_tiles, n_tiles);
+    if ((threadIdx.x & 31) == 0) {
+        const int32_t r = rows.idx[c];
+        if (!isfinite(v)) set_error(err, FR_ERR_NAN_LOGIT);
+        lse[r] = v;
+        loss[r] = v - xt[c];
+    }
+}
+
+// One launch of the gradient: the products of one piece (tokens [v0, v1),
+// G in buffer `buf`) and the G tiles of the next (tokens [w0, w1), buffer
+// buf ^ 1).  Empty ranges leave their part out.
+struct CeGrad {
+    static constexpr bool I8 = false;
+    static constexpr int BN = CE_BN, STAGES = CE_STAGES;
+    enum { DH, DW, GT };
+    struct Tile {
+        int nk, type, m0, n0, k0, split;
+        uint32_t idesc;
+    };
+    struct State {
+        int32_t n, m_tiles, dh_tiles, dw_tiles, g_tiles;
+    };
+    CUtensorMap map_h_k, map_h_mn;   // packed rows: K-major (128 x 64) and MN-major (64 x 64) boxes
+    CUtensorMap map_w_k, map_w_mn;   // weight: K-major (256 x 64) and MN-major (64 x 64) boxes
+    CUtensorMap map_g_k, map_g_mn;   // G of the piece whose products run
+    CeRows rows;
+    __nv_bfloat16* g_next;           // G of the piece whose tiles are computed
+    int64_t g_pitch;
+    int32_t V, d, d_tiles, splits, first;
+    int32_t v0, v1, w0, w1;
+    float* dh;                       // [splits, cap, pitch] fp32 partials, null: no dh
+    int64_t dh_split;                // cap * pitch
+    __nv_bfloat16* dw;               // the caller's dW, null: no dW
+    int64_t ldw;
+    int32_t dw_vec;
+
+    __device__ __forceinline__ State begin() const {
+        State st;
+        st.n = *rows.n;
+        st.m_tiles = ce_m_tiles(st.n);
+        st.dh_tiles = dh && v1 > v0 && st.n ? st.m_tiles * d_tiles * splits : 0;
+        st.dw_tiles = dw && v1 > v0 ? (v1 - v0 + GM_BM - 1) / GM_BM * d_tiles : 0;
+        st.g_tiles = w1 > w0 ? (w1 - w0 + BN - 1) / BN * st.m_tiles : 0;
+        return st;
+    }
+    __device__ __forceinline__ bool tile(const State& st, int i, Tile& t) const {
+        int g = blockIdx.x + i * gridDim.x;
+        if (g < st.dh_tiles) {
+            const int kb = (v1 - v0 + 63) / 64, per = (kb + splits - 1) / splits;
+            t.type = DH;
+            t.m0 = g % st.m_tiles * GM_BM;
+            g /= st.m_tiles;
+            t.n0 = g % d_tiles * BN;
+            t.split = g / d_tiles;
+            t.k0 = t.split * per;
+            t.nk = max(min(per, kb - t.k0), 0);
+            t.idesc = gm_idesc(false, BN, false, true);
+            return true;
+        }
+        g -= st.dh_tiles;
+        if (g < st.dw_tiles) {
+            t.type = DW;
+            t.n0 = g % d_tiles * BN;
+            t.m0 = g / d_tiles * GM_BM;
+            t.k0 = 0;
+            t.nk = max((st.n + 63) / 64, 1);
+            t.idesc = gm_idesc(false, BN, true, true);
+            return true;
+        }
+        g -= st.dw_tiles;
+        if (g < st.g_tiles) {
+            t.type = GT;
+            t.m0 = g % st.m_tiles * GM_BM;
+            t.n0 = g / st.m_tiles * BN;
+            t.k0 = 0;
+            t.nk = (d + 63) / 64;
+            t.idesc = gm_idesc(false, BN);
+            return true;
+        }
+        return false;
+    }
+    __device__ __forceinline__ bool a_mn(const Tile& t) const { return t.type == DW; }
+    __device__ __forceinline__ bool b_mn(const Tile& t) const { return t.type != GT; }
+    __device__ __forceinline__ void load(const Tile& t, int kb, uint8_t* a, uint8_t* b, uint64_t* bar) const {
+        const int k = (t.k0 + kb) * 64;
+        if (t.type == GT) {
+            tc_tma_load_2d(&map_h_k, a, bar, k, t.m0);
+            tc_tma_load_2d(&map_w_k, b, bar, k, w0 + t.n0);
+        } else if (t.type == DH) {
+            tc_tma_load_2d(&map_g_k, a, bar, k, t.m0);
+#pragma unroll
+            for (int j = 0; j < BN / 64; ++j) tc_tma_load_2d(&map_w_mn, b + j * 8192, bar, t.n0 + j * 64, v0 + k);
+        } else {
+#pragma unroll
+            for (int j = 0; j < GM_BM / 64; ++j) tc_tma_load_2d(&map_g_mn, a + j * 8192, bar, t.m0 + j * 64, k);
+#pragma unroll
+            for (int j = 0; j < BN / 64; ++j) tc_tma_load_2d(&map_h_mn, b + j * 8192, bar, t.n0 + j * 64, k);
+        }
+    }
+    __device__ __forceinline__ void epilogue(const State& st, const Tile& t, uint32_t taddr, int r) const {
+        const int row = t.m0 + r;
+        if (t.type == GT) {
+            const bool live = row < st.n;
+            const float g = live ? rows.g[row] : 0.f, nl = live ? -rows.lse[row] * CE_L2E : 0.f;
+            const int32_t tgt = live ? rows.tgt[row] - w0 : -1;  // column in the piece
+            __nv_bfloat16* dst = g_next + row * g_pitch + t.n0;
+            const int width = w1 - w0 - t.n0;  // columns of this tile that are tokens
+#pragma unroll 1
+            for (int c = 0; c < BN; c += 32) {
+                float v[32];
+                tc_tmem_ld32(taddr + (uint32_t)c, v);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const float p = tc_ex2(fmaf(v[i], CE_L2E, nl)) - (t.n0 + c + i == tgt ? 1.f : 0.f);
+                    v[i] = live && c + i < width ? p * g : 0.f;  // zeros feed the products' ragged ends
+                }
+                gm_store32(dst + c, v, 32, true);
+            }
+        } else if (t.type == DH) {
+            if (t.nk == 0 && !first) return;  // a split without tokens adds nothing
+            float* dst = dh + t.split * dh_split + row * rows.pitch + t.n0;
+#pragma unroll 1
+            for (int c = 0; c < BN && t.n0 + c < d; c += 32) {
+                float v[32];
+                tc_tmem_ld32(taddr + (uint32_t)c, v);
+                if (row >= st.n) continue;
+#pragma unroll
+                for (int i = 0; i < 32; i += 4) {
+                    if (t.n0 + c + i < d) {  // the pitch is a multiple of 8: whole groups of 4 stay in the row
+                        float4* o = reinterpret_cast<float4*>(dst + c + i);
+                        float4 x = t.nk ? make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (!first) {
+                            const float4 y = *o;
+                            x.x += y.x;
+                            x.y += y.y;
+                            x.z += y.z;
+                            x.w += y.w;
+                        }
+                        *o = x;
+                    }
+                }
+            }
+        } else {
+            const int v = v0 + row;
+#pragma unroll 1
+            for (int c = 0; c < BN && t.n0 + c < d; c += 32) {
+                float x[32];
+                tc_tmem_ld32(taddr + (uint32_t)c, x);
+                if (v < v1) gm_store32(dw + v * ldw + t.n0 + c, x, min(32, d - t.n0 - c), dw_vec != 0);
+            }
+        }
+    }
+};
+
+__global__ void __launch_bounds__(GM_THREADS, 1) k_ce_grad(const __grid_constant__ CeGrad p, const GmCtl ctl) {
+    gm_run(p, ctl);
+}
+
+// A warp per packed row: the splits' partials in split order, one rounding.
+__global__ void __launch_bounds__(256) k_ce_finish(const float* __restrict__ dh, int64_t dh_split, int32_t splits,
+                                                   int32_t d, CeRows rows, __nv_bfloat16* __restrict__ grad_hidden,
+                                                   int64_t ldgh, int32_t vec) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t c = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (c >= *rows.n) return;
+    const float* src = dh + c * rows.pitch;
+    __nv_bfloat16* dst = grad_hidden + rows.idx[c] * ldgh;
+    for (int32_t j = (threadIdx.x & 31) * 4; j < d; j += 128) {
+        float4 x = *reinterpret_cast<const float4*>(src + j);
+        for (int k = 1; k < splits; ++k) {
+            const float4 y = *reinterpret_cast<const float4*>(src + k * dh_split + j);
+            x.x += y.x;
+            x.y += y.y;
+            x.z += y.z;
+            x.w += y.w;
+        }
+        if (vec && j + 4 <= d) {
+            const __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), b = __floats2bfloat162_rn(x.z, x.w);
+            *reinterpret_cast<uint2*>(dst + j) =
+                make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+        } else {
+            dst[j] = __float2bfloat16_rn(x.x);
+            if (j + 1 < d) dst[j + 1] = __float2bfloat16_rn(x.y);
+            if (j + 2 < d) dst[j + 2] = __float2bfloat16_rn(x.z);
+            if (j + 3 < d) dst[j + 3] = __float2bfloat16_rn(x.w);
+        }
+    }
+}
+
+int64_t ce_round(int64_t x, int64_t q) { return (x + q - 1) / q * q; }
+
+// Splits of dh's token axis within a piece: enough tiles for every SM when
+// there are few rows.
+int32_t ce_splits(int32_t sms, int64_t m_tiles, int64_t d_tiles) {
+    return (int32_t)std::max<int64_t>(1, std::min<int64_t>(16, sms / (m_tiles * d_tiles)));
+}
+
+}  // namespace
+}  // namespace fr
+
+struct fr_ce {
+    int32_t V = 0, d = 0, max_rows = 0, n_tiles = 0, sms = 0, device = 0, piece = 0;
+    int64_t cap = 0;
+    fr::CeRows rows{};
+    float2* partial = nullptr;       // [cap, n_tiles]
+    float* xt = nullptr;             // [cap]
+    __nv_bfloat16* g[2] = {};        // [cap, piece] each
+    float* dh = nullptr;             // fp32 partials of dh
+    int32_t* err = nullptr;
+    CUtensorMap map_h_k, map_h_mn, map_g_k[2], map_g_mn[2];
+    cudaStream_t last_stream = nullptr;
+    uint64_t wait_ns = FR_WAIT_LIMIT_NS;
+    int32_t starve = 0;
+};
+
+namespace {
+
+void ce_free(fr_ce* h) {
+    cudaFree(h->rows.h);
+    cudaFree(h->rows.tgt);
+    cudaFree(h->partial);
+    cudaFree(h->g[0]);
+    cudaFree(h->dh);
+    cudaFree(h->err);
+    delete h;
+}
+
+// What the loss and the gradient both ask of their arguments.
+bool ce_bad_inputs(const fr_ce* h, const void* hidden, int64_t ldh, const void* weight, int64_t ldw,
+                   const int32_t* targets, int32_t rows, const void* lse) {
+    return !h || !hidden || !weight || !targets || !lse || rows < 0 || rows > h->max_rows || ldh < h->d || ldw < h->d ||
+           (ldh & 7) || (ldw & 7) || (reinterpret_cast<uintptr_t>(hidden) & 15u) ||
+           (reinterpret_cast<uintptr_t>(weight) & 15u) || (reinterpret_cast<uintptr_t>(targets) & 3u) ||
+           (reinterpret_cast<uintptr_t>(lse) & 3u);
+}
+
+bool ce_on_device(const fr_ce* h) {
+    int dev = -1;
+    return cudaGetDevice(&dev) == cudaSuccess && dev == h->device;
+}
+
+}  // namespace
+
+extern "C" fr_status fr_ce_init(int32_t V, int32_t d, int32_t max_rows, fr_ce** out) {
+    if (!out) return FR_ERR_INVALID_ARG;
+    *out = nullptr;
+    if (V < 1 || d < 1 || max_rows < 1 || max_rows > (1 << 24)) return FR_ERR_INVALID_ARG;
+    fr_ce* h = new (std::nothrow) fr_ce();
+    if (!h) return FR_ERR_OOM;
+    h->V = V;
+    h->d = d;
+    h->max_rows = max_rows;
+    h->cap = fr::ce_round(max_rows, fr::GM_BM);
+    h->n_tiles = (V + fr::CE_BN - 1) / fr::CE_BN;
+    h->piece = (int32_t)std::min<int64_t>(fr::CE_PIECE, fr::ce_round(V, fr::CE_BN));
+    h->rows.pitch = fr::ce_round(d, 8);
+    if (cudaGetDevice(&h->device) != cudaSuccess ||
+        cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, h->device) != cudaSuccess ||
+        cudaFuncSetAttribute(fr::k_ce_loss, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)fr::gm_smem_bytes<fr::CeLoss>()) != cudaSuccess ||
+        cudaFuncSetAttribute(fr::k_ce_grad, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)fr::gm_smem_bytes<fr::CeGrad>()) != cudaSuccess) {
+        (void)cudaGetLastError();
+        delete h;
+        return FR_ERR_CUDA;
+    }
+    const size_t cap = (size_t)h->cap, pitch = (size_t)h->rows.pitch, d_tiles = (d + fr::CE_BN - 1) / fr::CE_BN;
+    // dh partials: one plane of all rows, or, with few rows, at most one tile row per SM
+    const size_t dh_rows = std::max(cap, std::max<size_t>(h->sms / d_tiles, 1) * fr::GM_BM);
+    cudaError_t e = cudaMalloc(&h->rows.h, cap * pitch * 2);
+    if (e == cudaSuccess) e = cudaMalloc(&h->rows.tgt, cap * 4 * 5 + 4);
+    if (e == cudaSuccess) e = cudaMalloc(&h->partial, cap * h->n_tiles * sizeof(float2));
+    if (e == cudaSuccess) e = cudaMalloc(&h->g[0], cap * h->piece * 2 * 2);
+    if (e == cudaSuccess) e = cudaMalloc(&h->dh, dh_rows * pitch * 4);
+    if (e == cudaSuccess) e = cudaMalloc(&h->err, sizeof(int32_t));
+    if (e == cudaSuccess) e = cudaMemset(h->err, 0, sizeof(int32_t));
+    if (e != cudaSuccess) {
+        (void)cudaGetLastError();
+        ce_free(h);
+        return e == cudaErrorMemoryAllocation ? FR_ERR_OOM : FR_ERR_CUDA;
+    }
+    h->rows.lse = reinterpret_cast<float*>(h->rows.tgt + cap);
+    h->rows.g = h->rows.lse + cap;
+    h->xt = h->rows.g + cap;
+    h->rows.idx = reinterpret_cast<int32_t*>(h->xt + cap);
+    h->rows.n = h->rows.idx + cap;
+    h->g[1] = h->g[0] + cap * h->piece;
+    bool ok = fr::gm_encode(&h->map_h_k, false, h->rows.h, h->cap, d, h->rows.pitch * 2, fr::GM_BM) &&
+              fr::gm_encode(&h->map_h_mn, false, h->rows.h, h->cap, d, h->rows.pitch * 2, 64);
+    for (int b = 0; b < 2; ++b)
+        ok = ok && fr::gm_encode(&h->map_g_k[b], false, h->g[b], h->cap, h->piece, (int64_t)h->piece * 2, fr::GM_BM) &&
+             fr::gm_encode(&h->map_g_mn[b], false, h->g[b], h->cap, h->piece, (int64_t)h->piece * 2, 64);
+    if (!ok) {
+        ce_free(h);
+        return FR_ERR_CUDA;
+    }
+    *out = h;
+    return FR_OK;
+}
+
+extern "C" fr_status fr_ce_loss(fr_ce* h, const void* hidden_dev, int64_t ldh, const void* weight_dev, int64_t ldw,
+                                const int32_t* targets_dev, int32_t rows, float* loss_dev, float* lse_dev,
+                                fr_stream stream) {
+    if (ce_bad_inputs(h, hidden_dev, ldh, weight_dev, ldw, targets_dev, rows, lse_dev) || !loss_dev ||
+        (reinterpret_cast<uintptr_t>(loss_dev) & 3u) || !ce_on_device(h))
+        return FR_ERR_INVALID_ARG;
+    const cudaStream_t s = (cudaStream_t)stream;
+    h->last_stream = s;
+    if (rows == 0) return FR_OK;
+    fr::CeLoss p{};
+    if (!fr::gm_encode(&p.map_w, false, weight_dev, h->V, h->d, ldw * 2, fr::CE_BN)) return FR_ERR_CUDA;
+    p.map_h = h->map_h_k;
+    p.rows = h->rows;
+    p.V = h->V;
+    p.k_blocks = (h->d + 63) / 64;
+    p.n_tiles = h->n_tiles;
+    p.partial = h->partial;
+    p.xt = h->xt;
+    const int32_t gather = (rows + fr::CE_GATHER_ROWS - 1) / fr::CE_GATHER_ROWS;
+    FR_CUDA_TRY(fr::launch_pdl(fr::k_ce_gather, gather, fr::CE_GATHER_THREADS, 0, s, (const __nv_bfloat16*)hidden_dev, ldh,
+                               targets_dev, (const float*)nullptr, (const float*)nullptr, rows, h->V, h->d, h->rows,
+                               loss_dev, lse_dev, (__nv_bfloat16*)nullptr, (int64_t)0, h->err));
+    const int64_t tiles = fr::ce_round(rows, fr::GM_BM) / fr::GM_BM * h->n_tiles;
+    fr::GmCtl ctl{h->err, h->wait_ns, h->starve};
+    FR_CUDA_TRY(fr::launch_pdl(fr::k_ce_loss, std::min<int64_t>(tiles, h->sms), fr::GM_THREADS,
+                               fr::gm_smem_bytes<fr::CeLoss>(), s, p, ctl));
+    FR_CUDA_TRY(fr::launch_pdl(fr::k_ce_combine, ((int64_t)rows + 7) / 8, 256, 0, s, (const float2*)h->partial, h->n_tiles,
+                               h->rows, (const float*)h->xt, loss_dev, lse_dev, h->err));
+    return FR_OK;
+}
+
+extern "C" fr_status fr_ce_grad(fr_ce* h, const void* hidden_dev, int64_t ldh, const void* weight_dev, int64_t ldw,
+                                const int32_t* targets_dev, const float* lse_dev, const float* grad_loss_dev,
+                                int32_t rows, void* grad_hidden_dev, int64_t ldgh, void* grad_weight_dev, int64_t ldgw,
+                                fr_stream stream) {
+    if (ce_bad_inputs(h, hidden_dev, ldh, weight_dev, ldw, targets_dev, rows, lse_dev) || !grad_loss_dev ||
+        (reinterpret_cast<uintptr_t>(grad_loss_dev) & 3u) || (!grad_hidden_dev && !grad_weight_dev) ||
+        (grad_hidden_dev && (ldgh < h->d || (reinterpret_cast<uintptr_t>(grad_hidden_dev) & 1u))) ||
+        (grad_weight_dev && (ldgw < h->d || (reinterpret_cast<uintptr_t>(grad_weight_dev) & 1u))) ||
+        !ce_on_device(h))
+        return FR_ERR_INVALID_ARG;
+    const cudaStream_t s = (cudaStream_t)stream;
+    h->last_stream = s;
+    fr::CeGrad p{};
+    if (!fr::gm_encode(&p.map_w_k, false, weight_dev, h->V, h->d, ldw * 2, fr::CE_BN) ||
+        !fr::gm_encode(&p.map_w_mn, false, weight_dev, h->V, h->d, ldw * 2, 64))
+        return FR_ERR_CUDA;
+    __nv_bfloat16* gh = (__nv_bfloat16*)grad_hidden_dev;
+    const int64_t m_tiles = fr::ce_round(std::max(rows, 1), fr::GM_BM) / fr::GM_BM;  // no rows: dW is still written (zeros)
+    p.map_h_k = h->map_h_k;
+    p.map_h_mn = h->map_h_mn;
+    p.rows = h->rows;
+    p.g_pitch = h->piece;
+    p.V = h->V;
+    p.d = h->d;
+    p.d_tiles = (h->d + fr::CE_BN - 1) / fr::CE_BN;
+    p.splits = fr::ce_splits(h->sms, m_tiles, p.d_tiles);
+    p.dh = gh ? h->dh : nullptr;
+    p.dh_split = m_tiles * fr::GM_BM * h->rows.pitch;
+    p.dw = (__nv_bfloat16*)grad_weight_dev;
+    p.ldw = ldgw;
+    p.dw_vec = (reinterpret_cast<uintptr_t>(grad_weight_dev) & 15u) == 0 && (ldgw & 7) == 0;
+    const int32_t gather = std::max((rows + fr::CE_GATHER_ROWS - 1) / fr::CE_GATHER_ROWS, 1);
+    FR_CUDA_TRY(fr::launch_pdl(fr::k_ce_gather, gather, fr::CE_GATHER_THREADS, 0, s, (const __nv_bfloat16*)hidden_dev, ldh,
+                               targets_dev, lse_dev, grad_loss_dev, rows, h->V, h->d, h->rows, (float*)nullptr,
+                               (float*)nullptr, gh, ldgh, h->err));
+    fr::GmCtl ctl{h->err, h->wait_ns, h->starve};
+    const int32_t pieces = (h->V + h->piece - 1) / h->piece;
+    for (int32_t k = 0; k <= pieces; ++k) {
+        p.v0 = p.v1 = p.w0 = p.w1 = 0;
+        int64_t tiles = 0;
+        if (k > 0) {
+            p.v0 = (k - 1) * h->piece;
+            p.v1 = std::min(h->V, k * h->piece);
+            p.first = k == 1;
+            p.map_g_k = h->map_g_k[(k - 1) & 1];
+            p.map_g_mn = h->map_g_mn[(k - 1) & 1];
+            if (gh) tiles += m_tiles * p.d_tiles * p.splits;
+            if (p.dw) tiles += (int64_t)(p.v1 - p.v0 + fr::GM_BM - 1) / fr::GM_BM * p.d_tiles;
+        }
+        if (k < pieces) {
+            p.w0 = k * h->piece;
+            p.w1 = std::min(h->V, (k + 1) * h->piece);
+            p.g_next = h->g[k & 1];
+            tiles += (int64_t)(p.w1 - p.w0 + fr::CE_BN - 1) / fr::CE_BN * m_tiles;
+        }
+        FR_CUDA_TRY(fr::launch_pdl(fr::k_ce_grad, std::min<int64_t>(tiles, h->sms), fr::GM_THREADS,
+                                   fr::gm_smem_bytes<fr::CeGrad>(), s, p, ctl));
+    }
+    if (gh && rows > 0)
+        FR_CUDA_TRY(fr::launch_pdl(fr::k_ce_finish, ((int64_t)rows + 7) / 8, 256, 0, s, (const float*)h->dh, p.dh_split,
+                                   p.splits, h->d, h->rows, gh, ldgh,
+                                   (int32_t)((reinterpret_cast<uintptr_t>(gh) & 7u) == 0 && (ldgh & 3) == 0)));
+    return FR_OK;
+}
+
+extern "C" fr_status fr_ce_status(fr_ce* h) {
+    if (!h) return FR_ERR_INVALID_ARG;
+    FR_CUDA_TRY(cudaStreamSynchronize(h->last_stream));
+    int32_t err = 0;
+    FR_CUDA_TRY(cudaMemcpy(&err, h->err, sizeof(int32_t), cudaMemcpyDeviceToHost));
+    return (fr_status)err;
+}
+
+extern "C" fr_status fr_ce_clear_status(fr_ce* h, fr_stream stream) {
+    if (!h) return FR_ERR_INVALID_ARG;
+    const cudaStream_t s = (cudaStream_t)stream;
+    FR_CUDA_TRY(cudaMemsetAsync(h->err, 0, sizeof(int32_t), s));
+    h->last_stream = s;
+    return FR_OK;
+}
+
+extern "C" fr_status fr_ce_set_wait_test(fr_ce* h, uint64_t wait_limit_ns, int32_t starve_copies) {
+    if (!h || (wait_limit_ns != 0 && (wait_limit_ns < 1000ull || wait_limit_ns > 60000000000ull)) ||
+        (starve_copies != 0 && starve_copies != 1))
+        return FR_ERR_INVALID_ARG;
+    h->wait_ns = wait_limit_ns ? wait_limit_ns : FR_WAIT_LIMIT_NS;
+    h->starve = starve_copies;
+    return FR_OK;
+}
+
+extern "C" void fr_ce_destroy(fr_ce* h) {
+    if (!h) return;
+    ce_free(h);
+}

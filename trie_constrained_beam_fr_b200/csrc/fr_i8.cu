@@ -1,0 +1,389 @@
+// fr_i8.cu -- the lm_head product in 8-bit integers with a scale for each
+// token and each output channel.
+//
+//   scale_r = max_j |x_rj| / 127,  q_rj = rne(x_rj / scale_r)
+//   y_rn    = (sum_j q_rj w_nj) * scale_r * wscale_n
+//
+// The sums are int32 (exact: d <= 131,071), so only the two products by the
+// scales round.  The row and channel scales factor out of the sum, which is
+// why the whole product runs on integers.
+//
+//   k_i8_quantize  a warp per row; reads the row twice (maximum, then values).
+//   k_i8_out       tcgen05 kind::i8 tiles of 128 rows x 256 channels; the
+//                  epilogue scales and writes logits (bf16 or fp32).
+//   k_i8_lse       the same product whose epilogue reduces each row to
+//                  (max, scaled sum) partials and writes the SID slice, for
+//                  the step from rows; k_i8_combine merges the partials.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <new>
+
+#include "fr.h"
+#include "fr_gemm.cuh"
+#include "fr_handles.h"
+#include "fr_internal.cuh"
+
+namespace fr {
+namespace {
+
+template <class T>
+__device__ __forceinline__ float i8_load(const T* p);
+template <>
+__device__ __forceinline__ float i8_load(const float* p) { return *p; }
+template <>
+__device__ __forceinline__ float i8_load(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+
+// q of one value: the quotient and its rounding are IEEE (nearest even); a
+// row whose scale is zero or not finite quantises to zeros (a scale that is
+// not finite makes every product of the row NaN or infinite).
+__device__ __forceinline__ int8_t i8_quant(float x, float scale, bool live) {
+    return live ? (int8_t)__float2int_rn(fminf(fmaxf(__fdiv_rn(x, scale), -127.f), 127.f)) : (int8_t)0;
+}
+
+template <class T>
+__global__ void __launch_bounds__(256) k_i8_quantize(const T* __restrict__ x, int64_t ldx, int32_t rows, int32_t d,
+                                                     int8_t* __restrict__ q, int64_t ldq, float* __restrict__ scale) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (r >= rows) return;
+    const T* xr = x + r * ldx;
+    float m = 0.f;
+    bool nan = false;
+    for (int j = lane; j < d; j += 32) {
+        const float v = i8_load(xr + j);
+        nan |= v != v;
+        m = fmaxf(m, fabsf(v));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (__any_sync(0xffffffffu, nan)) m = NAN;
+    const float s = __fdiv_rn(m, 127.f);
+    const bool live = s > 0.f && isfinite(s);
+    for (int j = lane; j < d; j += 32) q[r * ldq + j] = i8_quant(i8_load(xr + j), s, live);
+    if (lane == 0) scale[r] = s;
+}
+
+// Tile walk shared by the two products: m fastest, so CTAs running together
+// share the weight tile and the activations stay in L2.
+struct I8Base {
+    static constexpr bool I8 = true;
+    static constexpr int BN = 256, STAGES = 4;
+    struct Tile {
+        int nk, m0, n0;
+        uint32_t idesc;
+    };
+    CUtensorMap map_x, map_w;
+    int32_t rows, N, k_blocks, m_tiles, n_tiles;
+    const float* xs;
+    const float* ws;
+    int32_t ws_vec;  // ws starts on 16 bytes
+
+    struct State {};
+    __device__ __forceinline__ State begin() const { return {}; }
+    __device__ __forceinline__ bool tile(const State&, int i, Tile& t) const {
+        const int64_t g = blockIdx.x + (int64_t)i * gridDim.x;
+        if (g >= (int64_t)m_tiles * n_tiles) return false;
+        t.m0 = (int)(g % m_tiles) * GM_BM;
+        t.n0 = (int)(g / m_tiles) * BN;
+        t.nk = k_blocks;
+        t.idesc = gm_idesc(true, BN);
+        return true;
+    }
+    __device__ __forceinline__ bool a_mn(const Tile&) const { return false; }
+    __device__ __forceinline__ bool b_mn(const Tile&) const { return false; }
+    __device__ __forceinline__ void load(const Tile& t, int kb, uint8_t* a, uint8_t* b, uint64_t* bar) const {
+        tc_tma_load_2d(&map_x, a, bar, kb * GM_KB_BYTES, t.m0);
+        tc_tma_load_2d(&map_w, b, bar, kb * GM_KB_BYTES, t.n0);
+    }
+    // y of 32 columns from n on: the row's scale first, then the channel's
+    __device__ __forceinline__ void scaled(uint32_t taddr, int n, float xscale, float (&v)[32]) const {
+        int32_t acc[32];
+        gm_ld32_i32(taddr, acc);
+        if (ws_vec && n + 32 <= N) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+                const float4 w = __ldg(reinterpret_cast<const float4*>(ws + n + i));
+                v[i] = (float)acc[i] * xscale * w.x;
+                v[i + 1] = (float)acc[i + 1] * xscale * w.y;
+                v[i + 2] = (float)acc[i + 2] * xscale * w.z;
+                v[i + 3] = (float)acc[i + 3] * xscale * w.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = n + i < N ? (float)acc[i] * xscale * __ldg(ws + n + i) : 0.f;
+        }
+    }
+};
+
+template <class T>
+struct I8Out : I8Base {
+    T* out;
+    int64_t ldo;
+    int32_t out_vec;
+    __device__ __forceinline__ void epilogue(const State&, const Tile& t, uint32_t taddr, int r) const {
+        const int row = t.m0 + r;
+        const float xscale = row < rows ? xs[row] : 0.f;
+#pragma unroll 1
+        for (int c = 0; c < BN && t.n0 + c < N; c += 32) {
+            float v[32];
+            scaled(taddr + (uint32_t)c, t.n0 + c, xscale, v);
+            if (row < rows) gm_store32(out + row * ldo + t.n0 + c, v, min(32, N - t.n0 - c), out_vec != 0);
+        }
+    }
+};
+
+struct I8Lse : I8Base {
+    float2* partial;  // [rows, n_tiles]
+    float* slice;     // [rows, sid_span]
+    int32_t sid_base, sid_span;
+    __device__ __forceinline__ void epilogue(const State&, const Tile& t, uint32_t taddr, int r) const {
+        const int row = t.m0 + r;
+        const float xscale = row < rows ? xs[row] : 0.f;
+        float m = -INFINITY, s = 0.f;
+#pragma unroll 1
+        for (int c = 0; c < BN && t.n0 + c < N; c += 32) {
+            const int n = t.n0 + c;
+            float v[32];
+            scaled(taddr + (uint32_t)c, n, xscale, v);
+            const int lo = max(n, sid_base), hi = min(n + 32, sid_base + sid_span);
+            if (row < rows && lo < hi) {
+                float* dst = slice + (int64_t)row * sid_span;
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (n + i >= lo && n + i < hi) dst[n + i - sid_base] = v[i];
+            }
+            if (n + 32 > N) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (n + i >= N) v[i] = -INFINITY;
+            }
+            gm_lse_fold(v, m, s);
+        }
+        if (row < rows) partial[(int64_t)row * n_tiles + t.n0 / BN] = make_float2(m, s);
+    }
+};
+
+template <class P>
+__global__ void __launch_bounds__(GM_THREADS, 1) k_i8(const __grid_constant__ P p, const GmCtl ctl) {
+    gm_run(p, ctl);
+}
+
+__global__ void __launch_bounds__(256) k_i8_combine(const float2* __restrict__ partial, int32_t rows, int32_t n_tiles,
+                                                    float* __restrict__ lse, int32_t* __restrict__ err) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (r >= rows) return;
+    const float v = gm_lse_combine(partial + r * n_tiles, n_tiles);
+    if ((threadIdx.x & 31) == 0) {
+        if (!isfinite(v)) set_error(err, FR_ERR_NAN_LOGIT);
+        lse[r] = v;
+    }
+}
+
+}  // namespace
+}  // namespace fr
+
+struct fr_i8 {
+    const int8_t* wq = nullptr;
+    const float* ws = nullptr;
+    int32_t N = 0, d = 0, max_rows = 0, sid_base = 0, sid_span = 0, n_tiles = 0, sms = 0, device = 0;
+    CUtensorMap map_w;
+    float2* partial = nullptr;  // [max_rows, n_tiles]
+    int32_t* err = nullptr;
+    cudaStream_t last_stream = nullptr;
+    uint64_t wait_ns = FR_WAIT_LIMIT_NS;
+    int32_t starve = 0;
+};
+
+namespace {
+
+bool i8_on_device(const fr_i8* h) {
+    int dev = -1;
+    return cudaGetDevice(&dev) == cudaSuccess && dev == h->device;
+}
+
+fr_status i8_base(fr_i8* h, const int8_t* xq, int64_t ldx, const float* xs, int32_t rows, fr::I8Base* b) {
+    if (!fr::gm_encode(&b->map_x, true, xq, rows, h->d, ldx, fr::GM_BM)) return FR_ERR_CUDA;
+    b->map_w = h->map_w;
+    b->rows = rows;
+    b->N = h->N;
+    b->k_blocks = (h->d + fr::GM_KB_BYTES - 1) / fr::GM_KB_BYTES;
+    b->m_tiles = (rows + fr::GM_BM - 1) / fr::GM_BM;
+    b->n_tiles = h->n_tiles;
+    b->xs = xs;
+    b->ws = h->ws;
+    b->ws_vec = (reinterpret_cast<uintptr_t>(h->ws) & 15u) == 0;
+    return FR_OK;
+}
+
+template <class P>
+fr_status i8_launch(fr_i8* h, const P& p, cudaStream_t s) {
+    fr::GmCtl ctl{h->err, h->wait_ns, h->starve};
+    const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles;
+    FR_CUDA_TRY(fr::launch_pdl(fr::k_i8<P>, std::min<int64_t>(tiles, h->sms), fr::GM_THREADS, fr::gm_smem_bytes<P>(), s,
+                               p, ctl));
+    return FR_OK;
+}
+
+bool i8_bad_x(const fr_i8* h, const int8_t* xq, int64_t ldx, const float* xs, int32_t rows) {
+    return !h || !xq || !xs || rows < 0 || rows > h->max_rows || ldx < h->d || (ldx & 15) ||
+           (reinterpret_cast<uintptr_t>(xq) & 15u) || (reinterpret_cast<uintptr_t>(xs) & 3u);
+}
+
+}  // namespace
+
+extern "C" fr_status fr_i8_quantize(const void* x_dev, int64_t ldx, fr_dtype dtype, int32_t rows, int32_t d,
+                                    int8_t* q_dev, int64_t ldq, float* scale_dev, fr_stream stream) {
+    if (!x_dev || !q_dev || !scale_dev || rows < 0 || d < 1 || ldx < d || ldq < d ||
+        (dtype != FR_F32 && dtype != FR_BF16) ||
+        (reinterpret_cast<uintptr_t>(x_dev) & (dtype == FR_F32 ? 3u : 1u)) ||
+        (reinterpret_cast<uintptr_t>(scale_dev) & 3u))
+        return FR_ERR_INVALID_ARG;
+    if (rows == 0) return FR_OK;
+    const cudaStream_t s = (cudaStream_t)stream;
+    const int64_t grid = ((int64_t)rows + 7) / 8;
+    if (dtype == FR_F32)
+        FR_CUDA_TRY(fr::launch_pdl(fr::k_i8_quantize<float>, grid, 256, 0, s, (const float*)x_dev, ldx, rows, d, q_dev,
+                                   ldq, scale_dev));
+    else
+        FR_CUDA_TRY(fr::launch_pdl(fr::k_i8_quantize<__nv_bfloat16>, grid, 256, 0, s, (const __nv_bfloat16*)x_dev, ldx,
+                                   rows, d, q_dev, ldq, scale_dev));
+    return FR_OK;
+}
+
+extern "C" fr_status fr_i8_init(const int8_t* weight_dev, int64_t ldw, const float* wscale_dev, int32_t N, int32_t d,
+                                int32_t max_rows, int32_t sid_base, int32_t sid_span, fr_i8** out) {
+    if (!out) return FR_ERR_INVALID_ARG;
+    *out = nullptr;
+    if (!weight_dev || !wscale_dev || N < 1 || d < 1 || d > 131071 || ldw < d || max_rows < 1 || sid_base < 0 ||
+        sid_span < 0 || (int64_t)sid_base + sid_span > N)
+        return FR_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(weight_dev) & 15u) || (ldw & 15) || (reinterpret_cast<uintptr_t>(wscale_dev) & 3u))
+        return FR_ERR_INVALID_ARG;
+    fr_i8* h = new (std::nothrow) fr_i8();
+    if (!h) return FR_ERR_OOM;
+    h->wq = weight_dev;
+    h->ws = wscale_dev;
+    h->N = N;
+    h->d = d;
+    h->max_rows = max_rows;
+    h->sid_base = sid_base;
+    h->sid_span = sid_span;
+    h->n_tiles = (N + fr::I8Base::BN - 1) / fr::I8Base::BN;
+    const int smem = (int)fr::gm_smem_bytes<fr::I8Base>();
+    if (cudaGetDevice(&h->device) != cudaSuccess ||
+        cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, h->device) != cudaSuccess ||
+        !fr::gm_encode(&h->map_w, true, weight_dev, N, d, ldw, fr::I8Base::BN) ||
+        cudaFuncSetAttribute(fr::k_i8<fr::I8Out<float>>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+        cudaFuncSetAttribute(fr::k_i8<fr::I8Out<__nv_bfloat16>>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+            cudaSuccess ||
+        cudaFuncSetAttribute(fr::k_i8<fr::I8Lse>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+        (void)cudaGetLastError();
+        delete h;
+        return FR_ERR_CUDA;
+    }
+    cudaError_t e = cudaMalloc(&h->partial, sizeof(float2) * (size_t)max_rows * h->n_tiles);
+    if (e == cudaSuccess) e = cudaMalloc(&h->err, sizeof(int32_t));
+    if (e == cudaSuccess) e = cudaMemset(h->err, 0, sizeof(int32_t));
+    if (e != cudaSuccess) {
+        (void)cudaGetLastError();
+        cudaFree(h->partial);
+        cudaFree(h->err);
+        delete h;
+        return e == cudaErrorMemoryAllocation ? FR_ERR_OOM : FR_ERR_CUDA;
+    }
+    *out = h;
+    return FR_OK;
+}
+
+extern "C" fr_status fr_i8_matmul(fr_i8* h, const int8_t* xq_dev, int64_t ldx, const float* xscale_dev, int32_t rows,
+                                  void* out_dev, int64_t ldo, fr_dtype out_dtype, fr_stream stream) {
+    if (i8_bad_x(h, xq_dev, ldx, xscale_dev, rows) || !out_dev || ldo < h->N ||
+        (out_dtype != FR_F32 && out_dtype != FR_BF16))
+        return FR_ERR_INVALID_ARG;
+    const int esize = out_dtype == FR_F32 ? 4 : 2;
+    if (reinterpret_cast<uintptr_t>(out_dev) & (esize - 1)) return FR_ERR_INVALID_ARG;
+    if (!i8_on_device(h)) return FR_ERR_INVALID_ARG;
+    const cudaStream_t s = (cudaStream_t)stream;
+    h->last_stream = s;
+    if (rows == 0) return FR_OK;
+    const int32_t vec = (reinterpret_cast<uintptr_t>(out_dev) & 15u) == 0 && (ldo * esize) % 16 == 0;
+    if (out_dtype == FR_F32) {
+        fr::I8Out<float> p{};
+        const fr_status st = i8_base(h, xq_dev, ldx, xscale_dev, rows, &p);
+        if (st != FR_OK) return st;
+        p.out = (float*)out_dev;
+        p.ldo = ldo;
+        p.out_vec = vec;
+        return i8_launch(h, p, s);
+    }
+    fr::I8Out<__nv_bfloat16> p{};
+    const fr_status st = i8_base(h, xq_dev, ldx, xscale_dev, rows, &p);
+    if (st != FR_OK) return st;
+    p.out = (__nv_bfloat16*)out_dev;
+    p.ldo = ldo;
+    p.out_vec = vec;
+    return i8_launch(h, p, s);
+}
+
+extern "C" fr_status fr_i8_lse(fr_i8* h, const int8_t* xq_dev, int64_t ldx, const float* xscale_dev, int32_t rows,
+                               float* lse_dev, float* slice_dev, fr_stream stream) {
+    if (i8_bad_x(h, xq_dev, ldx, xscale_dev, rows) || !lse_dev || (h->sid_span > 0 && !slice_dev) ||
+        (reinterpret_cast<uintptr_t>(lse_dev) & 3u) || (reinterpret_cast<uintptr_t>(slice_dev) & 3u))
+        return FR_ERR_INVALID_ARG;
+    if (!i8_on_device(h)) return FR_ERR_INVALID_ARG;
+    const cudaStream_t s = (cudaStream_t)stream;
+    h->last_stream = s;
+    if (rows == 0) return FR_OK;
+    fr::I8Lse p{};
+    fr_status st = i8_base(h, xq_dev, ldx, xscale_dev, rows, &p);
+    if (st != FR_OK) return st;
+    p.partial = h->partial;
+    p.slice = slice_dev;
+    p.sid_base = h->sid_base;
+    p.sid_span = h->sid_span;
+    st = i8_launch(h, p, s);
+    if (st != FR_OK) return st;
+    FR_CUDA_TRY(fr::launch_pdl(fr::k_i8_combine, ((int64_t)rows + 7) / 8, 256, 0, s, (const float2*)h->partial, rows,
+                               h->n_tiles, lse_dev, h->err));
+    return FR_OK;
+}
+
+extern "C" fr_status fr_i8_status(fr_i8* h) {
+    if (!h) return FR_ERR_INVALID_ARG;
+    FR_CUDA_TRY(cudaStreamSynchronize(h->last_stream));
+    int32_t err = 0;
+    FR_CUDA_TRY(cudaMemcpy(&err, h->err, sizeof(int32_t), cudaMemcpyDeviceToHost));
+    return (fr_status)err;
+}
+
+extern "C" fr_status fr_i8_clear_status(fr_i8* h, fr_stream stream) {
+    if (!h) return FR_ERR_INVALID_ARG;
+    const cudaStream_t s = (cudaStream_t)stream;
+    FR_CUDA_TRY(cudaMemsetAsync(h->err, 0, sizeof(int32_t), s));
+    h->last_stream = s;
+    return FR_OK;
+}
+
+extern "C" fr_status fr_i8_set_wait_test(fr_i8* h, uint64_t wait_limit_ns, int32_t starve_copies) {
+    if (!h || (wait_limit_ns != 0 && (wait_limit_ns < 1000ull || wait_limit_ns > 60000000000ull)) ||
+        (starve_copies != 0 && starve_copies != 1))
+        return FR_ERR_INVALID_ARG;
+    h->wait_ns = wait_limit_ns ? wait_limit_ns : FR_WAIT_LIMIT_NS;
+    h->starve = starve_copies;
+    return FR_OK;
+}
+
+extern "C" void fr_i8_destroy(fr_i8* h) {
+    if (!h) return;
+    cudaFree(h->partial);
+    cudaFree(h->err);
+    delete h;
+}

@@ -36,6 +36,7 @@
 #include "fr.h"
 #include "fr_handles.h"
 #include "fr_internal.cuh"
+#include "fr_tc.cuh"
 
 namespace fr {
 namespace {
@@ -59,88 +60,6 @@ static_assert(LM_BK * 2 == 128, "one K stage is one 128-byte swizzle span");
 constexpr uint32_t LM_IDESC = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(LM_BN >> 3) << 17) |
                               ((uint32_t)(LM_BM >> 4) << 24);
 
-// Shared-memory matrix descriptor of a K-major operand tile stored with the
-// 128-byte swizzle (rows of 128 bytes, 8-row groups of 1024 bytes): start
-// address >> 4 (bits 0-13), leading-dimension offset 1 (16 bytes; unused by
-// the swizzled K-major layout), stride-dimension offset 1024 >> 4 (bits
-// 32-45), descriptor version 1 (bits 46-47), swizzle mode 2 = 128-byte
-// (bits 61-63).  The tile base must be 1024-byte aligned; the k-th 16-element
-// slice of the 64-element stage starts 32 * k bytes further.
-__device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr) {
-    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
-           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
-
-__device__ __forceinline__ uint32_t smem_u32(const void* p) {
-    return (uint32_t)__cvta_generic_to_shared(p);
-}
-
-__device__ __forceinline__ void lm_mbar_init(uint64_t* bar, uint32_t count) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");
-}
-
-__device__ __forceinline__ bool lm_mbar_try_wait(uint64_t* bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
-__device__ __forceinline__ uint64_t lm_now_ns() {
-    uint64_t t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
-}
-
-// Bounded wait; false after the time limit or once another thread aborted.
-__device__ __forceinline__ bool lm_wait(uint64_t* bar, uint32_t parity, volatile int32_t* abort_flag,
-                                        int32_t* err, uint64_t limit_ns) {
-    if (lm_mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = lm_now_ns();
-    for (uint32_t it = 0;; ++it) {
-        if (lm_mbar_try_wait(bar, parity)) return true;
-        if (*abort_flag) return false;
-        if ((it & 63u) == 63u && lm_now_ns() - t0 > limit_ns) {
-            *abort_flag = 1;
-            set_error(err, FR_ERR_DEVICE);
-            return false;
-        }
-    }
-}
-
-// Bounded wait that ignores the abort flag (draining work already issued).
-__device__ __forceinline__ void lm_wait_drain(uint64_t* bar, uint32_t parity) {
-    const uint64_t t0 = lm_now_ns();
-    for (uint32_t it = 0;; ++it) {
-        if (lm_mbar_try_wait(bar, parity)) return;
-        if ((it & 63u) == 63u && lm_now_ns() - t0 > FR_WAIT_LIMIT_NS) return;
-    }
-}
-
-__device__ __forceinline__ void lm_arrive_expect_tx(uint64_t* bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes)
-                 : "memory");
-}
-
-__device__ __forceinline__ void lm_arrive(uint64_t* bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-
-// 2-D tiled TMA load (no multicast): box at (x = inner coordinate, y).
-__device__ __forceinline__ void lm_tma_load_2d(const CUtensorMap* map, void* dst, uint64_t* bar, int32_t x,
-                                               int32_t y) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-            smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar))
-        : "memory");
-}
-
 __device__ __forceinline__ void lm_umma(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t accumulate) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
@@ -148,39 +67,6 @@ __device__ __forceinline__ void lm_umma(uint32_t tmem_d, uint64_t adesc, uint64_
         "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
         "l"(adesc), "l"(bdesc), "r"(LM_IDESC), "r"(accumulate)
         : "memory");
-}
-
-// Arrives on the mbarrier once every tcgen05.mma issued so far by this thread
-// has completed.
-__device__ __forceinline__ void lm_umma_commit(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-                 : "memory");
-}
-
-__device__ __forceinline__ void lm_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void lm_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-// 32 consecutive fp32 columns of this thread's TMEM lane.
-__device__ __forceinline__ void lm_tmem_ld32(uint32_t taddr, float (&v)[32]) {
-    uint32_t r[32];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
-
-__device__ __forceinline__ float lm_ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
 }
 
 struct LmArgs {
@@ -220,14 +106,14 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < LM_STAGES; ++s) {
-            lm_mbar_init(&sm->full[s], 1);
-            lm_mbar_init(&sm->empty[s], 1);
+            tc_mbar_init(&sm->full[s], 1);
+            tc_mbar_init(&sm->empty[s], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            lm_mbar_init(&sm->tmem_full[i], 1);
-            lm_mbar_init(&sm->tmem_empty[i], 4 * 32);
+            tc_mbar_init(&sm->tmem_full[i], 1);
+            tc_mbar_init(&sm->tmem_empty[i], 4 * 32);
         }
-        lm_mbar_init(&sm->mma_done, 1);
+        tc_mbar_init(&sm->mma_done, 1);
         sm->abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -237,9 +123,9 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    lm_fence_before();
+    tc_fence_before();
     __syncthreads();
-    lm_fence_after();
+    tc_fence_after();
     const uint32_t tmem = sm->tmem_base;
 
     if (warp == 0) {
@@ -252,20 +138,20 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
                 for (int kb = 0; kb < k_blocks; ++kb, ++it) {
                     const int s = (int)(it % LM_STAGES);
                     if (it >= (uint32_t)LM_STAGES &&
-                        !lm_wait(&sm->empty[s], ((it / LM_STAGES) & 1u) ^ 1u, abort_flag, a.err, a.wait_ns)) {
+                        !tc_wait(&sm->empty[s], ((it / LM_STAGES) & 1u) ^ 1u, abort_flag, a.err, a.wait_ns)) {
                         ok = false;
                         break;
                     }
-                    lm_arrive_expect_tx(&sm->full[s], (uint32_t)(LM_A_BYTES + LM_B_BYTES));
-                    lm_tma_load_2d(&map_h, tileA + s * LM_A_BYTES, &sm->full[s], kb * LM_BK, m0);
-                    lm_tma_load_2d(&map_w, tileB + s * LM_B_BYTES, &sm->full[s], kb * LM_BK, n0);
+                    tc_arrive_expect_tx(&sm->full[s], (uint32_t)(LM_A_BYTES + LM_B_BYTES));
+                    tc_tma_load_2d(&map_h, tileA + s * LM_A_BYTES, &sm->full[s], kb * LM_BK, m0);
+                    tc_tma_load_2d(&map_w, tileB + s * LM_B_BYTES, &sm->full[s], kb * LM_BK, n0);
                 }
             }
             // the last min(it, STAGES) copies were issued into stages nobody
             // may wait on any more after an abort: let them land
             if (!ok) {
                 for (uint32_t j = (it > (uint32_t)LM_STAGES ? it - LM_STAGES : 0u); j < it; ++j)
-                    lm_wait_drain(&sm->full[j % LM_STAGES], (j / LM_STAGES) & 1u);
+                    tc_wait_drain(&sm->full[j % LM_STAGES], (j / LM_STAGES) & 1u);
             }
         }
     } else if (warp == 1) {
@@ -276,31 +162,31 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
             bool ok = true;
             for (int tile = blockIdx.x; tile < total_tiles && ok; tile += gridDim.x, ++local) {
                 const int acc = local & 1;
-                if (local >= 2 && !lm_wait(&sm->tmem_empty[acc], ((local >> 1) & 1) ^ 1, abort_flag, a.err, a.wait_ns)) {
+                if (local >= 2 && !tc_wait(&sm->tmem_empty[acc], ((local >> 1) & 1) ^ 1, abort_flag, a.err, a.wait_ns)) {
                     ok = false;
                     break;
                 }
-                lm_fence_after();
+                tc_fence_after();
                 const uint32_t d_tmem = tmem + (uint32_t)(acc * LM_BN);
                 for (int kb = 0; kb < k_blocks; ++kb, ++it) {
                     const int s = (int)(it % LM_STAGES);
-                    if (!lm_wait(&sm->full[s], (it / LM_STAGES) & 1u, abort_flag, a.err, a.wait_ns)) {
+                    if (!tc_wait(&sm->full[s], (it / LM_STAGES) & 1u, abort_flag, a.err, a.wait_ns)) {
                         ok = false;
                         break;
                     }
-                    lm_fence_after();
+                    tc_fence_after();
                     const uint32_t sa = smem_u32(tileA + s * LM_A_BYTES), sb = smem_u32(tileB + s * LM_B_BYTES);
 #pragma unroll
                     for (int kk = 0; kk < LM_BK / LM_UMMA_K; ++kk)
                         lm_umma(d_tmem, smem_desc_sw128(sa + kk * LM_UMMA_K * 2), smem_desc_sw128(sb + kk * LM_UMMA_K * 2),
                                 (kb | kk) != 0 ? 1u : 0u);
-                    lm_umma_commit(&sm->empty[s]);  // the stage is free once these MMAs are done
+                    tc_umma_commit(&sm->empty[s]);  // the stage is free once these MMAs are done
                 }
-                lm_umma_commit(&sm->tmem_full[acc]);  // the accumulator is complete (or, on abort, quiet)
+                tc_umma_commit(&sm->tmem_full[acc]);  // the accumulator is complete (or, on abort, quiet)
             }
             // the tensor memory is freed only after every MMA issued here is done
-            lm_umma_commit(&sm->mma_done);
-            lm_wait_drain(&sm->mma_done, 0);
+            tc_umma_commit(&sm->mma_done);
+            tc_wait_drain(&sm->mma_done, 0);
         }
     } else if (warp >= 4) {
         // epilogue: warp w reads TMEM lanes 32 * (w % 4) .. + 31, one row per thread
@@ -309,8 +195,8 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
         int local = 0;
         for (int tile = blockIdx.x; tile < total_tiles; tile += gridDim.x, ++local) {
             const int acc = local & 1;
-            if (!lm_wait(&sm->tmem_full[acc], (local >> 1) & 1, abort_flag, a.err, a.wait_ns)) break;
-            lm_fence_after();
+            if (!tc_wait(&sm->tmem_full[acc], (local >> 1) & 1, abort_flag, a.err, a.wait_ns)) break;
+            tc_fence_after();
             const int mt = tile % a.m_tiles, nt = tile / a.m_tiles;
             const int row = mt * LM_BM + r_in, n0 = nt * LM_BN;
             const uint32_t t_row = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * LM_BN);
@@ -318,7 +204,7 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
 #pragma unroll 1
             for (int c = 0; c < LM_BN; c += 32) {
                 float v[32];
-                lm_tmem_ld32(t_row + (uint32_t)c, v);
+                tc_tmem_ld32(t_row + (uint32_t)c, v);
                 float cm = -INFINITY;
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
@@ -326,13 +212,13 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
                     cm = fmaxf(cm, v[i]);
                 }
                 if (cm > m) {
-                    s = (m == -INFINITY) ? 0.f : s * lm_ex2((m - cm) * LM_L2E);
+                    s = (m == -INFINITY) ? 0.f : s * tc_ex2((m - cm) * LM_L2E);
                     m = cm;
                 }
                 if (m != -INFINITY) {
                     const float nm = -m * LM_L2E;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) s += lm_ex2(fmaf(v[i], LM_L2E, nm));
+                    for (int i = 0; i < 32; ++i) s += tc_ex2(fmaf(v[i], LM_L2E, nm));
                 }
                 // SID-range columns of this chunk
                 const int lo = max(n0 + c, a.sid_base), hi = min(n0 + c + 32, a.sid_base + a.sid_span);
@@ -346,17 +232,17 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
                 }
             }
             if (row < a.rows) a.partial[(int64_t)row * a.n_tiles + nt] = make_float2(m, s);
-            lm_fence_before();
-            lm_arrive(&sm->tmem_empty[acc]);
+            tc_fence_before();
+            tc_arrive(&sm->tmem_empty[acc]);
         }
     }
 
     // the MMA thread has seen all its MMAs complete (mma_done) and the epilogue
     // has finished its tensor-memory loads: free the columns
-    lm_fence_before();
+    tc_fence_before();
     __syncthreads();
     if (warp == 2) {
-        lm_fence_after();
+        tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"((uint32_t)LM_TMEM_COLS)
                      : "memory");
     }
@@ -375,7 +261,7 @@ __global__ void __launch_bounds__(256) k_lmhead_combine(const float2* __restrict
         const float2 q = p[i];
         const float M = fmaxf(m, q.x);
         if (M != -INFINITY) {
-            s = (m == M ? s : s * lm_ex2((m - M) * LM_L2E)) + (q.x == M ? q.y : q.y * lm_ex2((q.x - M) * LM_L2E));
+            s = (m == M ? s : s * tc_ex2((m - M) * LM_L2E)) + (q.x == M ? q.y : q.y * tc_ex2((q.x - M) * LM_L2E));
             m = M;
         }
     }
@@ -384,7 +270,7 @@ __global__ void __launch_bounds__(256) k_lmhead_combine(const float2* __restrict
         const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
         const float M = fmaxf(m, m2);
         if (M != -INFINITY) {
-            s = (m == M ? s : s * lm_ex2((m - M) * LM_L2E)) + (m2 == M ? s2 : s2 * lm_ex2((m2 - M) * LM_L2E));
+            s = (m == M ? s : s * tc_ex2((m - M) * LM_L2E)) + (m2 == M ? s2 : s2 * tc_ex2((m2 - M) * LM_L2E));
             m = M;
         }
     }
@@ -393,22 +279,6 @@ __global__ void __launch_bounds__(256) k_lmhead_combine(const float2* __restrict
         if (!isfinite(v)) set_error(err, FR_ERR_NAN_LOGIT);
         lse[r] = v;
     }
-}
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-    static EncodeTiledFn fn = nullptr;
-    if (!fn) {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-    }
-    return fn;
 }
 
 // Row-major bf16 [rows, cols] with row stride ld elements, box rows x 64,

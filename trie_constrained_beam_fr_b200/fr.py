@@ -74,6 +74,27 @@ FR_FUNCS = [
     ("fr_lmhead_clear_status", _I32, [_VP, _VP]),
     ("fr_lmhead_set_wait_test", _I32, [_VP, _U64, _I32]),
     ("fr_lmhead_destroy", None, [_VP]),
+    ("fr_embed_init", _I32, [_I32, _I32, _I32, _P(_VP)]),
+    ("fr_embed_lookup", _I32, [_VP, _VP, _I64, _I32, _VP, _I32, ctypes.c_float, _VP, _I64, _I32, _VP]),
+    ("fr_embed_grad", _I32, [_VP, _VP, _I64, _I32, _VP, _I32, ctypes.c_float, _VP, _I64, _I32, _I32, _VP]),
+    ("fr_embed_status", _I32, [_VP]),
+    ("fr_embed_clear_status", _I32, [_VP, _VP]),
+    ("fr_embed_destroy", None, [_VP]),
+    ("fr_ce_init", _I32, [_I32, _I32, _I32, _P(_VP)]),
+    ("fr_ce_loss", _I32, [_VP, _VP, _I64, _VP, _I64, _VP, _I32, _VP, _VP, _VP]),
+    ("fr_ce_grad", _I32, [_VP, _VP, _I64, _VP, _I64, _VP, _VP, _VP, _I32, _VP, _I64, _VP, _I64, _VP]),
+    ("fr_ce_status", _I32, [_VP]),
+    ("fr_ce_clear_status", _I32, [_VP, _VP]),
+    ("fr_ce_set_wait_test", _I32, [_VP, _U64, _I32]),
+    ("fr_ce_destroy", None, [_VP]),
+    ("fr_i8_quantize", _I32, [_VP, _I64, _I32, _I32, _I32, _VP, _I64, _VP, _VP]),
+    ("fr_i8_init", _I32, [_VP, _I64, _VP, _I32, _I32, _I32, _I32, _I32, _P(_VP)]),
+    ("fr_i8_matmul", _I32, [_VP, _VP, _I64, _VP, _I32, _VP, _I64, _I32, _VP]),
+    ("fr_i8_lse", _I32, [_VP, _VP, _I64, _VP, _I32, _VP, _VP, _VP]),
+    ("fr_i8_status", _I32, [_VP]),
+    ("fr_i8_clear_status", _I32, [_VP, _VP]),
+    ("fr_i8_set_wait_test", _I32, [_VP, _U64, _I32]),
+    ("fr_i8_destroy", None, [_VP]),
 ]
 FR_GEN_FUNCS = [
     ("fr_gen_hash_logits", _I32, [_U64, _I64, _I32, _I32, _I32, _I64, _I32, _VP, _I32, _I32, _VP, _VP, _VP]),
@@ -426,3 +447,244 @@ def fr_lmhead_set_wait_test(lmhead, wait_limit_ns: int = 0, starve_copies: bool 
 
 def fr_lmhead_destroy(lmhead) -> None:
     libfr().fr_lmhead_destroy(lmhead)
+
+
+# ---------------------------------------------------------------------------
+# The vocabulary operators: token embedding, cross entropy, 8-bit product.
+# The C side sees neither bounds nor devices, so shapes, strides and devices
+# are checked here.
+
+
+def _on_current_device(*tensors: Optional[torch.Tensor]) -> None:
+    here = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("expected a CUDA tensor")
+        if here is None:
+            here = torch.cuda.current_device()
+        if t.device.index != here:
+            raise ValueError("every tensor must be on the current CUDA device (%d)" % here)
+
+
+def _matrix(t: torch.Tensor, what: str, dtypes, rows: Optional[int], cols: int) -> int:
+    """Checks a [rows, cols] tensor with unit column stride; returns its row
+    pitch in elements."""
+    if t.dtype not in dtypes or t.dim() != 2 or t.shape[1] != cols or (rows is not None and t.shape[0] != rows):
+        raise ValueError("%s must be a [%s, %d] tensor of %s"
+                         % (what, "rows" if rows is None else rows, cols, " or ".join(map(str, dtypes))))
+    # the strides of an axis of one or no element say nothing
+    if cols > 1 and t.shape[0] > 0 and t.stride(1) != 1:
+        raise ValueError("%s must have unit column stride" % what)
+    if t.shape[0] <= 1:
+        return max(cols, t.stride(0))
+    if t.stride(0) < cols:
+        raise ValueError("%s has overlapping rows" % what)
+    return t.stride(0)
+
+
+def _vector(t: torch.Tensor, what: str, dtype, n: int) -> None:
+    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s [%d] tensor" % (what, dtype, n))
+
+
+def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
+    """The data pointer; an empty tensor's, which is null, becomes a pointer
+    that no kernel follows."""
+    if t is None:
+        return None
+    return t.data_ptr() or 256
+
+
+_FLOATS = (torch.float32, torch.bfloat16)
+
+
+def fr_embed_init(V: int, d: int, max_tokens: int) -> ctypes.c_void_p:
+    out = _VP()
+    _check(libfr().fr_embed_init(int(V), int(d), int(max_tokens), ctypes.byref(out)), "fr_embed_init")
+    out.V, out.d = int(V), int(d)
+    return out
+
+
+def fr_embed_lookup(embed, table: torch.Tensor, tokens: torch.Tensor, out: torch.Tensor, scale: float = 1.0,
+                    stream=None) -> None:
+    """out[i] = scale * table[tokens[i]] (zeros for token -1).  table [V, d]
+    and out [n, d] float32 or bf16, tokens int32 [n]."""
+    n = tokens.shape[0] if tokens.dim() == 1 else -1
+    _on_current_device(table, tokens, out)
+    _vector(tokens, "tokens", torch.int32, n)
+    ldt = _matrix(table, "table", _FLOATS, embed.V, embed.d)
+    ldo = _matrix(out, "out", _FLOATS, n, embed.d)
+    _check(libfr().fr_embed_lookup(embed, _ptr(table), ldt, _dtype_code(table.dtype), _ptr(tokens), n, float(scale),
+                                   _ptr(out), ldo, _dtype_code(out.dtype), _stream(stream)), "fr_embed_lookup")
+
+
+def fr_embed_grad(embed, grad_out: torch.Tensor, tokens: torch.Tensor, grad_table: torch.Tensor, scale: float = 1.0,
+                  accumulate: bool = False, stream=None) -> None:
+    """grad_table[v] (+)= scale * sum of grad_out's rows whose token is v."""
+    n = tokens.shape[0] if tokens.dim() == 1 else -1
+    _on_current_device(grad_out, tokens, grad_table)
+    _vector(tokens, "tokens", torch.int32, n)
+    ldg = _matrix(grad_out, "grad_out", _FLOATS, n, embed.d)
+    ldt = _matrix(grad_table, "grad_table", _FLOATS, embed.V, embed.d)
+    _check(libfr().fr_embed_grad(embed, _ptr(grad_out), ldg, _dtype_code(grad_out.dtype), _ptr(tokens), n, float(scale),
+                                 _ptr(grad_table), ldt, _dtype_code(grad_table.dtype), int(bool(accumulate)),
+                                 _stream(stream)), "fr_embed_grad")
+
+
+def fr_embed_status(embed) -> int:
+    return int(libfr().fr_embed_status(embed))
+
+
+def fr_embed_clear_status(embed, stream=None) -> None:
+    _check(libfr().fr_embed_clear_status(embed, _stream(stream)), "fr_embed_clear_status")
+
+
+def fr_embed_destroy(embed) -> None:
+    libfr().fr_embed_destroy(embed)
+
+
+def fr_ce_init(V: int, d: int, max_rows: int) -> ctypes.c_void_p:
+    out = _VP()
+    _check(libfr().fr_ce_init(int(V), int(d), int(max_rows), ctypes.byref(out)), "fr_ce_init")
+    out.V, out.d = int(V), int(d)
+    return out
+
+
+def _ce_inputs(ce, hidden, weight, targets):
+    rows = targets.shape[0] if targets.dim() == 1 else -1
+    _vector(targets, "targets", torch.int32, rows)
+    ldh = _matrix(hidden, "hidden", (torch.bfloat16,), rows, ce.d)
+    ldw = _matrix(weight, "weight", (torch.bfloat16,), ce.V, ce.d)
+    # one row's pitch is never used as a stride: any multiple of 8 will do
+    return rows, ldh if rows > 1 else -(-ldh // 8) * 8, ldw if ce.V > 1 else -(-ldw // 8) * 8
+
+
+def fr_ce_loss(ce, hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, loss: torch.Tensor,
+               lse: torch.Tensor, stream=None) -> None:
+    """Each row's cross entropy of hidden @ weight.T against its target (0 for
+    target -1) and its log-sum-exp.  hidden bf16 [rows, d], weight bf16 [V, d],
+    targets int32 [rows], loss and lse float32 [rows]."""
+    _on_current_device(hidden, weight, targets, loss, lse)
+    rows, ldh, ldw = _ce_inputs(ce, hidden, weight, targets)
+    _vector(loss, "loss", torch.float32, rows)
+    _vector(lse, "lse", torch.float32, rows)
+    _check(libfr().fr_ce_loss(ce, _ptr(hidden), ldh, _ptr(weight), ldw, _ptr(targets), rows, _ptr(loss), _ptr(lse),
+                              _stream(stream)), "fr_ce_loss")
+
+
+def fr_ce_grad(ce, hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor,
+               grad_loss: torch.Tensor, grad_hidden: Optional[torch.Tensor], grad_weight: Optional[torch.Tensor],
+               stream=None) -> None:
+    """The loss's gradients from fr_ce_loss's lse and the rows' incoming
+    gradients (float32 [rows]): grad_hidden bf16 [rows, d], grad_weight bf16
+    [V, d]; either may be None."""
+    _on_current_device(hidden, weight, targets, lse, grad_loss, grad_hidden, grad_weight)
+    rows, ldh, ldw = _ce_inputs(ce, hidden, weight, targets)
+    _vector(lse, "lse", torch.float32, rows)
+    _vector(grad_loss, "grad_loss", torch.float32, rows)
+    ldgh = 0 if grad_hidden is None else _matrix(grad_hidden, "grad_hidden", (torch.bfloat16,), rows, ce.d)
+    ldgw = 0 if grad_weight is None else _matrix(grad_weight, "grad_weight", (torch.bfloat16,), ce.V, ce.d)
+    _check(libfr().fr_ce_grad(ce, _ptr(hidden), ldh, _ptr(weight), ldw, _ptr(targets), _ptr(lse), _ptr(grad_loss), rows,
+                              _ptr(grad_hidden), ldgh, _ptr(grad_weight), ldgw, _stream(stream)), "fr_ce_grad")
+
+
+def fr_ce_status(ce) -> int:
+    return int(libfr().fr_ce_status(ce))
+
+
+def fr_ce_clear_status(ce, stream=None) -> None:
+    _check(libfr().fr_ce_clear_status(ce, _stream(stream)), "fr_ce_clear_status")
+
+
+def fr_ce_set_wait_test(ce, wait_limit_ns: int = 0, starve_copies: bool = False) -> None:
+    """Test hook: as fr_beam_set_wait_test, for the cross-entropy kernels."""
+    _check(libfr().fr_ce_set_wait_test(ce, int(wait_limit_ns), int(bool(starve_copies))), "fr_ce_set_wait_test")
+
+
+def fr_ce_destroy(ce) -> None:
+    libfr().fr_ce_destroy(ce)
+
+
+def fr_i8_quantize(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, stream=None) -> None:
+    """Rows of x (float32 or bf16 [rows, d]) to int8 q [rows, d] with a scale
+    for each row (float32 [rows])."""
+    _on_current_device(x, q, scale)
+    if x.dim() != 2:
+        raise ValueError("x must be a [rows, d] tensor")
+    rows, d = x.shape
+    ldx = _matrix(x, "x", _FLOATS, rows, d)
+    ldq = _matrix(q, "q", (torch.int8,), rows, d)
+    _vector(scale, "scale", torch.float32, rows)
+    _check(libfr().fr_i8_quantize(_ptr(x), ldx, _dtype_code(x.dtype), rows, d, _ptr(q), ldq, _ptr(scale),
+                                  _stream(stream)), "fr_i8_quantize")
+
+
+def fr_i8_init(weight: torch.Tensor, weight_scale: torch.Tensor, max_rows: int, sid_base: int = 0,
+               sid_span: int = 0) -> ctypes.c_void_p:
+    """weight: int8 [N, d] CUDA tensor whose row pitch is a multiple of 16,
+    weight_scale: float32 [N]; the handle keeps them alive, and they must not change."""
+    _on_current_device(weight, weight_scale)
+    if weight.dim() != 2:
+        raise ValueError("weight must be an int8 [N, d] tensor")
+    N, d = weight.shape
+    ldw = _matrix(weight, "weight", (torch.int8,), N, d)
+    if N == 1:
+        ldw = -(-ldw // 16) * 16
+    _vector(weight_scale, "weight_scale", torch.float32, N)
+    out = _VP()
+    _check(libfr().fr_i8_init(_ptr(weight), ldw, _ptr(weight_scale), N, d, int(max_rows), int(sid_base), int(sid_span),
+                              ctypes.byref(out)), "fr_i8_init")
+    out.N, out.d, out.sid_span = N, d, int(sid_span)
+    out.kept = (weight, weight_scale)  # the library keeps their addresses
+    return out
+
+
+def _i8_inputs(i8, xq, xscale):
+    rows = xscale.shape[0] if xscale.dim() == 1 else -1
+    _vector(xscale, "xscale", torch.float32, rows)
+    ldx = _matrix(xq, "xq", (torch.int8,), rows, i8.d)
+    return rows, ldx if rows > 1 else -(-ldx // 16) * 16
+
+
+def fr_i8_matmul(i8, xq: torch.Tensor, xscale: torch.Tensor, out: torch.Tensor, stream=None) -> None:
+    """out[r, n] = (xq[r] . weight[n]) * xscale[r] * weight_scale[n]; xq int8
+    [rows, d] (row pitch a multiple of 16), out float32 or bf16 [rows, N]."""
+    _on_current_device(xq, xscale, out)
+    rows, ldx = _i8_inputs(i8, xq, xscale)
+    ldo = _matrix(out, "out", _FLOATS, rows, i8.N)
+    _check(libfr().fr_i8_matmul(i8, _ptr(xq), ldx, _ptr(xscale), rows, _ptr(out), ldo, _dtype_code(out.dtype),
+                                _stream(stream)), "fr_i8_matmul")
+
+
+def fr_i8_lse(i8, xq: torch.Tensor, xscale: torch.Tensor, lse: torch.Tensor, slice_: Optional[torch.Tensor],
+              stream=None) -> None:
+    """The same product as each row's log-sum-exp (float32 [rows]) and SID
+    slice (float32 [rows, sid_span], contiguous), for fr_beam_step_lse."""
+    _on_current_device(xq, xscale, lse, slice_)
+    rows, ldx = _i8_inputs(i8, xq, xscale)
+    _vector(lse, "lse", torch.float32, rows)
+    if slice_ is None:
+        if i8.sid_span:
+            raise ValueError("the handle has a SID range: slice is needed")
+    elif _matrix(slice_, "slice", (torch.float32,), rows, i8.sid_span) != i8.sid_span and rows > 1:
+        raise ValueError("slice must be contiguous")
+    _check(libfr().fr_i8_lse(i8, _ptr(xq), ldx, _ptr(xscale), rows, _ptr(lse), _ptr(slice_), _stream(stream)), "fr_i8_lse")
+
+
+def fr_i8_status(i8) -> int:
+    return int(libfr().fr_i8_status(i8))
+
+
+def fr_i8_clear_status(i8, stream=None) -> None:
+    _check(libfr().fr_i8_clear_status(i8, _stream(stream)), "fr_i8_clear_status")
+
+
+def fr_i8_set_wait_test(i8, wait_limit_ns: int = 0, starve_copies: bool = False) -> None:
+    """Test hook: as fr_beam_set_wait_test, for the 8-bit product kernels."""
+    _check(libfr().fr_i8_set_wait_test(i8, int(wait_limit_ns), int(bool(starve_copies))), "fr_i8_set_wait_test")
+
+
+def fr_i8_destroy(i8) -> None:
+    libfr().fr_i8_destroy(i8)
