@@ -11,8 +11,8 @@
 //
 //   k_ce_gather   packs the counted rows: hidden states, targets, (gradients:
 //                 lse and g) and their row numbers; zero rows up to the next
-//                 multiple of 128.
-//   k_ce_loss     tcgen05 tiles of x (128 rows x 256 tokens); the epilogue
+//                 multiple of 256.
+//   k_ce_loss     tcgen05 tiles of x (256 rows x 256 tokens); the epilogue
 //                 keeps a (max, scaled sum) partial per row and tile and the
 //                 target's logit.  k_ce_combine: lse and loss.
 //   k_ce_grad     works through the vocabulary in pieces: for a piece, tiles
@@ -26,7 +26,11 @@
 //   k_ce_finish   dh = sum of the fp32 partials, rounded, at the original rows.
 //
 // G is rounded to bf16, the operand type of the products: half a step (2^-8)
-// of each entry, the same as one rounding of the inputs.
+// of each entry, the same as one rounding of the inputs.  What is rounded is
+// G / max |g|; the maximum multiplies the fp32 sums.  So the entries at the
+// targets, which carry most of a gradient whose probabilities are spread, are
+// p - 1 without g's own rounding when all rows have the same g (a mean), and a
+// small or large g neither underflows nor overflows.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -44,9 +48,10 @@
 namespace fr {
 namespace {
 
-constexpr int CE_BN = 256;
-constexpr int CE_STAGES = 4;
-constexpr int CE_PIECE = 8192;  // tokens per piece of the gradient
+// Tokens per piece of the gradient: at least CE_PIECE_MIN, and as many as keep
+// a piece of G within CE_PIECE_BYTES.
+constexpr int CE_PIECE_MIN = 4096;
+constexpr int64_t CE_PIECE_BYTES = 256 << 20;
 constexpr float CE_L2E = 1.4426950408889634f;
 
 // The packed rows and what belongs to them.
@@ -58,7 +63,10 @@ struct CeRows {
     float* g;          // [cap]
     int32_t* idx;      // [cap] original row
     int32_t* n;        // [1] counted rows
+    float* gmax;       // [1] largest finite |g| of a counted row
 };
+
+__device__ __forceinline__ int32_t ce_m_tiles(int32_t n) { return max((n + GM_TILE - 1) / GM_TILE, 1); }
 
 // A CTA packs 64 consecutive rows: it counts the counted rows before its own
 // (reading the targets up to there), so no CTA waits for another.
@@ -70,10 +78,11 @@ __global__ void __launch_bounds__(CE_GATHER_THREADS)
                 CeRows out, float* __restrict__ loss_out, float* __restrict__ lse_out,
                 __nv_bfloat16* __restrict__ grad_hidden, int64_t ldgh, int32_t* __restrict__ err) {
     __shared__ int32_t before_s, pos_s[CE_GATHER_ROWS], total_s;
+    __shared__ uint32_t gmax_s;
     griddep_wait();
     griddep_launch_dependents();
     const int32_t r0 = blockIdx.x * CE_GATHER_ROWS, tid = threadIdx.x;
-    if (tid == 0) before_s = 0;
+    if (tid == 0) before_s = 0, gmax_s = 0u;
     __syncthreads();
     int32_t c = 0;
 #pragma unroll 4
@@ -131,18 +140,30 @@ __global__ void __launch_bounds__(CE_GATHER_THREADS)
         }
     }
     if (blockIdx.x == gridDim.x - 1) {
-        const int32_t n = total_s, end = max((n + GM_BM - 1) / GM_BM, 1) * GM_BM;
+        const int32_t n = total_s, end = ce_m_tiles(n) * GM_TILE;
         for (int32_t r = n + (tid >> 5); r < end; r += CE_GATHER_THREADS / 32)
             for (int32_t j = tid & 31; j < out.pitch; j += 32) out.h[r * out.pitch + j] = __float2bfloat16_rn(0.f);
         if (tid == 0) *out.n = n;
+        if (lse) {
+            float m = 0.f;
+#pragma unroll 4
+            for (int32_t i = tid; i < rows; i += CE_GATHER_THREADS) {
+                const int32_t t = targets[i];
+                const float g = fabsf(grad_loss[i]);
+                if (t >= 0 && t < V && g < INFINITY) m = fmaxf(m, g);
+            }
+            // non-negative floats order as their bits
+            const uint32_t w = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+            if ((tid & 31) == 0) atomicMax(&gmax_s, w);
+            __syncthreads();
+            if (tid == 0) *out.gmax = __uint_as_float(gmax_s);
+        }
     }
 }
 
-__device__ __forceinline__ int32_t ce_m_tiles(int32_t n) { return max((n + GM_BM - 1) / GM_BM, 1); }
-
 struct CeLoss {
-    static constexpr bool I8 = false;
-    static constexpr int BN = CE_BN, STAGES = CE_STAGES;
+    static constexpr bool I8 = false, STAGED = false;
+    static constexpr int STAGES = 7;
     struct Tile {
         int nk, m0, n0;
         uint32_t idesc;
@@ -153,34 +174,34 @@ struct CeLoss {
     CUtensorMap map_h, map_w;
     CeRows rows;
     int32_t V, k_blocks, n_tiles;
-    float2* partial;  // [cap, n_tiles]
+    float2* partial;  // [cap, 2 * n_tiles] (max, scaled sum) of 128 tokens each
     float* xt;        // [cap] the target's logit
 
     __device__ __forceinline__ State begin() const {
         const int32_t n = *rows.n;
         return {n, n ? ce_m_tiles(n) : 0};
     }
-    __device__ __forceinline__ bool tile(const State& st, int i, Tile& t) const {
-        const int64_t g = blockIdx.x + (int64_t)i * gridDim.x;
+    __device__ __forceinline__ bool tile(const State& st, int64_t pair, int64_t pairs, int i, Tile& t) const {
+        const int64_t g = pair + i * pairs;
         if (g >= (int64_t)st.m_tiles * n_tiles) return false;
-        t.m0 = (int)(g % st.m_tiles) * GM_BM;
-        t.n0 = (int)(g / st.m_tiles) * BN;
+        t.m0 = (int)(g % st.m_tiles) * GM_TILE;
+        t.n0 = (int)(g / st.m_tiles) * GM_TILE;
         t.nk = k_blocks;
-        t.idesc = gm_idesc(false, BN);
+        t.idesc = gm_idesc(false);
         return true;
     }
     __device__ __forceinline__ bool a_mn(const Tile&) const { return false; }
     __device__ __forceinline__ bool b_mn(const Tile&) const { return false; }
-    __device__ __forceinline__ void load(const Tile& t, int kb, uint8_t* a, uint8_t* b, uint64_t* bar) const {
-        tc_tma_load_2d(&map_h, a, bar, kb * 64, t.m0);
-        tc_tma_load_2d(&map_w, b, bar, kb * 64, t.n0);
+    __device__ __forceinline__ void load(const Tile& t, int kb, int rank, uint8_t* a, uint8_t* b, uint32_t bar) const {
+        gm_tma_load(&map_h, a, bar, kb * 64, t.m0 + rank * GM_HALF);
+        gm_tma_load(&map_w, b, bar, kb * 64, t.n0 + rank * GM_HALF);
     }
-    __device__ __forceinline__ void epilogue(const State& st, const Tile& t, uint32_t taddr, int r) const {
+    __device__ __forceinline__ void epilogue(const State& st, const Tile& t, uint32_t taddr, int r, int c0, const GmStage&) const {
         const int row = t.m0 + r;
         const int32_t tgt = row < st.n ? rows.tgt[row] : -1;
         float m = -INFINITY, s = 0.f;
 #pragma unroll 1
-        for (int c = 0; c < BN && t.n0 + c < V; c += 32) {
+        for (int c = c0; c < c0 + GM_EPI_COLS && t.n0 + c < V; c += 32) {
             const int n = t.n0 + c;
             float v[32];
             tc_tmem_ld32(taddr + (uint32_t)c, v);
@@ -198,7 +219,7 @@ struct CeLoss {
             }
             gm_lse_fold(v, m, s);
         }
-        if (row < st.n) partial[(int64_t)row * n_tiles + t.n0 / BN] = make_float2(m, s);
+        if (row < st.n) partial[(int64_t)row * 2 * n_tiles + (t.n0 + c0) / GM_EPI_COLS] = make_float2(m, s);
     }
 };
 
@@ -206,14 +227,14 @@ __global__ void __launch_bounds__(GM_THREADS, 1) k_ce_loss(const __grid_constant
     gm_run(p, ctl);
 }
 
-__global__ void __launch_bounds__(256) k_ce_combine(const float2* __restrict__ partial, int32_t n_tiles, CeRows rows,
+__global__ void __launch_bounds__(256) k_ce_combine(const float2* __restrict__ partial, int32_t n_parts, CeRows rows,
                                                     const float* __restrict__ xt, float* __restrict__ loss,
                                                     float* __restrict__ lse, int32_t* __restrict__ err) {
     griddep_wait();
     griddep_launch_dependents();
     const int64_t c = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     if (c >= *rows.n) return;
-    const float v = gm_lse_combine(partial + c * n_tiles, n_tiles);
+    const float v = gm_lse_combine(partial + c * n_parts, n_parts);
     if ((threadIdx.x & 31) == 0) {
         const int32_t r = rows.idx[c];
         if (!isfinite(v)) set_error(err, FR_ERR_NAN_LOGIT);
@@ -226,143 +247,162 @@ __global__ void __launch_bounds__(256) k_ce_combine(const float2* __restrict__ p
 // G in buffer `buf`) and the G tiles of the next (tokens [w0, w1), buffer
 // buf ^ 1).  Empty ranges leave their part out.
 struct CeGrad {
-    static constexpr bool I8 = false;
-    static constexpr int BN = CE_BN, STAGES = CE_STAGES;
+    static constexpr bool I8 = false, STAGED = true;
+    static constexpr int STAGES = 6;
     enum { DH, DW, GT };
     struct Tile {
         int nk, type, m0, n0, k0, split;
         uint32_t idesc;
     };
     struct State {
-        int32_t n, m_tiles, dh_tiles, dw_tiles, g_tiles;
+        int32_t n, m_tiles, dh_tiles, dw_tiles, g_tiles, extra, dw_nk;
+        float gmax, ginv;
     };
     CUtensorMap map_h_k, map_h_mn;   // packed rows: K-major (128 x 64) and MN-major (64 x 64) boxes
-    CUtensorMap map_w_k, map_w_mn;   // weight: K-major (256 x 64) and MN-major (64 x 64) boxes
+    CUtensorMap map_w_k, map_w_mn;   // weight: K-major (128 x 64) and MN-major (64 x 64) boxes
     CUtensorMap map_g_k, map_g_mn;   // G of the piece whose products run
+    CUtensorMap map_g_out;           // G of the piece whose tiles are computed: 32 x 64 boxes
+    CUtensorMap map_dw;              // the caller's dW, where its rows start on 16 bytes: 32 x 64 boxes
     CeRows rows;
-    __nv_bfloat16* g_next;           // G of the piece whose tiles are computed
-    int64_t g_pitch;
     int32_t V, d, d_tiles, splits, first;
     int32_t v0, v1, w0, w1;
-    float* dh;                       // [splits, cap, pitch] fp32 partials, null: no dh
-    int64_t dh_split;                // cap * pitch
+    CUtensorMap map_dh;              // [splits, dh_rows] rows of fp32 partials: 32 x 32 boxes
+    int32_t dh, dh_rows;             // whether dh is wanted; rows of one split
     __nv_bfloat16* dw;               // the caller's dW, null: no dW
     int64_t ldw;
-    int32_t dw_vec;
+    int32_t dw_staged;               // columns of dW that go out through shared memory and TMA
 
     __device__ __forceinline__ State begin() const {
         State st;
         st.n = *rows.n;
+        st.gmax = *rows.gmax;
+        st.ginv = st.gmax > 0.f ? 1.f / st.gmax : 0.f;
         st.m_tiles = ce_m_tiles(st.n);
         st.dh_tiles = dh && v1 > v0 && st.n ? st.m_tiles * d_tiles * splits : 0;
-        st.dw_tiles = dw && v1 > v0 ? (v1 - v0 + GM_BM - 1) / GM_BM * d_tiles : 0;
-        st.g_tiles = w1 > w0 ? (w1 - w0 + BN - 1) / BN * st.m_tiles : 0;
+        st.dw_tiles = dw && v1 > v0 ? (v1 - v0 + GM_TILE - 1) / GM_TILE * d_tiles : 0;
+        st.g_tiles = w1 > w0 ? (w1 - w0 + GM_TILE - 1) / GM_TILE * st.m_tiles : 0;
+        st.dw_nk = max((st.n + 63) / 64, 1);
+        st.extra = st.dw_nk / ((d + 63) / 64);
         return st;
     }
-    __device__ __forceinline__ bool tile(const State& st, int i, Tile& t) const {
-        int g = blockIdx.x + i * gridDim.x;
+    // The pairs take the long tiles (dh, dW) in turn, then the G tiles.  Where
+    // the long ones do not come out even, the pairs that have one less first
+    // take as many G tiles as make up for it (3% of a piece of 8,192 tokens x
+    // 7,782 rows on 74 pairs).
+    __device__ __forceinline__ bool tile(const State& st, int64_t pair, int64_t pairs, int i, Tile& t) const {
+        const int P = (int)pairs, p = (int)pair, longs = st.dh_tiles + st.dw_tiles;
+        const int mine = (longs - p + P - 1) / P;
+        int g = p + i * P;
+        if (i >= mine) {
+            const int even = longs % P;  // pairs [even, P) have one less (none if 0)
+            const int less = even ? P - even : 0;
+            const int extra = less ? min(st.extra, st.g_tiles / less) : 0;
+            const int own = p >= even ? extra : 0;
+            const int k = i - mine;
+            g = k < own ? (p - even) * extra + k : less * extra + (P - 1 - p) + (k - own) * P;
+            g += longs;
+        }
         if (g < st.dh_tiles) {
             const int kb = (v1 - v0 + 63) / 64, per = (kb + splits - 1) / splits;
             t.type = DH;
-            t.m0 = g % st.m_tiles * GM_BM;
+            t.m0 = g % st.m_tiles * GM_TILE;
             g /= st.m_tiles;
-            t.n0 = g % d_tiles * BN;
+            t.n0 = g % d_tiles * GM_TILE;
             t.split = g / d_tiles;
             t.k0 = t.split * per;
             t.nk = max(min(per, kb - t.k0), 0);
-            t.idesc = gm_idesc(false, BN, false, true);
+            t.idesc = gm_idesc(false, false, true);
             return true;
         }
         g -= st.dh_tiles;
         if (g < st.dw_tiles) {
             t.type = DW;
-            t.n0 = g % d_tiles * BN;
-            t.m0 = g / d_tiles * GM_BM;
+            t.n0 = g % d_tiles * GM_TILE;
+            t.m0 = g / d_tiles * GM_TILE;
             t.k0 = 0;
-            t.nk = max((st.n + 63) / 64, 1);
-            t.idesc = gm_idesc(false, BN, true, true);
+            t.nk = st.dw_nk;
+            t.idesc = gm_idesc(false, true, true);
             return true;
         }
         g -= st.dw_tiles;
         if (g < st.g_tiles) {
             t.type = GT;
-            t.m0 = g % st.m_tiles * GM_BM;
-            t.n0 = g / st.m_tiles * BN;
+            t.m0 = g % st.m_tiles * GM_TILE;
+            t.n0 = g / st.m_tiles * GM_TILE;
             t.k0 = 0;
             t.nk = (d + 63) / 64;
-            t.idesc = gm_idesc(false, BN);
+            t.idesc = gm_idesc(false);
             return true;
         }
         return false;
     }
     __device__ __forceinline__ bool a_mn(const Tile& t) const { return t.type == DW; }
     __device__ __forceinline__ bool b_mn(const Tile& t) const { return t.type != GT; }
-    __device__ __forceinline__ void load(const Tile& t, int kb, uint8_t* a, uint8_t* b, uint64_t* bar) const {
-        const int k = (t.k0 + kb) * 64;
+    __device__ __forceinline__ void load(const Tile& t, int kb, int rank, uint8_t* a, uint8_t* b, uint32_t bar) const {
+        const int k = (t.k0 + kb) * 64, m = t.m0 + rank * GM_HALF, n = t.n0 + rank * GM_HALF;
         if (t.type == GT) {
-            tc_tma_load_2d(&map_h_k, a, bar, k, t.m0);
-            tc_tma_load_2d(&map_w_k, b, bar, k, w0 + t.n0);
+            gm_tma_load(&map_h_k, a, bar, k, m);
+            gm_tma_load(&map_w_k, b, bar, k, w0 + n);
         } else if (t.type == DH) {
-            tc_tma_load_2d(&map_g_k, a, bar, k, t.m0);
-#pragma unroll
-            for (int j = 0; j < BN / 64; ++j) tc_tma_load_2d(&map_w_mn, b + j * 8192, bar, t.n0 + j * 64, v0 + k);
+            gm_tma_load(&map_g_k, a, bar, k, m);
+            gm_tma_load(&map_w_mn, b, bar, n, v0 + k);
+            gm_tma_load(&map_w_mn, b + 8192, bar, n + 64, v0 + k);
         } else {
-#pragma unroll
-            for (int j = 0; j < GM_BM / 64; ++j) tc_tma_load_2d(&map_g_mn, a + j * 8192, bar, t.m0 + j * 64, k);
-#pragma unroll
-            for (int j = 0; j < BN / 64; ++j) tc_tma_load_2d(&map_h_mn, b + j * 8192, bar, t.n0 + j * 64, k);
+            gm_tma_load(&map_g_mn, a, bar, m, k);
+            gm_tma_load(&map_g_mn, a + 8192, bar, m + 64, k);
+            gm_tma_load(&map_h_mn, b, bar, n, k);
+            gm_tma_load(&map_h_mn, b + 8192, bar, n + 64, k);
         }
     }
-    __device__ __forceinline__ void epilogue(const State& st, const Tile& t, uint32_t taddr, int r) const {
-        const int row = t.m0 + r;
+    __device__ __forceinline__ void epilogue(const State& st, const Tile& t, uint32_t taddr, int r, int c0, const GmStage& sg) const {
+        const int row = t.m0 + r, lane = threadIdx.x & 31, row0 = row - lane;
         if (t.type == GT) {
             const bool live = row < st.n;
-            const float g = live ? rows.g[row] : 0.f, nl = live ? -rows.lse[row] * CE_L2E : 0.f;
-            const int32_t tgt = live ? rows.tgt[row] - w0 : -1;  // column in the piece
-            __nv_bfloat16* dst = g_next + row * g_pitch + t.n0;
+            const float g = live ? rows.g[row] * st.ginv : 0.f, nl = live ? -rows.lse[row] * CE_L2E : 0.f;
+            const int32_t tgt = live ? rows.tgt[row] - w0 - t.n0 : -1;  // column in the tile
             const int width = w1 - w0 - t.n0;  // columns of this tile that are tokens
 #pragma unroll 1
-            for (int c = 0; c < BN; c += 32) {
-                float v[32];
-                tc_tmem_ld32(taddr + (uint32_t)c, v);
+            for (int c = c0; c < c0 + GM_EPI_COLS; c += 64) {
+                float v[64];
+                gm_ld32(taddr + (uint32_t)c, v);
+                gm_ld32(taddr + (uint32_t)c + 32, v + 32);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const float p = tc_ex2(fmaf(v[i], CE_L2E, nl)) - (t.n0 + c + i == tgt ? 1.f : 0.f);
+                for (int i = 0; i < 64; ++i) {
+                    const float p = tc_ex2(fmaf(v[i], CE_L2E, nl)) - (c + i == tgt ? 1.f : 0.f);
                     v[i] = live && c + i < width ? p * g : 0.f;  // zeros feed the products' ragged ends
                 }
-                gm_store32(dst + c, v, 32, true);
+                gm_stage64(sg, &map_g_out, lane, v, t.n0 + c, row0);
             }
         } else if (t.type == DH) {
             if (t.nk == 0 && !first) return;  // a split without tokens adds nothing
-            float* dst = dh + t.split * dh_split + row * rows.pitch + t.n0;
 #pragma unroll 1
-            for (int c = 0; c < BN && t.n0 + c < d; c += 32) {
+            for (int c = c0; c < c0 + GM_EPI_COLS && t.n0 + c < d; c += 32) {
                 float v[32];
                 tc_tmem_ld32(taddr + (uint32_t)c, v);
-                if (row >= st.n) continue;
+                if (t.nk == 0) {
 #pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                    if (t.n0 + c + i < d) {  // the pitch is a multiple of 8: whole groups of 4 stay in the row
-                        float4* o = reinterpret_cast<float4*>(dst + c + i);
-                        float4 x = t.nk ? make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (!first) {
-                            const float4 y = *o;
-                            x.x += y.x;
-                            x.y += y.y;
-                            x.z += y.z;
-                            x.w += y.w;
-                        }
-                        *o = x;
-                    }
+                    for (int i = 0; i < 32; ++i) v[i] = 0.f;
                 }
+                // one addition per launch and value: the order is that of the pieces
+                if (first)
+                    gm_stage32<false>(sg, &map_dh, lane, v, t.n0 + c, t.split * dh_rows + row0);
+                else
+                    gm_stage32<true>(sg, &map_dh, lane, v, t.n0 + c, t.split * dh_rows + row0);
             }
         } else {
             const int v = v0 + row;
 #pragma unroll 1
-            for (int c = 0; c < BN && t.n0 + c < d; c += 32) {
-                float x[32];
-                tc_tmem_ld32(taddr + (uint32_t)c, x);
-                if (v < v1) gm_store32(dw + v * ldw + t.n0 + c, x, min(32, d - t.n0 - c), dw_vec != 0);
+            for (int c = c0; c < c0 + GM_EPI_COLS && t.n0 + c < d; c += 64) {
+                float x[64];
+                gm_ld32(taddr + (uint32_t)c, x);
+                gm_ld32(taddr + (uint32_t)c + 32, x + 32);
+#pragma unroll
+                for (int i = 0; i < 64; ++i) x[i] *= st.gmax;
+                if (t.n0 + c < dw_staged) {
+                    if (v0 + row0 < v1) gm_stage64(sg, &map_dw, lane, x, t.n0 + c, v0 + row0);
+                } else if (v < v1) {
+                    gm_store(dw + v * ldw + t.n0 + c, x, min(64, d - t.n0 - c));
+                }
             }
         }
     }
@@ -380,10 +420,12 @@ __global__ void __launch_bounds__(256) k_ce_finish(const float* __restrict__ dh,
     griddep_launch_dependents();
     const int64_t c = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     if (c >= *rows.n) return;
+    const float gmax = *rows.gmax;
     const float* src = dh + c * rows.pitch;
     __nv_bfloat16* dst = grad_hidden + rows.idx[c] * ldgh;
     for (int32_t j = (threadIdx.x & 31) * 4; j < d; j += 128) {
         float4 x = *reinterpret_cast<const float4*>(src + j);
+#pragma unroll 4
         for (int k = 1; k < splits; ++k) {
             const float4 y = *reinterpret_cast<const float4*>(src + k * dh_split + j);
             x.x += y.x;
@@ -391,6 +433,10 @@ __global__ void __launch_bounds__(256) k_ce_finish(const float* __restrict__ dh,
             x.z += y.z;
             x.w += y.w;
         }
+        x.x *= gmax;
+        x.y *= gmax;
+        x.z *= gmax;
+        x.w *= gmax;
         if (vec && j + 4 <= d) {
             const __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), b = __floats2bfloat162_rn(x.z, x.w);
             *reinterpret_cast<uint2*>(dst + j) =
@@ -406,10 +452,10 @@ __global__ void __launch_bounds__(256) k_ce_finish(const float* __restrict__ dh,
 
 int64_t ce_round(int64_t x, int64_t q) { return (x + q - 1) / q * q; }
 
-// Splits of dh's token axis within a piece: enough tiles for every SM when
-// there are few rows.
-int32_t ce_splits(int32_t sms, int64_t m_tiles, int64_t d_tiles) {
-    return (int32_t)std::max<int64_t>(1, std::min<int64_t>(16, sms / (m_tiles * d_tiles)));
+// Splits of dh's token axis within a piece: enough tiles for every pair of
+// SMs when there are few rows.
+int32_t ce_splits(int32_t pairs, int64_t m_tiles, int64_t d_tiles) {
+    return (int32_t)std::max<int64_t>(1, std::min<int64_t>(16, pairs / (m_tiles * d_tiles)));
 }
 
 }  // namespace
@@ -419,12 +465,12 @@ struct fr_ce {
     int32_t V = 0, d = 0, max_rows = 0, n_tiles = 0, sms = 0, device = 0, piece = 0;
     int64_t cap = 0;
     fr::CeRows rows{};
-    float2* partial = nullptr;       // [cap, n_tiles]
+    float2* partial = nullptr;       // [cap, 2 * n_tiles]
     float* xt = nullptr;             // [cap]
     __nv_bfloat16* g[2] = {};        // [cap, piece] each
     float* dh = nullptr;             // fp32 partials of dh
     int32_t* err = nullptr;
-    CUtensorMap map_h_k, map_h_mn, map_g_k[2], map_g_mn[2];
+    CUtensorMap map_h_k, map_h_mn, map_g_k[2], map_g_mn[2], map_g_out[2];
     cudaStream_t last_stream = nullptr;
     uint64_t wait_ns = FR_WAIT_LIMIT_NS;
     int32_t starve = 0;
@@ -467,26 +513,24 @@ extern "C" fr_status fr_ce_init(int32_t V, int32_t d, int32_t max_rows, fr_ce** 
     h->V = V;
     h->d = d;
     h->max_rows = max_rows;
-    h->cap = fr::ce_round(max_rows, fr::GM_BM);
-    h->n_tiles = (V + fr::CE_BN - 1) / fr::CE_BN;
-    h->piece = (int32_t)std::min<int64_t>(fr::CE_PIECE, fr::ce_round(V, fr::CE_BN));
+    h->cap = fr::ce_round(max_rows, fr::GM_TILE);
+    h->n_tiles = (V + fr::GM_TILE - 1) / fr::GM_TILE;
+    h->piece = (int32_t)std::min(std::max<int64_t>(fr::CE_PIECE_MIN, fr::CE_PIECE_BYTES / (2 * h->cap) / fr::GM_TILE * fr::GM_TILE),
+                                 fr::ce_round(V, fr::GM_TILE));
     h->rows.pitch = fr::ce_round(d, 8);
     if (cudaGetDevice(&h->device) != cudaSuccess ||
         cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, h->device) != cudaSuccess ||
-        cudaFuncSetAttribute(fr::k_ce_loss, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)fr::gm_smem_bytes<fr::CeLoss>()) != cudaSuccess ||
-        cudaFuncSetAttribute(fr::k_ce_grad, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)fr::gm_smem_bytes<fr::CeGrad>()) != cudaSuccess) {
+        fr::gm_setup(fr::k_ce_loss) != cudaSuccess || fr::gm_setup(fr::k_ce_grad) != cudaSuccess) {
         (void)cudaGetLastError();
         delete h;
         return FR_ERR_CUDA;
     }
-    const size_t cap = (size_t)h->cap, pitch = (size_t)h->rows.pitch, d_tiles = (d + fr::CE_BN - 1) / fr::CE_BN;
+    const size_t cap = (size_t)h->cap, pitch = (size_t)h->rows.pitch, d_tiles = (d + fr::GM_TILE - 1) / fr::GM_TILE;
     // dh partials: one plane of all rows, or, with few rows, at most one tile row per SM
-    const size_t dh_rows = std::max(cap, std::max<size_t>(h->sms / d_tiles, 1) * fr::GM_BM);
+    const size_t dh_rows = std::max(cap, std::max<size_t>(h->sms / d_tiles, 1) * fr::GM_TILE);
     cudaError_t e = cudaMalloc(&h->rows.h, cap * pitch * 2);
-    if (e == cudaSuccess) e = cudaMalloc(&h->rows.tgt, cap * 4 * 5 + 4);
-    if (e == cudaSuccess) e = cudaMalloc(&h->partial, cap * h->n_tiles * sizeof(float2));
+    if (e == cudaSuccess) e = cudaMalloc(&h->rows.tgt, cap * 4 * 5 + 8);
+    if (e == cudaSuccess) e = cudaMalloc(&h->partial, cap * 2 * h->n_tiles * sizeof(float2));
     if (e == cudaSuccess) e = cudaMalloc(&h->g[0], cap * h->piece * 2 * 2);
     if (e == cudaSuccess) e = cudaMalloc(&h->dh, dh_rows * pitch * 4);
     if (e == cudaSuccess) e = cudaMalloc(&h->err, sizeof(int32_t));
@@ -501,12 +545,15 @@ extern "C" fr_status fr_ce_init(int32_t V, int32_t d, int32_t max_rows, fr_ce** 
     h->xt = h->rows.g + cap;
     h->rows.idx = reinterpret_cast<int32_t*>(h->xt + cap);
     h->rows.n = h->rows.idx + cap;
+    h->rows.gmax = reinterpret_cast<float*>(h->rows.n + 1);
     h->g[1] = h->g[0] + cap * h->piece;
-    bool ok = fr::gm_encode(&h->map_h_k, false, h->rows.h, h->cap, d, h->rows.pitch * 2, fr::GM_BM) &&
-              fr::gm_encode(&h->map_h_mn, false, h->rows.h, h->cap, d, h->rows.pitch * 2, 64);
+    const int64_t gp = (int64_t)h->piece * 2;
+    bool ok = fr::gm_encode(&h->map_h_k, 2, h->rows.h, h->cap, d, h->rows.pitch * 2, fr::GM_HALF) &&
+              fr::gm_encode(&h->map_h_mn, 2, h->rows.h, h->cap, d, h->rows.pitch * 2, 64);
     for (int b = 0; b < 2; ++b)
-        ok = ok && fr::gm_encode(&h->map_g_k[b], false, h->g[b], h->cap, h->piece, (int64_t)h->piece * 2, fr::GM_BM) &&
-             fr::gm_encode(&h->map_g_mn[b], false, h->g[b], h->cap, h->piece, (int64_t)h->piece * 2, 64);
+        ok = ok && fr::gm_encode(&h->map_g_k[b], 2, h->g[b], h->cap, h->piece, gp, fr::GM_HALF) &&
+             fr::gm_encode(&h->map_g_mn[b], 2, h->g[b], h->cap, h->piece, gp, 64) &&
+             fr::gm_encode(&h->map_g_out[b], 2, h->g[b], h->cap, h->piece, gp, 32);
     if (!ok) {
         ce_free(h);
         return FR_ERR_CUDA;
@@ -525,7 +572,7 @@ extern "C" fr_status fr_ce_loss(fr_ce* h, const void* hidden_dev, int64_t ldh, c
     h->last_stream = s;
     if (rows == 0) return FR_OK;
     fr::CeLoss p{};
-    if (!fr::gm_encode(&p.map_w, false, weight_dev, h->V, h->d, ldw * 2, fr::CE_BN)) return FR_ERR_CUDA;
+    if (!fr::gm_encode(&p.map_w, 2, weight_dev, h->V, h->d, ldw * 2, fr::GM_HALF)) return FR_ERR_CUDA;
     p.map_h = h->map_h_k;
     p.rows = h->rows;
     p.V = h->V;
@@ -537,11 +584,9 @@ extern "C" fr_status fr_ce_loss(fr_ce* h, const void* hidden_dev, int64_t ldh, c
     FR_CUDA_TRY(fr::launch_pdl(fr::k_ce_gather, gather, fr::CE_GATHER_THREADS, 0, s, (const __nv_bfloat16*)hidden_dev, ldh,
                                targets_dev, (const float*)nullptr, (const float*)nullptr, rows, h->V, h->d, h->rows,
                                loss_dev, lse_dev, (__nv_bfloat16*)nullptr, (int64_t)0, h->err));
-    const int64_t tiles = fr::ce_round(rows, fr::GM_BM) / fr::GM_BM * h->n_tiles;
     fr::GmCtl ctl{h->err, h->wait_ns, h->starve};
-    FR_CUDA_TRY(fr::launch_pdl(fr::k_ce_loss, std::min<int64_t>(tiles, h->sms), fr::GM_THREADS,
-                               fr::gm_smem_bytes<fr::CeLoss>(), s, p, ctl));
-    FR_CUDA_TRY(fr::launch_pdl(fr::k_ce_combine, ((int64_t)rows + 7) / 8, 256, 0, s, (const float2*)h->partial, h->n_tiles,
+    FR_CUDA_TRY(fr::gm_launch(fr::k_ce_loss, fr::ce_round(rows, fr::GM_TILE) / fr::GM_TILE * h->n_tiles, h->sms, s, p, ctl));
+    FR_CUDA_TRY(fr::launch_pdl(fr::k_ce_combine, ((int64_t)rows + 7) / 8, 256, 0, s, (const float2*)h->partial, 2 * h->n_tiles,
                                h->rows, (const float*)h->xt, loss_dev, lse_dev, h->err));
     return FR_OK;
 }
@@ -559,24 +604,27 @@ extern "C" fr_status fr_ce_grad(fr_ce* h, const void* hidden_dev, int64_t ldh, c
     const cudaStream_t s = (cudaStream_t)stream;
     h->last_stream = s;
     fr::CeGrad p{};
-    if (!fr::gm_encode(&p.map_w_k, false, weight_dev, h->V, h->d, ldw * 2, fr::CE_BN) ||
-        !fr::gm_encode(&p.map_w_mn, false, weight_dev, h->V, h->d, ldw * 2, 64))
+    if (!fr::gm_encode(&p.map_w_k, 2, weight_dev, h->V, h->d, ldw * 2, fr::GM_HALF) ||
+        !fr::gm_encode(&p.map_w_mn, 2, weight_dev, h->V, h->d, ldw * 2, 64))
         return FR_ERR_CUDA;
     __nv_bfloat16* gh = (__nv_bfloat16*)grad_hidden_dev;
-    const int64_t m_tiles = fr::ce_round(std::max(rows, 1), fr::GM_BM) / fr::GM_BM;  // no rows: dW is still written (zeros)
+    const int64_t m_tiles = fr::ce_round(std::max(rows, 1), fr::GM_TILE) / fr::GM_TILE;  // no rows: dW is still written (zeros)
     p.map_h_k = h->map_h_k;
     p.map_h_mn = h->map_h_mn;
     p.rows = h->rows;
-    p.g_pitch = h->piece;
     p.V = h->V;
     p.d = h->d;
-    p.d_tiles = (h->d + fr::CE_BN - 1) / fr::CE_BN;
-    p.splits = fr::ce_splits(h->sms, m_tiles, p.d_tiles);
-    p.dh = gh ? h->dh : nullptr;
-    p.dh_split = m_tiles * fr::GM_BM * h->rows.pitch;
+    p.d_tiles = (h->d + fr::GM_TILE - 1) / fr::GM_TILE;
+    p.splits = fr::ce_splits(h->sms / 2, m_tiles, p.d_tiles);
+    p.dh = gh != nullptr;
+    p.dh_rows = (int32_t)(m_tiles * fr::GM_TILE);
+    if (!fr::gm_encode(&p.map_dh, 4, h->dh, (int64_t)p.splits * p.dh_rows, h->rows.pitch, h->rows.pitch * 4, 32))
+        return FR_ERR_CUDA;
     p.dw = (__nv_bfloat16*)grad_weight_dev;
     p.ldw = ldgw;
-    p.dw_vec = (reinterpret_cast<uintptr_t>(grad_weight_dev) & 15u) == 0 && (ldgw & 7) == 0;
+    if (p.dw && (reinterpret_cast<uintptr_t>(grad_weight_dev) & 15u) == 0 && (ldgw & 7) == 0)
+        p.dw_staged = fr::gm_staged_columns(h->d, 2);
+    if (p.dw_staged && !fr::gm_encode(&p.map_dw, 2, grad_weight_dev, h->V, h->d, ldgw * 2, 32)) return FR_ERR_CUDA;
     const int32_t gather = std::max((rows + fr::CE_GATHER_ROWS - 1) / fr::CE_GATHER_ROWS, 1);
     FR_CUDA_TRY(fr::launch_pdl(fr::k_ce_gather, gather, fr::CE_GATHER_THREADS, 0, s, (const __nv_bfloat16*)hidden_dev, ldh,
                                targets_dev, lse_dev, grad_loss_dev, rows, h->V, h->d, h->rows, (float*)nullptr,
@@ -593,19 +641,19 @@ extern "C" fr_status fr_ce_grad(fr_ce* h, const void* hidden_dev, int64_t ldh, c
             p.map_g_k = h->map_g_k[(k - 1) & 1];
             p.map_g_mn = h->map_g_mn[(k - 1) & 1];
             if (gh) tiles += m_tiles * p.d_tiles * p.splits;
-            if (p.dw) tiles += (int64_t)(p.v1 - p.v0 + fr::GM_BM - 1) / fr::GM_BM * p.d_tiles;
+            if (p.dw) tiles += (int64_t)(p.v1 - p.v0 + fr::GM_TILE - 1) / fr::GM_TILE * p.d_tiles;
         }
         if (k < pieces) {
             p.w0 = k * h->piece;
             p.w1 = std::min(h->V, (k + 1) * h->piece);
-            p.g_next = h->g[k & 1];
-            tiles += (int64_t)(p.w1 - p.w0 + fr::CE_BN - 1) / fr::CE_BN * m_tiles;
+            p.map_g_out = h->map_g_out[k & 1];
+            tiles += (int64_t)(p.w1 - p.w0 + fr::GM_TILE - 1) / fr::GM_TILE * m_tiles;
         }
-        FR_CUDA_TRY(fr::launch_pdl(fr::k_ce_grad, std::min<int64_t>(tiles, h->sms), fr::GM_THREADS,
-                                   fr::gm_smem_bytes<fr::CeGrad>(), s, p, ctl));
+        FR_CUDA_TRY(fr::gm_launch(fr::k_ce_grad, tiles, h->sms, s, p, ctl));
     }
     if (gh && rows > 0)
-        FR_CUDA_TRY(fr::launch_pdl(fr::k_ce_finish, ((int64_t)rows + 7) / 8, 256, 0, s, (const float*)h->dh, p.dh_split,
+        FR_CUDA_TRY(fr::launch_pdl(fr::k_ce_finish, ((int64_t)rows + 7) / 8, 256, 0, s, (const float*)h->dh,
+                                   p.dh_rows * h->rows.pitch,
                                    p.splits, h->d, h->rows, gh, ldgh,
                                    (int32_t)((reinterpret_cast<uintptr_t>(gh) & 7u) == 0 && (ldgh & 3) == 0)));
     return FR_OK;

@@ -1,49 +1,66 @@
 // fr_gemm.cuh -- the persistent, warp-specialised tcgen05 tile loop that the
 // cross-entropy and 8-bit kernels share.
 //
-// A kernel walks output tiles of 128 x BN values: warp 0 lane 0 copies each
-// K stage's operand tiles (128 bytes of K wide) into a ring with TMA, warp 1
-// lane 0 issues the stage's four tcgen05.mma into one of two tensor-memory
-// accumulators, warps 4..7 (one tensor-memory lane quarter each, one output
-// row per thread) run the kernel's epilogue on the finished accumulator while
-// the next tile's products run.  What differs between kernels is a policy:
+// A cluster of two CTAs walks output tiles of 256 x 256 values
+// (cta_group::2): each CTA stages 128 rows of A and 128 of B per K stage (128
+// bytes of K wide) and holds 128 rows of the accumulator in its tensor memory.
+// The pair reads each operand value once where two single CTAs with 128 x 256
+// tiles would read B twice: 32 KB instead of 48 KB per stage and CTA, which is
+// what bounds the 8-bit products (L2 to shared memory).
+// In each CTA warp 0 lane 0 copies its half of the stage into a ring with TMA
+// (arrivals on the first CTA's barrier); in the first CTA warp 1 lane 0 issues
+// the stage's four tcgen05.mma into one of two tensor-memory accumulators;
+// warps 4..11 (a tensor-memory lane quarter and half of the columns each, one
+// output row per thread; with four warps the exponentials of a log-sum-exp
+// epilogue took longer than an 8-bit tile's products) run the kernel's epilogue
+// on the finished accumulator while the next tile's products run.  What differs
+// between kernels is a policy:
 //
 //   struct P {
 //     static constexpr bool I8;            // 8-bit integers (int32 sums) or bf16 (fp32 sums)
-//     static constexpr int BN, STAGES;     // tile columns, ring depth
+//     static constexpr bool STAGED;        // the epilogue stores through shared memory
+//     static constexpr int STAGES;         // ring depth
 //     struct Tile { int nk; uint32_t idesc; ... };   // K stages; instruction descriptor
 //     struct State { ... };                          // what begin() read after the previous kernel
 //     __device__ State begin() const;
-//     __device__ bool tile(const State&, int i, Tile&) const;      // the i-th tile of this CTA
-//     __device__ void load(const Tile&, int kb, uint8_t* a, uint8_t* b, uint64_t* bar) const;
+//     __device__ bool tile(const State&, int64_t pair, int64_t pairs, int i, Tile&) const;  // the pair's i-th tile
+//     __device__ void load(const Tile&, int kb, int rank, uint8_t* a, uint8_t* b, uint32_t bar) const;
 //     __device__ bool a_mn(const Tile&) const, b_mn(const Tile&) const;  // operand stored MN-major
-//     __device__ void epilogue(const State&, const Tile&, uint32_t taddr, int row_in_tile) const;
+//     // columns [c0, c0 + 128) of one row
+//     __device__ void epilogue(const State&, const Tile&, uint32_t taddr, int row_in_tile, int c0, GmStage&) const;
 //   };
 //
-// Every wait is bounded; on expiry the kernel records FR_ERR_DEVICE, stops
-// issuing, drains the copies and products already issued, frees its tensor
-// memory and returns.
+// Every wait on a barrier is bounded; on expiry the kernel records
+// FR_ERR_DEVICE, stops issuing, drains the copies and products already issued,
+// frees its tensor memory and returns.
 #pragma once
 
 #include <cuda_bf16.h>
+
+#include <algorithm>
 
 #include "fr_internal.cuh"
 #include "fr_tc.cuh"
 
 namespace fr {
 
-constexpr int GM_BM = 128;           // rows per tile: the tensor-memory lanes
+constexpr int GM_TILE = 256;         // rows and columns of a pair's tile
+constexpr int GM_HALF = 128;         // rows of A and of B that one CTA stages: the tensor-memory lanes
 constexpr int GM_KB_BYTES = 128;     // K bytes per stage: one 128-byte swizzle span
-constexpr int GM_THREADS = 256;      // 8 warps
-constexpr int GM_A_BYTES = GM_BM * GM_KB_BYTES;
+constexpr int GM_THREADS = 384;      // 12 warps, 8 of them for the epilogue
+constexpr int GM_EPI_WARPS = 8;
+constexpr int GM_EPI_COLS = 128;     // columns of a tile that one epilogue warp takes
+constexpr int GM_OP_BYTES = GM_HALF * GM_KB_BYTES;  // one operand's half tile per stage
+constexpr int GM_STAGE_BUF = 32 * 128;              // one staged store: 32 rows x 128 bytes
+constexpr uint32_t GM_TMEM_COLS = 2 * GM_TILE;      // two accumulators
 
 // Instruction descriptor: accumulator type at bits 4-5 (1 = fp32, 2 = int32),
 // A and B types at bits 7-9 and 10-12 (kind::f16: 1 = bf16; kind::i8: 1 =
 // signed), "MN-major" flags of A and B at bits 15 and 16, N >> 3 at bits
 // 17-22, M >> 4 at bits 24-28.
-__host__ __device__ constexpr uint32_t gm_idesc(bool i8, int n, bool a_mn = false, bool b_mn = false) {
+__host__ __device__ constexpr uint32_t gm_idesc(bool i8, bool a_mn = false, bool b_mn = false) {
     return ((i8 ? 2u : 1u) << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
-           ((uint32_t)(n >> 3) << 17) | ((uint32_t)(GM_BM >> 4) << 24);
+           ((uint32_t)(GM_TILE >> 3) << 17) | ((uint32_t)(GM_TILE >> 4) << 24);
 }
 
 // Shared-memory descriptor of an MN-major bf16 tile with the 128-byte
@@ -63,25 +80,101 @@ __device__ __forceinline__ void gm_umma(uint32_t tmem_d, uint64_t adesc, uint64_
         asm volatile(
             "{\n\t.reg .pred p;\n\t"
             "setp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+            "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
             "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
             : "memory");
     else
         asm volatile(
             "{\n\t.reg .pred p;\n\t"
             "setp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
             "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
             : "memory");
 }
 
+// Arrives on the barrier at this offset in both CTAs once every product issued
+// so far by this thread has completed.
+__device__ __forceinline__ void gm_commit_both(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+__device__ __forceinline__ uint32_t gm_cta_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+// Address of `p`'s counterpart in the pair's first CTA.
+__device__ __forceinline__ uint32_t gm_in_first(const void* p) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(p)));
+    return a;
+}
+
+__device__ __forceinline__ void gm_arrive_remote(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void gm_cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// 2-D tiled TMA load into this CTA that arrives on the first CTA's barrier.
+__device__ __forceinline__ void gm_tma_load(const CUtensorMap* map, void* dst, uint32_t bar, int32_t x, int32_t y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+        "[%4];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+// A warp's staging buffer of 32 rows x 128 bytes, written out with TMA
+// (128-byte swizzle: 16-byte piece j of row l lies at piece j ^ (l & 7), which
+// also spreads the lanes' writes over the banks).
+struct GmStage {
+    uint8_t* buf;
+    __device__ __forceinline__ uint8_t* row(int lane) const {
+        // the buffer's last store has read its data
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        __syncwarp();
+        return buf + lane * 128;
+    }
+    __device__ __forceinline__ void put(uint8_t* row, int lane, int piece, uint4 v) const {
+        *reinterpret_cast<uint4*>(row + ((piece ^ (lane & 7)) << 4)) = v;
+    }
+    // Stores the buffer's 32 rows at (x, y), or adds them (fp32), clipped to
+    // the map's extent.
+    template <bool ADD>
+    __device__ __forceinline__ void send(const CUtensorMap* map, int lane, int32_t x, int32_t y) const {
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+            if (ADD)
+                asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                                 reinterpret_cast<uint64_t>(map)),
+                             "r"(x), "r"(y), "r"(smem_u32(buf))
+                             : "memory");
+            else
+                asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                                 reinterpret_cast<uint64_t>(map)),
+                             "r"(x), "r"(y), "r"(smem_u32(buf))
+                             : "memory");
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+    }
+};
+
 template <int STAGES>
 struct GmSmem {
-    uint64_t full[STAGES];
-    uint64_t empty[STAGES];
+    uint64_t full[STAGES];      // used in the first CTA: both CTAs' copies of a stage have landed
+    uint64_t empty[STAGES];     // the stage's products are done
     uint64_t tmem_full[2];
-    uint64_t tmem_empty[2];
-    uint64_t mma_done;  // every product this CTA issued has completed
+    uint64_t tmem_empty[2];     // used in the first CTA: both CTAs' epilogues have read the accumulator
+    uint64_t mma_done;          // every product the pair issued has completed
     uint32_t tmem_base;
     int32_t abort_flag;
 };
@@ -95,27 +188,22 @@ struct GmCtl {
 
 template <class P>
 __host__ __device__ constexpr size_t gm_smem_bytes() {
-    return 1024 + (size_t)P::STAGES * (GM_A_BYTES + P::BN * GM_KB_BYTES) + sizeof(GmSmem<P::STAGES>);
-}
-
-// Tensor-memory columns of the two accumulators (a power of two, at least 32).
-template <class P>
-__host__ __device__ constexpr uint32_t gm_tmem_cols() {
-    uint32_t c = 32;
-    while (c < 2u * P::BN) c *= 2;
-    return c;
+    return 1024 + (size_t)P::STAGES * 2 * GM_OP_BYTES + (P::STAGED ? GM_EPI_WARPS * GM_STAGE_BUF : 0) + sizeof(GmSmem<P::STAGES>);
 }
 
 template <class P>
 __device__ __forceinline__ void gm_run(const P& p, const GmCtl& ctl) {
     extern __shared__ uint8_t gm_smem_raw[];
-    constexpr int STAGES = P::STAGES, BN = P::BN, B_BYTES = BN * GM_KB_BYTES;
+    constexpr int STAGES = P::STAGES;
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(gm_smem_raw) + 1023) & ~(uintptr_t)1023);
     uint8_t* ringA = base;
-    uint8_t* ringB = base + STAGES * GM_A_BYTES;
-    GmSmem<STAGES>* sm = reinterpret_cast<GmSmem<STAGES>*>(ringB + STAGES * B_BYTES);
+    uint8_t* ringB = base + STAGES * GM_OP_BYTES;
+    uint8_t* stage = ringB + STAGES * GM_OP_BYTES;
+    GmSmem<STAGES>* sm = reinterpret_cast<GmSmem<STAGES>*>(stage + (P::STAGED ? GM_EPI_WARPS * GM_STAGE_BUF : 0));
     volatile int32_t* abort_flag = &sm->abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = gm_cta_rank();
+    const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -124,20 +212,21 @@ __device__ __forceinline__ void gm_run(const P& p, const GmCtl& ctl) {
         }
         for (int i = 0; i < 2; ++i) {
             tc_mbar_init(&sm->tmem_full[i], 1);
-            tc_mbar_init(&sm->tmem_empty[i], 4 * 32);
+            tc_mbar_init(&sm->tmem_empty[i], 2 * GM_EPI_WARPS);
         }
         tc_mbar_init(&sm->mma_done, 1);
         sm->abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 2) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm->tmem_base)),
-                     "r"(gm_tmem_cols<P>())
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm->tmem_base)),
+                     "r"(GM_TMEM_COLS)
                      : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     tc_fence_before();
     __syncthreads();
+    gm_cluster_sync();
     tc_fence_after();
     const uint32_t tmem = sm->tmem_base;
     griddep_wait();
@@ -149,7 +238,7 @@ __device__ __forceinline__ void gm_run(const P& p, const GmCtl& ctl) {
         if (lane == 0 && !ctl.starve) {
             uint32_t it = 0;
             bool ok = true;
-            for (int i = 0; ok && p.tile(st, i, t); ++i) {
+            for (int i = 0; ok && p.tile(st, pair, pairs, i, t); ++i) {
                 for (int kb = 0; kb < t.nk; ++kb, ++it) {
                     const uint32_t s = it % STAGES;
                     if (it >= (uint32_t)STAGES &&
@@ -157,24 +246,35 @@ __device__ __forceinline__ void gm_run(const P& p, const GmCtl& ctl) {
                         ok = false;
                         break;
                     }
-                    tc_arrive_expect_tx(&sm->full[s], (uint32_t)(GM_A_BYTES + B_BYTES));
-                    p.load(t, kb, ringA + s * GM_A_BYTES, ringB + s * B_BYTES, &sm->full[s]);
+                    // the first CTA's barrier counts both CTAs' bytes
+                    if (rank == 0) tc_arrive_expect_tx(&sm->full[s], (uint32_t)(4 * GM_OP_BYTES));
+                    p.load(t, kb, (int)rank, ringA + s * GM_OP_BYTES, ringB + s * GM_OP_BYTES, gm_in_first(&sm->full[s]));
                 }
             }
-            // the last copies land before the CTA ends, whoever waits for them
-            for (uint32_t j = (it > (uint32_t)STAGES ? it - STAGES : 0u); j < it; ++j)
-                tc_wait_drain(&sm->full[j % STAGES], (j / STAGES) & 1u);
+            // The last copies land before the CTAs end.  Normally the first
+            // CTA's barriers say so for both; after an abort the pair's CTAs
+            // may have issued different stages, so each also gives its own
+            // copies a millisecond.
+            if (rank == 0)
+                for (uint32_t j = (it > (uint32_t)STAGES ? it - STAGES : 0u); ok && j < it; ++j)
+                    tc_wait_drain(&sm->full[j % STAGES], (j / STAGES) & 1u);
+            if (!ok || *abort_flag) {
+                const uint64_t t0 = tc_now_ns();
+                for (uint32_t k = 0; k < (1u << 20) && tc_now_ns() - t0 < 1000000ull; ++k) __nanosleep(200);
+            }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (lane == 0 && rank == 0) {
             uint32_t it = 0;
             bool ok = true;
-            for (int i = 0; ok && p.tile(st, i, t); ++i) {
+            for (int i = 0; ok && p.tile(st, pair, pairs, i, t); ++i) {
                 const int acc = i & 1;
                 if (i >= 2 && !tc_wait(&sm->tmem_empty[acc], ((i >> 1) & 1) ^ 1, abort_flag, ctl.err, ctl.wait_ns)) break;
                 tc_fence_after();
-                const uint32_t d_tmem = tmem + (uint32_t)(acc * BN);
+                const uint32_t d_tmem = tmem + (uint32_t)(acc * GM_TILE);
                 const bool amn = p.a_mn(t), bmn = p.b_mn(t);
+                // address fields count 16-byte units: the K slices are 32 bytes (K-major) or 2,048 (MN-major) apart
+                const uint32_t ia = amn ? 2048 >> 4 : 32 >> 4, ib = bmn ? 2048 >> 4 : 32 >> 4;
                 for (int kb = 0; kb < t.nk; ++kb, ++it) {
                     const uint32_t s = it % STAGES;
                     if (!tc_wait(&sm->full[s], (it / STAGES) & 1u, abort_flag, ctl.err, ctl.wait_ns)) {
@@ -182,39 +282,44 @@ __device__ __forceinline__ void gm_run(const P& p, const GmCtl& ctl) {
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t sa = smem_u32(ringA + s * GM_A_BYTES), sb = smem_u32(ringB + s * B_BYTES);
+                    const uint32_t sa = smem_u32(ringA + s * GM_OP_BYTES), sb = smem_u32(ringB + s * GM_OP_BYTES);
                     const uint64_t da = amn ? smem_desc_mn_sw128(sa) : smem_desc_sw128(sa);
                     const uint64_t db = bmn ? smem_desc_mn_sw128(sb) : smem_desc_sw128(sb);
-                    // address fields count 16-byte units: the K slices are 32 bytes (K-major) or 2,048 (MN-major) apart
-                    const uint32_t ia = amn ? 2048 >> 4 : 32 >> 4, ib = bmn ? 2048 >> 4 : 32 >> 4;
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
                         gm_umma<P::I8>(d_tmem, da + (uint64_t)(kk * ia), db + (uint64_t)(kk * ib), t.idesc,
                                        (kb | kk) != 0 ? 1u : 0u);
-                    tc_umma_commit(&sm->empty[s]);  // the stage is free once these products are done
+                    gm_commit_both(&sm->empty[s]);  // the stage is free in both CTAs once these products are done
                 }
-                tc_umma_commit(&sm->tmem_full[acc]);  // the accumulator is complete (or, on abort, quiet)
+                gm_commit_both(&sm->tmem_full[acc]);  // the accumulators are complete (or, on abort, quiet)
             }
             // the tensor memory is freed only after every product issued here is done
-            tc_umma_commit(&sm->mma_done);
-            tc_wait_drain(&sm->mma_done, 0);
+            gm_commit_both(&sm->mma_done);
         }
+        // in both CTAs: the commits' arrivals reach no CTA that has ended
+        if (lane == 0) tc_wait_drain(&sm->mma_done, 0);
     } else if (warp >= 4) {
-        const int q = warp & 3;
-        for (int i = 0; p.tile(st, i, t); ++i) {
+        const int q = warp & 3, c0 = ((warp - 4) >> 2) * GM_EPI_COLS;
+        GmStage sg{stage + (warp - 4) * GM_STAGE_BUF};
+        const uint32_t empty0 = gm_in_first(&sm->tmem_empty[0]), empty1 = gm_in_first(&sm->tmem_empty[1]);
+        for (int i = 0; p.tile(st, pair, pairs, i, t); ++i) {
             const int acc = i & 1;
             if (!tc_wait(&sm->tmem_full[acc], (i >> 1) & 1, abort_flag, ctl.err, ctl.wait_ns)) break;
             tc_fence_after();
-            p.epilogue(st, t, tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BN), q * 32 + lane);
+            p.epilogue(st, t, tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * GM_TILE), (int)rank * GM_HALF + q * 32 + lane,
+                       c0, sg);
             tc_fence_before();
-            tc_arrive(&sm->tmem_empty[acc]);
+            __syncwarp();
+            if (lane == 0) gm_arrive_remote(acc ? empty1 : empty0);
         }
+        if (P::STAGED && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
     tc_fence_before();
     __syncthreads();
+    gm_cluster_sync();  // nobody's copies, products or arrivals reach a CTA that has ended
     if (warp == 2) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(gm_tmem_cols<P>()) : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(GM_TMEM_COLS) : "memory");
     }
 }
 
@@ -224,6 +329,13 @@ __device__ __forceinline__ void gm_ld32_i32(uint32_t taddr, int32_t (&v)[32]) {
     tc_tmem_ld32(taddr, f);
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = __float_as_int(f[i]);
+}
+
+__device__ __forceinline__ void gm_ld32(uint32_t taddr, float* v) {
+    float f[32];
+    tc_tmem_ld32(taddr, f);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = f[i];
 }
 
 // Maximum that keeps a NaN.
@@ -288,60 +400,63 @@ __device__ __forceinline__ uint4 gm_pack8(const float* v) {
     return o;
 }
 
-// Stores the first n (<= 32) of 32 values of one row; `vec`: dst and the row
-// pitch are multiples of 16 bytes, so whole 16-byte groups go out at once.
-__device__ __forceinline__ void gm_store32(__nv_bfloat16* dst, const float (&v)[32], int n, bool vec) {
-    if (vec) {
+// Stores the first n of CW values of one row whose start has no alignment.
+template <int CW>
+__device__ __forceinline__ void gm_store(__nv_bfloat16* dst, const float (&v)[CW], int n) {
 #pragma unroll
-        for (int i = 0; i < 32; i += 8) {
-            if (i + 8 <= n) {
-                *reinterpret_cast<uint4*>(dst + i) = gm_pack8(v + i);
-            } else {
+    for (int i = 0; i < CW; ++i)
+        if (i < n) dst[i] = __float2bfloat16_rn(v[i]);
+}
+template <int CW>
+__device__ __forceinline__ void gm_store(float* dst, const float (&v)[CW], int n) {
 #pragma unroll
-                for (int j = i; j < i + 8; ++j)
-                    if (j < n) dst[j] = __float2bfloat16_rn(v[j]);
-            }
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (i < n) dst[i] = __float2bfloat16_rn(v[i]);
-    }
+    for (int i = 0; i < CW; ++i)
+        if (i < n) dst[i] = v[i];
 }
 
-__device__ __forceinline__ void gm_store32(float* dst, const float (&v)[32], int n, bool vec) {
-    if (vec) {
+// Sends 64 bf16 columns of the warp's 32 rows to (x, y) of `map`.
+__device__ __forceinline__ void gm_stage64(const GmStage& sg, const CUtensorMap* map, int lane, const float (&v)[64], int x, int y) {
+    uint8_t* row = sg.row(lane);
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-            if (i + 4 <= n) {
-                *reinterpret_cast<float4*>(dst + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-            } else {
-#pragma unroll
-                for (int j = i; j < i + 4; ++j)
-                    if (j < n) dst[j] = v[j];
-            }
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (i < n) dst[i] = v[i];
-    }
+    for (int j = 0; j < 8; ++j) sg.put(row, lane, j, gm_pack8(v + 8 * j));
+    sg.send<false>(map, lane, x, y);
 }
 
-// 2-D row-major tensor map: `rows` x `cols` elements of `esize` bytes, row
-// pitch `pitch` bytes, box box_rows x 128 bytes, 128-byte swizzle, zero fill
-// out of bounds.
-inline bool gm_encode(CUtensorMap* map, bool i8, const void* ptr, int64_t rows, int64_t cols, int64_t pitch,
+// Sends (or adds) 32 fp32 columns of the warp's 32 rows to (x, y) of `map`.
+template <bool ADD>
+__device__ __forceinline__ void gm_stage32(const GmStage& sg, const CUtensorMap* map, int lane, const float (&v)[32], int x, int y) {
+    uint8_t* row = sg.row(lane);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        sg.put(row, lane, j, make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]), __float_as_uint(v[4 * j + 2]),
+                                        __float_as_uint(v[4 * j + 3])));
+    sg.send<ADD>(map, lane, x, y);
+}
+
+// 2-D row-major tensor map: `rows` x `cols` elements of `esize` bytes (1: 8-bit
+// integers, 2: bf16, 4: fp32), row pitch `pitch` bytes, box box_rows x 128
+// bytes, 128-byte swizzle, zero fill out of bounds.
+inline bool gm_encode(CUtensorMap* map, int esize, const void* ptr, int64_t rows, int64_t cols, int64_t pitch,
                       uint32_t box_rows) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)pitch};
-    const cuuint32_t box[2] = {(cuuint32_t)(i8 ? 128 : 64), box_rows};
+    const cuuint32_t box[2] = {(cuuint32_t)(128 / esize), box_rows};
     const cuuint32_t estr[2] = {1, 1};
-    return fn(map, i8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr),
-              dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const CUtensorMapDataType type = esize == 1   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                     : esize == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                  : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+    return fn(map, type, 2, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+           CUDA_SUCCESS;
+}
+
+// Columns of a row of `cols` elements that whole 128-byte TMA stores may write:
+// a store that the map clips fills up its last 16 bytes (with zeros, measured),
+// so a row that ends inside them keeps its last group for plain stores.
+inline int32_t gm_staged_columns(int32_t cols, int esize) {
+    return (int64_t)cols * esize % 16 == 0 ? cols : cols / (128 / esize) * (128 / esize);
 }
 
 // kernel<<<grid, block, smem, s>>>(args...) with programmatic stream
@@ -360,6 +475,33 @@ inline cudaError_t launch_pdl(void (*kernel)(KArgs...), int64_t grid, int block,
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, KArgs(args)...);
+}
+
+// Raises a gm_run kernel's shared-memory limit on the current device.
+template <class P>
+inline cudaError_t gm_setup(void (*kernel)(P, GmCtl)) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)gm_smem_bytes<P>());
+}
+
+// A gm_run kernel over `tiles` tiles: clusters of two CTAs, at most one CTA per SM.
+template <class P>
+inline cudaError_t gm_launch(void (*kernel)(P, GmCtl), int64_t tiles, int32_t sms, cudaStream_t s, const P& p,
+                             const GmCtl& ctl) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    cfg.gridDim = dim3((unsigned)(2 * std::min<int64_t>(tiles, sms / 2)));
+    cfg.blockDim = dim3(GM_THREADS);
+    cfg.dynamicSmemBytes = gm_smem_bytes<P>();
+    cfg.stream = s;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, p, ctl);
 }
 
 }  // namespace fr

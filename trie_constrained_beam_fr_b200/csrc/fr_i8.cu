@@ -9,9 +9,9 @@
 // why the whole product runs on integers.
 //
 //   k_i8_quantize  a warp per row; reads the row twice (maximum, then values).
-//   k_i8_out       tcgen05 kind::i8 tiles of 128 rows x 256 channels; the
+//   k_i8<I8Out>    tcgen05 kind::i8 tiles of 256 rows x 256 channels; the
 //                  epilogue scales and writes logits (bf16 or fp32).
-//   k_i8_lse       the same product whose epilogue reduces each row to
+//   k_i8<I8Lse>    the same product whose epilogue reduces each row to
 //                  (max, scaled sum) partials and writes the SID slice, for
 //                  the step from rows; k_i8_combine merges the partials.
 #include <cuda.h>
@@ -69,40 +69,39 @@ __global__ void __launch_bounds__(256) k_i8_quantize(const T* __restrict__ x, in
     if (lane == 0) scale[r] = s;
 }
 
-// Tile walk shared by the two products: m fastest, so CTAs running together
+// Tile walk shared by the two products: m fastest, so pairs running together
 // share the weight tile and the activations stay in L2.
 struct I8Base {
     static constexpr bool I8 = true;
-    static constexpr int BN = 256, STAGES = 4;
     struct Tile {
         int nk, m0, n0;
         uint32_t idesc;
     };
+    struct State {};
     CUtensorMap map_x, map_w;
     int32_t rows, N, k_blocks, m_tiles, n_tiles;
     const float* xs;
     const float* ws;
     int32_t ws_vec;  // ws starts on 16 bytes
 
-    struct State {};
     __device__ __forceinline__ State begin() const { return {}; }
-    __device__ __forceinline__ bool tile(const State&, int i, Tile& t) const {
-        const int64_t g = blockIdx.x + (int64_t)i * gridDim.x;
+    __device__ __forceinline__ bool tile(const State&, int64_t pair, int64_t pairs, int i, Tile& t) const {
+        const int64_t g = pair + i * pairs;
         if (g >= (int64_t)m_tiles * n_tiles) return false;
-        t.m0 = (int)(g % m_tiles) * GM_BM;
-        t.n0 = (int)(g / m_tiles) * BN;
+        t.m0 = (int)(g % m_tiles) * GM_TILE;
+        t.n0 = (int)(g / m_tiles) * GM_TILE;
         t.nk = k_blocks;
-        t.idesc = gm_idesc(true, BN);
+        t.idesc = gm_idesc(true);
         return true;
     }
     __device__ __forceinline__ bool a_mn(const Tile&) const { return false; }
     __device__ __forceinline__ bool b_mn(const Tile&) const { return false; }
-    __device__ __forceinline__ void load(const Tile& t, int kb, uint8_t* a, uint8_t* b, uint64_t* bar) const {
-        tc_tma_load_2d(&map_x, a, bar, kb * GM_KB_BYTES, t.m0);
-        tc_tma_load_2d(&map_w, b, bar, kb * GM_KB_BYTES, t.n0);
+    __device__ __forceinline__ void load(const Tile& t, int kb, int rank, uint8_t* a, uint8_t* b, uint32_t bar) const {
+        gm_tma_load(&map_x, a, bar, kb * GM_KB_BYTES, t.m0 + rank * GM_HALF);
+        gm_tma_load(&map_w, b, bar, kb * GM_KB_BYTES, t.n0 + rank * GM_HALF);
     }
     // y of 32 columns from n on: the row's scale first, then the channel's
-    __device__ __forceinline__ void scaled(uint32_t taddr, int n, float xscale, float (&v)[32]) const {
+    __device__ __forceinline__ void scaled(uint32_t taddr, int n, float xscale, float* v) const {
         int32_t acc[32];
         gm_ld32_i32(taddr, acc);
         if (ws_vec && n + 32 <= N) {
@@ -123,31 +122,52 @@ struct I8Base {
 
 template <class T>
 struct I8Out : I8Base {
+    static constexpr bool STAGED = true;
+    static constexpr int STAGES = 6;
+    CUtensorMap map_out;
     T* out;
     int64_t ldo;
-    int32_t out_vec;
-    __device__ __forceinline__ void epilogue(const State&, const Tile& t, uint32_t taddr, int r) const {
-        const int row = t.m0 + r;
+    // Columns below `staged` go out through shared memory and TMA: none unless
+    // rows start on 16 bytes; all when rows are whole 16-byte pieces, else the
+    // whole groups of columns (a clipped TMA store fills its last 16 bytes).
+    int32_t staged;
+    __device__ __forceinline__ void epilogue(const State&, const Tile& t, uint32_t taddr, int r, int c0, const GmStage& sg) const {
+        constexpr int CW = 128 / sizeof(T);  // columns per staged store
+        const int row = t.m0 + r, lane = threadIdx.x & 31, row0 = row - lane;
         const float xscale = row < rows ? xs[row] : 0.f;
 #pragma unroll 1
-        for (int c = 0; c < BN && t.n0 + c < N; c += 32) {
-            float v[32];
-            scaled(taddr + (uint32_t)c, t.n0 + c, xscale, v);
-            if (row < rows) gm_store32(out + row * ldo + t.n0 + c, v, min(32, N - t.n0 - c), out_vec != 0);
+        for (int c = c0; c < c0 + GM_EPI_COLS && t.n0 + c < N; c += CW) {
+            float v[CW];
+#pragma unroll
+            for (int k = 0; k < CW; k += 32) scaled(taddr + (uint32_t)(c + k), t.n0 + c + k, xscale, v + k);
+            if (t.n0 + c < staged) {
+                if (row0 < rows) put(sg, lane, v, t.n0 + c, row0);
+            } else if (row < rows) {
+                gm_store(out + row * ldo + t.n0 + c, v, min(CW, N - t.n0 - c));
+            }
         }
+    }
+    __device__ __forceinline__ void put(const GmStage& sg, int lane, const float (&v)[64], int x, int y) const {
+        gm_stage64(sg, &map_out, lane, v, x, y);
+    }
+    __device__ __forceinline__ void put(const GmStage& sg, int lane, const float (&v)[32], int x, int y) const {
+        gm_stage32<false>(sg, &map_out, lane, v, x, y);
     }
 };
 
 struct I8Lse : I8Base {
-    float2* partial;  // [rows, n_tiles]
+    static constexpr bool STAGED = false;
+    static constexpr int STAGES = 7;
+    float2* partial;  // [rows, n_parts] (max, scaled sum) of 128 columns each
+    int32_t n_parts;
     float* slice;     // [rows, sid_span]
     int32_t sid_base, sid_span;
-    __device__ __forceinline__ void epilogue(const State&, const Tile& t, uint32_t taddr, int r) const {
+    __device__ __forceinline__ void epilogue(const State&, const Tile& t, uint32_t taddr, int r, int c0, const GmStage&) const {
         const int row = t.m0 + r;
         const float xscale = row < rows ? xs[row] : 0.f;
         float m = -INFINITY, s = 0.f;
 #pragma unroll 1
-        for (int c = 0; c < BN && t.n0 + c < N; c += 32) {
+        for (int c = c0; c < c0 + GM_EPI_COLS && t.n0 + c < N; c += 32) {
             const int n = t.n0 + c;
             float v[32];
             scaled(taddr + (uint32_t)c, n, xscale, v);
@@ -165,7 +185,7 @@ struct I8Lse : I8Base {
             }
             gm_lse_fold(v, m, s);
         }
-        if (row < rows) partial[(int64_t)row * n_tiles + t.n0 / BN] = make_float2(m, s);
+        if (row < rows) partial[(int64_t)row * n_parts + (t.n0 + c0) / GM_EPI_COLS] = make_float2(m, s);
     }
 };
 
@@ -174,13 +194,13 @@ __global__ void __launch_bounds__(GM_THREADS, 1) k_i8(const __grid_constant__ P 
     gm_run(p, ctl);
 }
 
-__global__ void __launch_bounds__(256) k_i8_combine(const float2* __restrict__ partial, int32_t rows, int32_t n_tiles,
+__global__ void __launch_bounds__(256) k_i8_combine(const float2* __restrict__ partial, int32_t rows, int32_t n_parts,
                                                     float* __restrict__ lse, int32_t* __restrict__ err) {
     griddep_wait();
     griddep_launch_dependents();
     const int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     if (r >= rows) return;
-    const float v = gm_lse_combine(partial + r * n_tiles, n_tiles);
+    const float v = gm_lse_combine(partial + r * n_parts, n_parts);
     if ((threadIdx.x & 31) == 0) {
         if (!isfinite(v)) set_error(err, FR_ERR_NAN_LOGIT);
         lse[r] = v;
@@ -195,7 +215,7 @@ struct fr_i8 {
     const float* ws = nullptr;
     int32_t N = 0, d = 0, max_rows = 0, sid_base = 0, sid_span = 0, n_tiles = 0, sms = 0, device = 0;
     CUtensorMap map_w;
-    float2* partial = nullptr;  // [max_rows, n_tiles]
+    float2* partial = nullptr;  // [max_rows, 2 * n_tiles]
     int32_t* err = nullptr;
     cudaStream_t last_stream = nullptr;
     uint64_t wait_ns = FR_WAIT_LIMIT_NS;
@@ -210,12 +230,12 @@ bool i8_on_device(const fr_i8* h) {
 }
 
 fr_status i8_base(fr_i8* h, const int8_t* xq, int64_t ldx, const float* xs, int32_t rows, fr::I8Base* b) {
-    if (!fr::gm_encode(&b->map_x, true, xq, rows, h->d, ldx, fr::GM_BM)) return FR_ERR_CUDA;
+    if (!fr::gm_encode(&b->map_x, 1, xq, rows, h->d, ldx, fr::GM_HALF)) return FR_ERR_CUDA;
     b->map_w = h->map_w;
     b->rows = rows;
     b->N = h->N;
     b->k_blocks = (h->d + fr::GM_KB_BYTES - 1) / fr::GM_KB_BYTES;
-    b->m_tiles = (rows + fr::GM_BM - 1) / fr::GM_BM;
+    b->m_tiles = (rows + fr::GM_TILE - 1) / fr::GM_TILE;
     b->n_tiles = h->n_tiles;
     b->xs = xs;
     b->ws = h->ws;
@@ -226,10 +246,22 @@ fr_status i8_base(fr_i8* h, const int8_t* xq, int64_t ldx, const float* xs, int3
 template <class P>
 fr_status i8_launch(fr_i8* h, const P& p, cudaStream_t s) {
     fr::GmCtl ctl{h->err, h->wait_ns, h->starve};
-    const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles;
-    FR_CUDA_TRY(fr::launch_pdl(fr::k_i8<P>, std::min<int64_t>(tiles, h->sms), fr::GM_THREADS, fr::gm_smem_bytes<P>(), s,
-                               p, ctl));
+    FR_CUDA_TRY(fr::gm_launch(fr::k_i8<P>, (int64_t)p.m_tiles * p.n_tiles, h->sms, s, p, ctl));
     return FR_OK;
+}
+
+template <class T>
+fr_status i8_out(fr_i8* h, const int8_t* xq, int64_t ldx, const float* xs, int32_t rows, void* out, int64_t ldo,
+                 cudaStream_t s) {
+    fr::I8Out<T> p{};
+    const fr_status st = i8_base(h, xq, ldx, xs, rows, &p);
+    if (st != FR_OK) return st;
+    p.out = (T*)out;
+    p.ldo = ldo;
+    if ((reinterpret_cast<uintptr_t>(out) & 15u) == 0 && (ldo * sizeof(T)) % 16 == 0)
+        p.staged = fr::gm_staged_columns(h->N, sizeof(T));
+    if (p.staged && !fr::gm_encode(&p.map_out, sizeof(T), out, rows, h->N, ldo * sizeof(T), 32)) return FR_ERR_CUDA;
+    return i8_launch(h, p, s);
 }
 
 bool i8_bad_x(const fr_i8* h, const int8_t* xq, int64_t ldx, const float* xs, int32_t rows) {
@@ -276,20 +308,17 @@ extern "C" fr_status fr_i8_init(const int8_t* weight_dev, int64_t ldw, const flo
     h->max_rows = max_rows;
     h->sid_base = sid_base;
     h->sid_span = sid_span;
-    h->n_tiles = (N + fr::I8Base::BN - 1) / fr::I8Base::BN;
-    const int smem = (int)fr::gm_smem_bytes<fr::I8Base>();
+    h->n_tiles = (N + fr::GM_TILE - 1) / fr::GM_TILE;
     if (cudaGetDevice(&h->device) != cudaSuccess ||
         cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, h->device) != cudaSuccess ||
-        !fr::gm_encode(&h->map_w, true, weight_dev, N, d, ldw, fr::I8Base::BN) ||
-        cudaFuncSetAttribute(fr::k_i8<fr::I8Out<float>>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
-        cudaFuncSetAttribute(fr::k_i8<fr::I8Out<__nv_bfloat16>>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
-            cudaSuccess ||
-        cudaFuncSetAttribute(fr::k_i8<fr::I8Lse>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+        !fr::gm_encode(&h->map_w, 1, weight_dev, N, d, ldw, fr::GM_HALF) ||
+        fr::gm_setup(fr::k_i8<fr::I8Out<float>>) != cudaSuccess ||
+        fr::gm_setup(fr::k_i8<fr::I8Out<__nv_bfloat16>>) != cudaSuccess || fr::gm_setup(fr::k_i8<fr::I8Lse>) != cudaSuccess) {
         (void)cudaGetLastError();
         delete h;
         return FR_ERR_CUDA;
     }
-    cudaError_t e = cudaMalloc(&h->partial, sizeof(float2) * (size_t)max_rows * h->n_tiles);
+    cudaError_t e = cudaMalloc(&h->partial, sizeof(float2) * (size_t)max_rows * 2 * h->n_tiles);
     if (e == cudaSuccess) e = cudaMalloc(&h->err, sizeof(int32_t));
     if (e == cudaSuccess) e = cudaMemset(h->err, 0, sizeof(int32_t));
     if (e != cudaSuccess) {
@@ -314,23 +343,8 @@ extern "C" fr_status fr_i8_matmul(fr_i8* h, const int8_t* xq_dev, int64_t ldx, c
     const cudaStream_t s = (cudaStream_t)stream;
     h->last_stream = s;
     if (rows == 0) return FR_OK;
-    const int32_t vec = (reinterpret_cast<uintptr_t>(out_dev) & 15u) == 0 && (ldo * esize) % 16 == 0;
-    if (out_dtype == FR_F32) {
-        fr::I8Out<float> p{};
-        const fr_status st = i8_base(h, xq_dev, ldx, xscale_dev, rows, &p);
-        if (st != FR_OK) return st;
-        p.out = (float*)out_dev;
-        p.ldo = ldo;
-        p.out_vec = vec;
-        return i8_launch(h, p, s);
-    }
-    fr::I8Out<__nv_bfloat16> p{};
-    const fr_status st = i8_base(h, xq_dev, ldx, xscale_dev, rows, &p);
-    if (st != FR_OK) return st;
-    p.out = (__nv_bfloat16*)out_dev;
-    p.ldo = ldo;
-    p.out_vec = vec;
-    return i8_launch(h, p, s);
+    return out_dtype == FR_F32 ? i8_out<float>(h, xq_dev, ldx, xscale_dev, rows, out_dev, ldo, s)
+                               : i8_out<__nv_bfloat16>(h, xq_dev, ldx, xscale_dev, rows, out_dev, ldo, s);
 }
 
 extern "C" fr_status fr_i8_lse(fr_i8* h, const int8_t* xq_dev, int64_t ldx, const float* xscale_dev, int32_t rows,
@@ -346,13 +360,14 @@ extern "C" fr_status fr_i8_lse(fr_i8* h, const int8_t* xq_dev, int64_t ldx, cons
     fr_status st = i8_base(h, xq_dev, ldx, xscale_dev, rows, &p);
     if (st != FR_OK) return st;
     p.partial = h->partial;
+    p.n_parts = 2 * h->n_tiles;
     p.slice = slice_dev;
     p.sid_base = h->sid_base;
     p.sid_span = h->sid_span;
     st = i8_launch(h, p, s);
     if (st != FR_OK) return st;
     FR_CUDA_TRY(fr::launch_pdl(fr::k_i8_combine, ((int64_t)rows + 7) / 8, 256, 0, s, (const float2*)h->partial, rows,
-                               h->n_tiles, lse_dev, h->err));
+                               2 * h->n_tiles, lse_dev, h->err));
     return FR_OK;
 }
 
