@@ -97,6 +97,9 @@ def _grad_reference(grad, tok, V, scale, before):
     (2049, 5000, 40, F32, BF16, False, 8, 8),
     (4100, 300000, 24, BF16, BF16, True, 5, 3),   # 19 bits of tokens: three sort passes
     (9000, 64, 136, BF16, BF16, False, 0, 0),     # runs over many chunks
+    (1024, 500, 264, F32, BF16, False, 0, 0),     # the most tokens of the one-kernel form
+    (1025, 500, 264, F32, BF16, False, 0, 0),     # the fewest of the sorted form
+    (300000, 700, 8, F32, F32, False, 0, 0),      # several tiles per sorting CTA
 ])
 def test_grad(handle, kind, n, V, d, tg, tt, add, pad, offset):
     g = torch.Generator().manual_seed(n + V)

@@ -8,13 +8,14 @@
 // reads n rows and writes V (or the touched ones).
 //
 //   k_em_lookup   a warp per row, 8 elements a lane at a time.
-//   k_em_hist / k_em_scatter   stable radix sort of the tokens with their
-//                 positions, 9 bits a pass (two passes up to 2^18 tokens).
+//   k_em_small    the gradient of up to 1,024 tokens in one kernel.
+//   k_em_hist / k_em_scatter   otherwise a stable radix sort of the tokens with
+//                 their positions, 9 bits a pass (two passes for V < 2^18).
 //   k_em_sum      the sorted positions in chunks of EM_CHUNK: a CTA adds the
 //                 rows of a chunk, a column group per thread, and writes the
 //                 finished tokens; a token that reaches over a chunk's edge
-//                 leaves fp32 partials.
-//   k_em_join     adds such a token's partials in chunk order.
+//                 leaves fp32 partials, which the last of its chunks adds in
+//                 order.  More CTAs zero the rows that no token fell on.
 //
 // The sort is stable and the partials are joined in order, so a sum's order
 // depends on the tokens alone: no floating-point atomics.
@@ -35,9 +36,14 @@ namespace {
 
 constexpr int EM_THREADS = 256;
 constexpr int EM_WARPS = EM_THREADS / 32;
-constexpr int EM_TILE = 2048;       // tokens per CTA of the sort
+constexpr int EM_TILE = 1024;       // tokens that a sorting CTA ranks at a time
 constexpr int EM_BITS = 9;          // most digit bits of a sort pass
+constexpr int EM_SORT_CTAS = 128;   // most CTAs of a sort pass
 constexpr int EM_CHUNK = 32;        // sorted positions per CTA of the sum
+constexpr int EM_UNROLL = 4;        // rows in flight per thread of the sum
+constexpr int EM_ZERO_ROWS = 128;   // table rows per CTA that zeros
+constexpr int EM_SMALL = 1024;      // most tokens of the gradient in one kernel
+constexpr int EM_SMALL_THREADS = 128;
 
 // VEC consecutive elements (1, or 8 that start on 16 bytes) as fp32, and back.
 template <int VEC>
@@ -114,87 +120,142 @@ __global__ void __launch_bounds__(EM_THREADS) k_em_lookup(const TI* __restrict__
     }
 }
 
-// Digit counts of one tile: counts[digit * tiles + tile].  The first pass
-// reads the tokens themselves (kin null).
+// Lanes whose digit equals this lane's (digits of `bits` bits; lanes that are
+// not live match nobody).  A ballot per bit: __match_any_sync takes a round per
+// distinct value, twice as long on spread tokens.
+__device__ __forceinline__ uint32_t em_match(uint32_t digit, int bits, bool live) {
+    uint32_t same = __ballot_sync(0xffffffffu, live);
+    for (int b = 0; b < bits; ++b) {
+        const uint32_t set = __ballot_sync(0xffffffffu, digit >> b & 1u);
+        same &= digit >> b & 1u ? set : ~set;
+    }
+    return same;
+}
+
+// Digit counts of the `per` keys of each CTA: counts[cta * bins + digit].  The
+// first pass reads the tokens themselves (kin null).  Also clears the sum's counters.
 __global__ void __launch_bounds__(EM_THREADS) k_em_hist(const int32_t* __restrict__ tokens,
-                                                        const uint32_t* __restrict__ kin, int32_t n, int32_t V,
-                                                        int32_t shift, int32_t bits, int32_t tiles,
-                                                        int32_t* __restrict__ counts, int32_t* __restrict__ err) {
+                                                        const uint32_t* __restrict__ kin, int32_t n, int32_t per, int32_t V,
+                                                        int32_t shift, int32_t bits, int32_t* __restrict__ counts,
+                                                        int32_t* __restrict__ err, int32_t* __restrict__ arrived, int32_t chunks) {
     __shared__ int32_t h[1 << EM_BITS];
     griddep_wait();
     griddep_launch_dependents();
     const int bins = 1 << bits;
     for (int b = threadIdx.x; b < bins; b += EM_THREADS) h[b] = 0;
+    for (int32_t c = blockIdx.x * EM_THREADS + threadIdx.x; c < chunks; c += gridDim.x * EM_THREADS) arrived[c] = 0;
     __syncthreads();
-    const int64_t i0 = (int64_t)blockIdx.x * EM_TILE;
-#pragma unroll
-    for (int k = 0; k < EM_TILE; k += EM_THREADS) {
-        const int64_t i = i0 + k + threadIdx.x;
-        if (i < n) {
-            const uint32_t key = kin ? kin[i] : em_key(tokens[i], V, err);
-            atomicAdd(&h[(key >> shift) & (bins - 1)], 1);
-        }
+    const int64_t i0 = (int64_t)blockIdx.x * per, i1 = min(i0 + per, (int64_t)n);
+#pragma unroll 4
+    for (int64_t i = i0 + threadIdx.x; i < i1; i += EM_THREADS) {
+        const uint32_t key = kin ? kin[i] : em_key(tokens[i], V, err);
+        atomicAdd(&h[(key >> shift) & (bins - 1)], 1);
     }
     __syncthreads();
-    for (int b = threadIdx.x; b < bins; b += EM_THREADS) counts[(int64_t)b * tiles + blockIdx.x] = h[b];
+    for (int b = threadIdx.x; b < bins; b += EM_THREADS) counts[blockIdx.x * bins + b] = h[b];
 }
 
-// Stable scatter of one tile: each warp takes 256 consecutive keys, 32 at a
-// time, and ranks equal digits by lane order; the warps' digit counts are
-// scanned in warp order.  offs: exclusive prefix of the counts.
+// Stable scatter of each CTA's keys, EM_TILE at a time: a warp takes 128
+// consecutive keys, 32 at a time, and ranks equal digits by lane order; the
+// warps' digit counts are scanned in warp order.  Where a digit begins is
+// summed from all CTAs' counts by every CTA (at most EM_SORT_CTAS x 512 reads),
+// which saves a scan kernel between the two.
 __global__ void __launch_bounds__(EM_THREADS) k_em_scatter(const int32_t* __restrict__ tokens,
                                                            const uint32_t* __restrict__ kin,
-                                                           const int32_t* __restrict__ pin, int32_t n, int32_t V,
-                                                           int32_t shift, int32_t bits, int32_t tiles,
-                                                           const int32_t* __restrict__ offs, uint32_t* __restrict__ kout,
+                                                           const int32_t* __restrict__ pin, int32_t n, int32_t per,
+                                                           int32_t V, int32_t shift, int32_t bits,
+                                                           const int32_t* __restrict__ counts, uint32_t* __restrict__ kout,
                                                            int32_t* __restrict__ pout, int32_t* __restrict__ err) {
-    constexpr int PER = EM_TILE / EM_THREADS;  // keys per lane
+    constexpr int PER = EM_TILE / EM_THREADS;             // keys per lane
+    constexpr int BPT = (1 << EM_BITS) / EM_THREADS;      // digits per thread
     __shared__ int32_t cnt[EM_WARPS][1 << EM_BITS];
     griddep_wait();
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, bins = 1 << bits;
-    for (int b = threadIdx.x; b < EM_WARPS * bins; b += EM_THREADS) cnt[b / bins][b % bins] = 0;
-    __syncthreads();
-    const int64_t i0 = (int64_t)blockIdx.x * EM_TILE + warp * (PER * 32);
-    uint32_t key[PER];
-    int32_t pos[PER], rank[PER];
+    int32_t base[BPT], total = 0;  // of digits threadIdx.x * BPT + k
 #pragma unroll
-    for (int k = 0; k < PER; ++k) {
-        const int64_t i = i0 + k * 32 + lane;
-        key[k] = i < n ? (kin ? kin[i] : em_key(tokens[i], V, err)) : 0u;
-        pos[k] = i < n ? (pin ? pin[i] : (int32_t)i) : 0;
+    for (int k = 0; k < BPT; ++k) {
+        const int b = threadIdx.x * BPT + k;
+        int32_t before = 0, all = 0;
+        if (b < bins) {
+#pragma unroll 8
+            for (int t = 0; t < (int)gridDim.x; ++t) {
+                const int32_t c = counts[t * bins + b];
+                all += c;
+                if (t < (int)blockIdx.x) before += c;
+            }
+        }
+        base[k] = total + before;
+        total += all;
     }
+    int sum;
+    const int32_t first = block_excl_scan(total, &sum);
 #pragma unroll
-    for (int k = 0; k < PER; ++k) {
-        const bool live = i0 + k * 32 + lane < n;
-        const uint32_t dig = live ? (key[k] >> shift) & (bins - 1) : 0xFFFFFFFFu;
-        const uint32_t same = __match_any_sync(0xffffffffu, dig);
-        const int before = __popc(same & ((1u << lane) - 1u));
-        int32_t base = 0;
-        if (live) base = cnt[warp][dig];
-        __syncwarp();
-        if (live && before == 0) cnt[warp][dig] = base + __popc(same);
-        __syncwarp();
-        rank[k] = base + before;
-    }
-    __syncthreads();
-    for (int b = threadIdx.x; b < bins; b += EM_THREADS) {
-        int32_t at = offs[(int64_t)b * tiles + blockIdx.x];
+    for (int k = 0; k < BPT; ++k) base[k] += first;
+    const int64_t end = min((int64_t)blockIdx.x * per + per, (int64_t)n);
+    for (int64_t tile = (int64_t)blockIdx.x * per; tile < end; tile += EM_TILE) {
+        __syncthreads();
+        for (int b = threadIdx.x; b < EM_WARPS * bins; b += EM_THREADS) cnt[b >> bits][b & (bins - 1)] = 0;
+        __syncthreads();
+        const int64_t i0 = tile + warp * (PER * 32);
+        uint32_t key[PER];
+        int32_t pos[PER], rank[PER];
 #pragma unroll
-        for (int w = 0; w < EM_WARPS; ++w) {
-            const int32_t c = cnt[w][b];
-            cnt[w][b] = at;
-            at += c;
+        for (int k = 0; k < PER; ++k) {
+            const int64_t i = i0 + k * 32 + lane;
+            key[k] = i < end ? (kin ? kin[i] : em_key(tokens[i], V, err)) : 0u;
+            pos[k] = i < end ? (pin ? pin[i] : (int32_t)i) : 0;
+        }
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            const bool live = i0 + k * 32 + lane < end;
+            const uint32_t dig = (key[k] >> shift) & (bins - 1);
+            const uint32_t same = em_match(dig, bits, live);
+            const int before = __popc(same & ((1u << lane) - 1u));
+            int32_t at = 0;
+            if (live) at = cnt[warp][dig];
+            __syncwarp();
+            if (live && before == 0) cnt[warp][dig] = at + __popc(same);
+            __syncwarp();
+            rank[k] = at + before;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < BPT; ++k) {
+            const int b = threadIdx.x * BPT + k;
+            if (b < bins) {
+#pragma unroll
+                for (int w = 0; w < EM_WARPS; ++w) {
+                    const int32_t c = cnt[w][b];
+                    cnt[w][b] = base[k];
+                    base[k] += c;
+                }
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            if (i0 + k * 32 + lane < end) {
+                const int32_t o = cnt[warp][(key[k] >> shift) & (bins - 1)] + rank[k];
+                kout[o] = key[k];
+                pout[o] = pos[k];
+            }
         }
     }
-    __syncthreads();
+}
+
+// Zeros the rows of [v0, v1) that `touched` (in shared memory) does not mark.
+template <class TT, int VEC>
+__device__ __forceinline__ void em_zero_rows(TT* table, int64_t ldt, int32_t d, int32_t v0, int32_t v1,
+                                             const uint8_t* touched) {
+    float zero[VEC];
 #pragma unroll
-    for (int k = 0; k < PER; ++k) {
-        if (i0 + k * 32 + lane < n) {
-            const int32_t o = cnt[warp][(key[k] >> shift) & (bins - 1)] + rank[k];
-            kout[o] = key[k];
-            pout[o] = pos[k];
-        }
+    for (int k = 0; k < VEC; ++k) zero[k] = 0.f;
+    for (int32_t v = v0 + (threadIdx.x >> 5); v < v1; v += blockDim.x >> 5) {
+        if (touched[v - v0]) continue;
+        TT* row = table + (int64_t)v * ldt;
+#pragma unroll 4
+        for (int32_t j = (threadIdx.x & 31) * VEC; j < d; j += 32 * VEC) em_store<VEC>(row + j, zero);
     }
 }
 
@@ -208,18 +269,50 @@ __device__ __forceinline__ void em_write(TT* dst, const float (&sum)[VEC], float
     em_store<VEC>(dst, v);
 }
 
+// First sorted position whose key is at least `key`: 32 probes at a time (a whole
+// warp).
+__device__ __forceinline__ int32_t em_lower_bound(const uint32_t* __restrict__ keys, int32_t n, uint32_t key) {
+    const int lane = threadIdx.x & 31;
+    int32_t lo = 0, hi = n;  // the answer lies in [lo, hi]
+    while (hi > lo) {
+        const int32_t step = (hi - lo + 31) / 32;
+        const int64_t at = lo + (int64_t)lane * step;
+        const bool below = at < hi && keys[at] < key;
+        const int c = __popc(__ballot_sync(0xffffffffu, below));  // probes 0 .. c - 1 lie below
+        if (c == 0) return lo;
+        hi = (int32_t)min((int64_t)hi, lo + (int64_t)c * step);
+        lo = lo + (c - 1) * step + 1;
+    }
+    return lo;
+}
+
 // Chunk c holds the sorted positions [c * EM_CHUNK, ...).  Its partials:
 // part[2c] the run that began in an earlier chunk, part[2c + 1] the run that
-// begins here and goes on.
+// begins here and goes on.  The last of a run's chunks to arrive adds its
+// partials in chunk order, so the sum does not depend on which that is.  The
+// CTAs behind the chunks' zero the rows that no token fell on, beside the
+// sums' reads.
 template <class TG, class TT, int VEC>
 __global__ void __launch_bounds__(EM_THREADS)
     k_em_sum(const TG* __restrict__ grad, int64_t ldg, int32_t d, const uint32_t* __restrict__ keys,
              const int32_t* __restrict__ order, int32_t n, int32_t V, float scale, TT* __restrict__ table, int64_t ldt,
-             int32_t accumulate, float* __restrict__ part, int64_t pitch) {
+             int32_t accumulate, float* part, int64_t pitch, int32_t* arrived, int32_t chunks) {
+    __shared__ uint8_t touched[EM_ZERO_ROWS];
     __shared__ uint32_t key_s[EM_CHUNK + 2];  // the chunk's keys between its neighbours'
     __shared__ int32_t ord_s[EM_CHUNK];
+    __shared__ int32_t last_s;
     griddep_wait();
     griddep_launch_dependents();
+    if ((int)blockIdx.x >= chunks) {
+        const int32_t v0 = (blockIdx.x - chunks) * EM_ZERO_ROWS, v1 = min(v0 + EM_ZERO_ROWS, V);
+        for (int k = threadIdx.x; k < EM_ZERO_ROWS; k += EM_THREADS) touched[k] = 0;
+        __syncthreads();
+        const int32_t end = em_lower_bound(keys, n, (uint32_t)v1);
+        for (int32_t i = em_lower_bound(keys, n, (uint32_t)v0) + threadIdx.x; i < end; i += EM_THREADS) touched[keys[i] - v0] = 1;
+        __syncthreads();
+        em_zero_rows<TT, VEC>(table, ldt, d, v0, v1, touched);
+        return;
+    }
     const int64_t i0 = (int64_t)blockIdx.x * EM_CHUNK;
     for (int k = threadIdx.x; k < EM_CHUNK + 2; k += EM_THREADS) {
         const int64_t i = i0 + k - 1;
@@ -227,34 +320,33 @@ __global__ void __launch_bounds__(EM_THREADS)
         if (k >= 1 && k <= EM_CHUNK) ord_s[k - 1] = i < n ? order[i] : 0;
     }
     __syncthreads();
-    const int m = (int)min((int64_t)EM_CHUNK, n - i0);
+    int m = (int)min((int64_t)EM_CHUNK, n - i0);
+    while (m > 0 && key_s[m] >= (uint32_t)V) --m;  // tokens that do not count are sorted last
+    if (m == 0) return;
+    const bool head = key_s[0] == key_s[1], tail = key_s[m + 1] == key_s[m];
     for (int32_t j = threadIdx.x * VEC; j < d; j += EM_THREADS * VEC) {
         float sum[VEC];
 #pragma unroll
         for (int q = 0; q < VEC; ++q) sum[q] = 0.f;
-        bool from_before = key_s[0] == key_s[1];
-        for (int k0 = 0; k0 < m; k0 += 4) {
-            float v[4][VEC];
+        bool from_before = head;
+        for (int k0 = 0; k0 < m; k0 += EM_UNROLL) {
+            float v[EM_UNROLL][VEC];
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-                if (k0 + u < m && key_s[k0 + u + 1] < (uint32_t)V)
-                    em_load<VEC>(grad + (int64_t)ord_s[k0 + u] * ldg + j, v[u]);
+            for (int u = 0; u < EM_UNROLL; ++u)
+                if (k0 + u < m) em_load<VEC>(grad + (int64_t)ord_s[k0 + u] * ldg + j, v[u]);
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
+            for (int u = 0; u < EM_UNROLL; ++u) {
                 const int k = k0 + u;
                 if (k >= m) break;
                 const uint32_t key = key_s[k + 1];
-                if (key >= (uint32_t)V) break;  // tokens that do not count are sorted last
 #pragma unroll
                 for (int q = 0; q < VEC; ++q) sum[q] += v[u][q];
                 const bool ends = key_s[k + 2] != key;
                 if (ends || k == m - 1) {
-                    if (ends && !from_before) {
+                    if (ends && !from_before)
                         em_write<TT, VEC>(table + (int64_t)key * ldt + j, sum, scale, accumulate != 0);
-                    } else {
-                        float* o = part + (2 * (int64_t)blockIdx.x + (from_before ? 0 : 1)) * pitch + j;
-                        em_store<VEC>(o, sum);
-                    }
+                    else
+                        em_store<VEC>(part + (2 * (int64_t)blockIdx.x + (from_before ? 0 : 1)) * pitch + j, sum);
                     from_before = false;
 #pragma unroll
                     for (int q = 0; q < VEC; ++q) sum[q] = 0.f;
@@ -262,33 +354,109 @@ __global__ void __launch_bounds__(EM_THREADS)
             }
         }
     }
+    // the runs that reach over this chunk's edges: the first key's and, unless
+    // it is the same run, the last key's
+    const bool one = head && tail && key_s[1] == key_s[m];
+    for (int r = 0; r < 2; ++r) {
+        if (!(r == 0 ? head : tail && !one)) continue;
+        const uint32_t key = r == 0 ? key_s[1] : key_s[m];
+        const int64_t c = em_lower_bound(keys, n, key) / EM_CHUNK, e = (em_lower_bound(keys, n, key + 1) - 1) / EM_CHUNK;
+        __threadfence();
+        __syncthreads();
+        if (threadIdx.x == 0) last_s = atomicAdd(&arrived[c], 1) == (int32_t)(e - c);
+        __syncthreads();
+        if (!last_s) continue;
+        __threadfence();
+        for (int32_t j = threadIdx.x * VEC; j < d; j += EM_THREADS * VEC) {
+            float sum[VEC];
+            em_load<VEC>(part + (2 * c + 1) * pitch + j, sum);
+#pragma unroll 4
+            for (int64_t k = c + 1; k <= e; ++k) {
+                float v[VEC];
+                em_load<VEC>(part + 2 * k * pitch + j, v);
+#pragma unroll
+                for (int q = 0; q < VEC; ++q) sum[q] += v[q];
+            }
+            em_write<TT, VEC>(table + (int64_t)key * ldt + j, sum, scale, accumulate != 0);
+        }
+    }
 }
 
-// The run that begins in chunk c and goes on: its partials in chunk order.
-template <class TT, int VEC>
-__global__ void __launch_bounds__(EM_THREADS)
-    k_em_join(const uint32_t* __restrict__ keys, int32_t n, int32_t V, int32_t d, float scale, TT* __restrict__ table,
-              int64_t ldt, int32_t accumulate, const float* __restrict__ part, int64_t pitch) {
+// The whole gradient of at most EM_SMALL tokens in one kernel, without a sort:
+// CTA (i, column block) compares token i with all tokens; the first occurrence
+// of a token adds its rows in order, four warps a quarter of the list each (32
+// * VEC columns), joined in warp order.  The CTAs behind those zero the rows
+// that no token fell on.  Bound by latency: reading 1,024 tokens per CTA costs
+// less than the sort's six launches.
+template <class TG, class TT, int VEC>
+__global__ void __launch_bounds__(EM_SMALL_THREADS)
+    k_em_small(const TG* __restrict__ grad, int64_t ldg, int32_t d, const int32_t* __restrict__ tokens, int32_t n, int32_t V,
+               float scale, TT* __restrict__ table, int64_t ldt, int32_t accumulate, int32_t blocks,
+               int32_t* __restrict__ err) {
+    constexpr int WARPS = EM_SMALL_THREADS / 32, ROUNDS = EM_SMALL / EM_SMALL_THREADS;
+    __shared__ uint8_t touched[EM_ZERO_ROWS];
+    __shared__ uint16_t list[EM_SMALL];
+    __shared__ int32_t cnt[ROUNDS][WARPS];
+    __shared__ float sums[WARPS][32 * VEC];
     griddep_wait();
     griddep_launch_dependents();
-    const int64_t c = blockIdx.x, last = c * EM_CHUNK + EM_CHUNK - 1;
-    if (last + 1 >= n) return;
-    const uint32_t key = keys[last];
-    if (key >= (uint32_t)V || keys[last + 1] != key) return;
-    if (c > 0 && keys[c * EM_CHUNK - 1] == key) return;  // begins in an earlier chunk
-    // the last chunk that the run reaches
-    int64_t e = c + 1;
-    while ((e + 1) * EM_CHUNK < n && keys[(e + 1) * EM_CHUNK] == key) ++e;
-    for (int32_t j = threadIdx.x * VEC; j < d; j += EM_THREADS * VEC) {
-        float sum[VEC];
-        em_load<VEC>(part + (2 * c + 1) * pitch + j, sum);
-        for (int64_t k = c + 1; k <= e; ++k) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if ((int)blockIdx.x >= n * blocks) {
+        const int32_t v0 = (blockIdx.x - n * blocks) * EM_ZERO_ROWS, v1 = min(v0 + EM_ZERO_ROWS, V);
+        for (int k = threadIdx.x; k < EM_ZERO_ROWS; k += EM_SMALL_THREADS) touched[k] = 0;
+        __syncthreads();
+        for (int i = threadIdx.x; i < n; i += EM_SMALL_THREADS) {
+            const int32_t t = tokens[i];
+            if (t >= v0 && t < v1) touched[t - v0] = 1;
+        }
+        __syncthreads();
+        em_zero_rows<TT, VEC>(table, ldt, d, v0, v1, touched);
+        return;
+    }
+    const int i = blockIdx.x / blocks, j = (blockIdx.x % blocks) * 32 * VEC + lane * VEC;
+    const uint32_t t = em_key(tokens[i], V, err);
+    if (t >= (uint32_t)V) return;
+    uint32_t hit[ROUNDS];
+    bool earlier = false;
+#pragma unroll
+    for (int r = 0; r < ROUNDS; ++r) {
+        const int k = r * EM_SMALL_THREADS + threadIdx.x;
+        const bool same = k < n && (uint32_t)tokens[k] == t;
+        earlier |= same && k < i;
+        hit[r] = __ballot_sync(0xffffffffu, same);
+        if (lane == 0) cnt[r][warp] = __popc(hit[r]);
+    }
+    if (__syncthreads_or(earlier)) return;
+    int m = 0;
+    for (int r = 0; r < ROUNDS; ++r)
+        for (int w = 0; w < WARPS; ++w) {
+            if (w == warp && (hit[r] >> lane & 1u))
+                list[m + __popc(hit[r] & ((1u << lane) - 1u))] = (uint16_t)(r * EM_SMALL_THREADS + threadIdx.x);
+            m += cnt[r][w];
+        }
+    __syncthreads();
+    float sum[VEC];
+#pragma unroll
+    for (int q = 0; q < VEC; ++q) sum[q] = 0.f;
+    const int k0 = m * warp / WARPS, k1 = m * (warp + 1) / WARPS;
+    if (j < d) {
+#pragma unroll 4
+        for (int k = k0; k < k1; ++k) {
             float v[VEC];
-            em_load<VEC>(part + 2 * k * pitch + j, v);
+            em_load<VEC>(grad + (int64_t)list[k] * ldg + j, v);
 #pragma unroll
             for (int q = 0; q < VEC; ++q) sum[q] += v[q];
         }
-        em_write<TT, VEC>(table + (int64_t)key * ldt + j, sum, scale, accumulate != 0);
+    }
+#pragma unroll
+    for (int q = 0; q < VEC; ++q) sums[warp][q * 32 + lane] = sum[q];
+    __syncthreads();
+    if (warp == 0 && j < d) {
+#pragma unroll
+        for (int w = 1; w < WARPS; ++w)
+#pragma unroll
+            for (int q = 0; q < VEC; ++q) sum[q] += sums[w][q * 32 + lane];
+        em_write<TT, VEC>(table + (int64_t)t * ldt + j, sum, scale, accumulate != 0);
     }
 }
 
@@ -300,8 +468,8 @@ struct fr_embed {
     uint32_t* keys[2] = {};
     int32_t* pos[2] = {};
     int32_t* counts = nullptr;
-    int32_t* temp = nullptr;
-    float* part = nullptr;  // [2 * chunks, pitch]
+    float* part = nullptr;       // [2 * chunks, pitch]
+    int32_t* arrived = nullptr;  // [chunks] chunks of a run that have arrived, at its first chunk
     int64_t pitch = 0;
     int32_t* err = nullptr;
     cudaStream_t last_stream = nullptr;
@@ -342,18 +510,54 @@ cudaError_t em_lookup(fr_embed* h, const void* table, int64_t ldt, const int32_t
                           scale, (TO*)out, ldo, h->err);
 }
 
-template <class TG, class TT>
-cudaError_t em_sum(fr_embed* h, const void* grad, int64_t ldg, const uint32_t* keys, const int32_t* order, int32_t n,
-                   float scale, void* table, int64_t ldt, int32_t accumulate, cudaStream_t s) {
-    const bool vec = em_vec(grad, ldg, sizeof(TG), h->d) && em_vec(table, ldt, sizeof(TT), h->d);
-    const int64_t chunks = em_ceil(n, fr::EM_CHUNK);
-    auto ks = vec ? fr::k_em_sum<TG, TT, 8> : fr::k_em_sum<TG, TT, 1>;
-    cudaError_t e = fr::launch_pdl(ks, chunks, fr::EM_THREADS, 0, s, (const TG*)grad, ldg, h->d, keys, order, n, h->V, scale,
-                                   (TT*)table, ldt, accumulate, h->part, h->pitch);
+// The keys run over [0, V]: V stands for tokens that do not count.
+cudaError_t em_sort(fr_embed* h, const int32_t* tokens, int32_t n, const uint32_t** keys, const int32_t** order,
+                    cudaStream_t s) {
+    int total_bits = 1;
+    while (total_bits < 32 && ((uint64_t)h->V >> total_bits) != 0) ++total_bits;
+    const int passes = (total_bits + fr::EM_BITS - 1) / fr::EM_BITS, bits = (total_bits + passes - 1) / passes;
+    const int32_t per = (int32_t)(em_ceil(em_ceil(n, fr::EM_SORT_CTAS), fr::EM_TILE) * fr::EM_TILE);
+    const int64_t ctas = em_ceil(n, per);
+    for (int p = 0; p < passes; ++p) {
+        const uint32_t* kin = p ? h->keys[(p - 1) & 1] : nullptr;
+        const int32_t* pin = p ? h->pos[(p - 1) & 1] : nullptr;
+        cudaError_t e = fr::launch_pdl(fr::k_em_hist, ctas, fr::EM_THREADS, 0, s, tokens, kin, n, per, h->V, p * bits, bits,
+                                       h->counts, h->err, h->arrived, p ? 0 : (int32_t)em_ceil(n, fr::EM_CHUNK));
+        if (e != cudaSuccess) return e;
+        e = fr::launch_pdl(fr::k_em_scatter, ctas, fr::EM_THREADS, 0, s, tokens, kin, pin, n, per, h->V, p * bits, bits,
+                           (const int32_t*)h->counts, h->keys[p & 1], h->pos[p & 1], h->err);
+        if (e != cudaSuccess) return e;
+    }
+    *keys = h->keys[(passes - 1) & 1];
+    *order = h->pos[(passes - 1) & 1];
+    return cudaSuccess;
+}
+
+template <class TG, class TT, int VEC>
+cudaError_t em_grad(fr_embed* h, const void* grad, int64_t ldg, const int32_t* tokens, int32_t n, float scale, void* table,
+                    int64_t ldt, int32_t accumulate, cudaStream_t s) {
+    const int32_t blocks = (int32_t)em_ceil(h->d, 32 * VEC);
+    const int64_t zeros = accumulate ? 0 : em_ceil(h->V, fr::EM_ZERO_ROWS);
+    if (n <= fr::EM_SMALL && (int64_t)n * blocks < (1 << 30)) {
+        if (n * (int64_t)blocks + zeros == 0) return cudaSuccess;
+        return fr::launch_pdl(fr::k_em_small<TG, TT, VEC>, n * (int64_t)blocks + zeros, fr::EM_SMALL_THREADS, 0, s,
+                              (const TG*)grad, ldg, h->d, tokens, n, h->V, scale, (TT*)table, ldt, accumulate, blocks, h->err);
+    }
+    const uint32_t* keys;
+    const int32_t* order;
+    cudaError_t e = em_sort(h, tokens, n, &keys, &order, s);
     if (e != cudaSuccess) return e;
-    auto kj = vec ? fr::k_em_join<TT, 8> : fr::k_em_join<TT, 1>;
-    return fr::launch_pdl(kj, chunks, fr::EM_THREADS, 0, s, keys, n, h->V, h->d, scale, (TT*)table, ldt, accumulate,
-                          (const float*)h->part, h->pitch);
+    const int64_t chunks = em_ceil(n, fr::EM_CHUNK);
+    return fr::launch_pdl(fr::k_em_sum<TG, TT, VEC>, chunks + zeros, fr::EM_THREADS, 0, s, (const TG*)grad, ldg, h->d, keys,
+                          order, n, h->V, scale, (TT*)table, ldt, accumulate, h->part, h->pitch, h->arrived, (int32_t)chunks);
+}
+
+template <class TG, class TT>
+cudaError_t em_grad_any(fr_embed* h, const void* grad, int64_t ldg, const int32_t* tokens, int32_t n, float scale,
+                        void* table, int64_t ldt, int32_t accumulate, cudaStream_t s) {
+    const bool vec = em_vec(grad, ldg, sizeof(TG), h->d) && em_vec(table, ldt, sizeof(TT), h->d);
+    return vec ? em_grad<TG, TT, 8>(h, grad, ldg, tokens, n, scale, table, ldt, accumulate, s)
+               : em_grad<TG, TT, 1>(h, grad, ldg, tokens, n, scale, table, ldt, accumulate, s);
 }
 
 }  // namespace
@@ -373,9 +577,9 @@ extern "C" fr_status fr_embed_init(int32_t V, int32_t d, int32_t max_tokens, fr_
         delete h;
         return FR_ERR_CUDA;
     }
-    const int64_t n = max_tokens, cells = (int64_t)em_ceil(n, fr::EM_TILE) << fr::EM_BITS;
+    const int64_t n = max_tokens;
     cudaError_t e = cudaMalloc(&h->keys[0], n * 16);
-    if (e == cudaSuccess) e = cudaMalloc(&h->counts, (cells + fr::scan_temp_elems(cells)) * 4);
+    if (e == cudaSuccess) e = cudaMalloc(&h->counts, ((fr::EM_SORT_CTAS << fr::EM_BITS) + em_ceil(n, fr::EM_CHUNK)) * sizeof(int32_t));
     if (e == cudaSuccess) e = cudaMalloc(&h->part, (size_t)em_ceil(n, fr::EM_CHUNK) * 2 * h->pitch * 4);
     if (e == cudaSuccess) e = cudaMalloc(&h->err, sizeof(int32_t));
     if (e == cudaSuccess) e = cudaMemset(h->err, 0, sizeof(int32_t));
@@ -387,7 +591,7 @@ extern "C" fr_status fr_embed_init(int32_t V, int32_t d, int32_t max_tokens, fr_
     h->keys[1] = h->keys[0] + n;
     h->pos[0] = reinterpret_cast<int32_t*>(h->keys[1] + n);
     h->pos[1] = h->pos[0] + n;
-    h->temp = h->counts + cells;
+    h->arrived = h->counts + (fr::EM_SORT_CTAS << fr::EM_BITS);
     *out = h;
     return FR_OK;
 }
@@ -422,37 +626,10 @@ extern "C" fr_status fr_embed_grad(fr_embed* h, const void* grad_out_dev, int64_
         return FR_ERR_INVALID_ARG;
     const cudaStream_t s = (cudaStream_t)stream;
     h->last_stream = s;
-    const size_t tsize = table_dtype == FR_F32 ? 4 : 2;
-    if (!accumulate)
-        FR_CUDA_TRY(cudaMemset2DAsync(grad_table_dev, ldt * tsize, 0, h->d * tsize, h->V, s));
-    if (n == 0) return FR_OK;
-    // keys run over [0, V]: V stands for tokens that do not count
-    int total_bits = 1;
-    while (total_bits < 32 && ((uint64_t)h->V >> total_bits) != 0) ++total_bits;
-    const int passes = (total_bits + fr::EM_BITS - 1) / fr::EM_BITS, bits = (total_bits + passes - 1) / passes;
-    const int32_t tiles = (int32_t)em_ceil(n, fr::EM_TILE);
-    for (int p = 0; p < passes; ++p) {
-        const uint32_t* kin = p ? h->keys[(p - 1) & 1] : nullptr;
-        const int32_t* pin = p ? h->pos[(p - 1) & 1] : nullptr;
-        FR_CUDA_TRY(fr::launch_pdl(fr::k_em_hist, tiles, fr::EM_THREADS, 0, s, tokens_dev, kin, n, h->V, p * bits, bits, tiles,
-                                   h->counts, h->err));
-        FR_CUDA_TRY(fr::scan_exclusive_i32(h->counts, h->counts, (int64_t)tiles << bits, h->temp, nullptr, s));
-        FR_CUDA_TRY(fr::launch_pdl(fr::k_em_scatter, tiles, fr::EM_THREADS, 0, s, tokens_dev, kin, pin, n, h->V, p * bits,
-                                   bits, tiles, (const int32_t*)h->counts, h->keys[p & 1], h->pos[p & 1], h->err));
-    }
-    const uint32_t* keys = h->keys[(passes - 1) & 1];
-    const int32_t* order = h->pos[(passes - 1) & 1];
-    cudaError_t e;
-    if (grad_dtype == FR_F32)
-        e = table_dtype == FR_F32
-                ? em_sum<float, float>(h, grad_out_dev, ldg, keys, order, n, scale, grad_table_dev, ldt, accumulate, s)
-                : em_sum<float, __nv_bfloat16>(h, grad_out_dev, ldg, keys, order, n, scale, grad_table_dev, ldt, accumulate, s);
-    else
-        e = table_dtype == FR_F32
-                ? em_sum<__nv_bfloat16, float>(h, grad_out_dev, ldg, keys, order, n, scale, grad_table_dev, ldt, accumulate, s)
-                : em_sum<__nv_bfloat16, __nv_bfloat16>(h, grad_out_dev, ldg, keys, order, n, scale, grad_table_dev, ldt,
-                                                       accumulate, s);
-    FR_CUDA_TRY(e);
+    auto run = grad_dtype == FR_F32 ? (table_dtype == FR_F32 ? em_grad_any<float, float> : em_grad_any<float, __nv_bfloat16>)
+                                    : (table_dtype == FR_F32 ? em_grad_any<__nv_bfloat16, float>
+                                                             : em_grad_any<__nv_bfloat16, __nv_bfloat16>);
+    FR_CUDA_TRY(run(h, grad_out_dev, ldg, tokens_dev, n, scale, grad_table_dev, ldt, accumulate, s));
     return FR_OK;
 }
 

@@ -141,8 +141,8 @@ def _check(status: int, what: str) -> None:
 
 
 def _stream(stream) -> Optional[int]:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the current stream's handle, without building a Stream object (a microsecond and a half)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -456,36 +456,34 @@ def fr_lmhead_destroy(lmhead) -> None:
 
 
 def _on_current_device(*tensors: Optional[torch.Tensor]) -> None:
-    here = None
+    here = torch.cuda.current_device()
     for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("expected a CUDA tensor")
-        if here is None:
-            here = torch.cuda.current_device()
-        if t.device.index != here:
+        if t is not None and t.get_device() != here:
+            if not t.is_cuda:
+                raise ValueError("expected a CUDA tensor")
             raise ValueError("every tensor must be on the current CUDA device (%d)" % here)
 
 
 def _matrix(t: torch.Tensor, what: str, dtypes, rows: Optional[int], cols: int) -> int:
     """Checks a [rows, cols] tensor with unit column stride; returns its row
     pitch in elements."""
-    if t.dtype not in dtypes or t.dim() != 2 or t.shape[1] != cols or (rows is not None and t.shape[0] != rows):
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != cols or (rows is not None and shape[0] != rows) or t.dtype not in dtypes:
         raise ValueError("%s must be a [%s, %d] tensor of %s"
                          % (what, "rows" if rows is None else rows, cols, " or ".join(map(str, dtypes))))
+    pitch, unit = t.stride()
     # the strides of an axis of one or no element say nothing
-    if cols > 1 and t.shape[0] > 0 and t.stride(1) != 1:
+    if unit != 1 and cols > 1 and shape[0] > 0:
         raise ValueError("%s must have unit column stride" % what)
-    if t.shape[0] <= 1:
-        return max(cols, t.stride(0))
-    if t.stride(0) < cols:
+    if shape[0] <= 1:
+        return max(cols, pitch)
+    if pitch < cols:
         raise ValueError("%s has overlapping rows" % what)
-    return t.stride(0)
+    return pitch
 
 
 def _vector(t: torch.Tensor, what: str, dtype, n: int) -> None:
-    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != (n,) or not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s [%d] tensor" % (what, dtype, n))
 
 
@@ -497,7 +495,7 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return t.data_ptr() or 256
 
 
-_FLOATS = (torch.float32, torch.bfloat16)
+_FLOATS = {torch.float32: FR_F32, torch.bfloat16: FR_BF16}
 
 
 def fr_embed_init(V: int, d: int, max_tokens: int) -> ctypes.c_void_p:
@@ -516,8 +514,8 @@ def fr_embed_lookup(embed, table: torch.Tensor, tokens: torch.Tensor, out: torch
     _vector(tokens, "tokens", torch.int32, n)
     ldt = _matrix(table, "table", _FLOATS, embed.V, embed.d)
     ldo = _matrix(out, "out", _FLOATS, n, embed.d)
-    _check(libfr().fr_embed_lookup(embed, _ptr(table), ldt, _dtype_code(table.dtype), _ptr(tokens), n, float(scale),
-                                   _ptr(out), ldo, _dtype_code(out.dtype), _stream(stream)), "fr_embed_lookup")
+    _check(libfr().fr_embed_lookup(embed, _ptr(table), ldt, _FLOATS[table.dtype], _ptr(tokens), n, float(scale),
+                                   _ptr(out), ldo, _FLOATS[out.dtype], _stream(stream)), "fr_embed_lookup")
 
 
 def fr_embed_grad(embed, grad_out: torch.Tensor, tokens: torch.Tensor, grad_table: torch.Tensor, scale: float = 1.0,
@@ -528,8 +526,8 @@ def fr_embed_grad(embed, grad_out: torch.Tensor, tokens: torch.Tensor, grad_tabl
     _vector(tokens, "tokens", torch.int32, n)
     ldg = _matrix(grad_out, "grad_out", _FLOATS, n, embed.d)
     ldt = _matrix(grad_table, "grad_table", _FLOATS, embed.V, embed.d)
-    _check(libfr().fr_embed_grad(embed, _ptr(grad_out), ldg, _dtype_code(grad_out.dtype), _ptr(tokens), n, float(scale),
-                                 _ptr(grad_table), ldt, _dtype_code(grad_table.dtype), int(bool(accumulate)),
+    _check(libfr().fr_embed_grad(embed, _ptr(grad_out), ldg, _FLOATS[grad_out.dtype], _ptr(tokens), n, float(scale),
+                                 _ptr(grad_table), ldt, _FLOATS[grad_table.dtype], int(bool(accumulate)),
                                  _stream(stream)), "fr_embed_grad")
 
 
@@ -617,7 +615,7 @@ def fr_i8_quantize(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, stream
     ldx = _matrix(x, "x", _FLOATS, rows, d)
     ldq = _matrix(q, "q", (torch.int8,), rows, d)
     _vector(scale, "scale", torch.float32, rows)
-    _check(libfr().fr_i8_quantize(_ptr(x), ldx, _dtype_code(x.dtype), rows, d, _ptr(q), ldq, _ptr(scale),
+    _check(libfr().fr_i8_quantize(_ptr(x), ldx, _FLOATS[x.dtype], rows, d, _ptr(q), ldq, _ptr(scale),
                                   _stream(stream)), "fr_i8_quantize")
 
 
@@ -654,7 +652,7 @@ def fr_i8_matmul(i8, xq: torch.Tensor, xscale: torch.Tensor, out: torch.Tensor, 
     _on_current_device(xq, xscale, out)
     rows, ldx = _i8_inputs(i8, xq, xscale)
     ldo = _matrix(out, "out", _FLOATS, rows, i8.N)
-    _check(libfr().fr_i8_matmul(i8, _ptr(xq), ldx, _ptr(xscale), rows, _ptr(out), ldo, _dtype_code(out.dtype),
+    _check(libfr().fr_i8_matmul(i8, _ptr(xq), ldx, _ptr(xscale), rows, _ptr(out), ldo, _FLOATS[out.dtype],
                                 _stream(stream)), "fr_i8_matmul")
 
 
