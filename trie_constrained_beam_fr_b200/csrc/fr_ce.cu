@@ -68,40 +68,47 @@ struct CeRows {
 
 __device__ __forceinline__ int32_t ce_m_tiles(int32_t n) { return max((n + GM_TILE - 1) / GM_TILE, 1); }
 
-// A CTA packs 64 consecutive rows: it counts the counted rows before its own
-// (reading the targets up to there), so no CTA waits for another.
-constexpr int CE_GATHER_ROWS = 64;
+// A CTA packs CE_GATHER_ROWS consecutive rows.  Each counts the counted rows
+// before its own and in all by reading every target, so no CTA waits for
+// another and the rows of padding are shared out.
+constexpr int CE_GATHER_ROWS = 16;
 constexpr int CE_GATHER_THREADS = 256;
+constexpr int CE_GATHER_CTAS = 32;  // at least: they share the padding
 __global__ void __launch_bounds__(CE_GATHER_THREADS)
     k_ce_gather(const __nv_bfloat16* __restrict__ hidden, int64_t ldh, const int32_t* __restrict__ targets,
                 const float* __restrict__ lse, const float* __restrict__ grad_loss, int32_t rows, int32_t V, int32_t d,
                 CeRows out, float* __restrict__ loss_out, float* __restrict__ lse_out,
-                __nv_bfloat16* __restrict__ grad_hidden, int64_t ldgh, int32_t* __restrict__ err) {
-    __shared__ int32_t before_s, pos_s[CE_GATHER_ROWS], total_s;
+                __nv_bfloat16* __restrict__ grad_hidden, int64_t ldgh, int32_t* __restrict__ counters, int32_t n_counters,
+                int32_t* __restrict__ err) {
+    __shared__ int32_t before_s, total_s, pos_s[CE_GATHER_ROWS];
     __shared__ uint32_t gmax_s;
     griddep_wait();
     griddep_launch_dependents();
-    const int32_t r0 = blockIdx.x * CE_GATHER_ROWS, tid = threadIdx.x;
-    if (tid == 0) before_s = 0, gmax_s = 0u;
+    const int32_t r0 = blockIdx.x * CE_GATHER_ROWS, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) before_s = 0, total_s = 0, gmax_s = 0u;
     __syncthreads();
-    int32_t c = 0;
-#pragma unroll 4
-    for (int32_t i = tid; i < r0; i += CE_GATHER_THREADS) {
-        const int32_t t = targets[i];
-        c += t >= 0 && t < V;
+    int32_t before = 0, total = 0;
+#pragma unroll 8
+    for (int32_t i = tid; i < rows; i += CE_GATHER_THREADS) {
+        const int32_t live = (uint32_t)targets[i] < (uint32_t)V;
+        total += live;
+        before += i < r0 ? live : 0;
     }
-    c = __reduce_add_sync(0xffffffffu, c);
-    if ((tid & 31) == 0 && c) atomicAdd(&before_s, c);
+    before = __reduce_add_sync(0xffffffffu, before);
+    total = __reduce_add_sync(0xffffffffu, total);
+    if (lane == 0) {
+        atomicAdd(&before_s, before);
+        atomicAdd(&total_s, total);
+    }
     __syncthreads();
-    if (tid < 32) {
-        int32_t at = before_s;
-        for (int k = 0; k < CE_GATHER_ROWS; k += 32) {
-            const int32_t r = r0 + k + tid;
-            const int32_t t = r < rows ? targets[r] : -1;
-            const bool live = t >= 0 && t < V;
-            const uint32_t m = __ballot_sync(0xffffffffu, live);
-            const int32_t pos = at + __popc(m & ((1u << tid) - 1u));
-            pos_s[k + tid] = live ? pos : -1;
+    if (warp == 0) {
+        const int32_t r = r0 + lane;
+        const int32_t t = lane < CE_GATHER_ROWS && r < rows ? targets[r] : -1;
+        const bool live = (uint32_t)t < (uint32_t)V;
+        const uint32_t m = __ballot_sync(0xffffffffu, live);
+        const int32_t pos = before_s + __popc(m & ((1u << lane) - 1u));
+        if (lane < CE_GATHER_ROWS) {
+            pos_s[lane] = live ? pos : -1;
             if (live) {
                 out.tgt[pos] = t;
                 out.idx[pos] = r;
@@ -117,52 +124,49 @@ __global__ void __launch_bounds__(CE_GATHER_THREADS)
                     lse_out[r] = bad ? NAN : 0.f;
                 }
             }
-            at += __popc(m);
         }
-        if (tid == 0) total_s = at;
     }
     __syncthreads();
-    const bool hvec = (d & 7) == 0;  // rows start on 16 bytes (checked by the caller)
-    const int32_t vecs = d >> 3;
-    for (int k = tid >> 5; k < CE_GATHER_ROWS; k += CE_GATHER_THREADS / 32) {
-        const int32_t r = r0 + k, lane = tid & 31;
-        if (r >= rows) break;
-        const int32_t pos = pos_s[k];
+    const int32_t vecs = d >> 3;  // rows start on 16 bytes (checked by the caller)
+    for (int k = warp; k < CE_GATHER_ROWS && r0 + k < rows; k += CE_GATHER_THREADS / 32) {
+        const int32_t r = r0 + k, pos = pos_s[k];
         if (pos >= 0) {
             const uint4* src = reinterpret_cast<const uint4*>(hidden + r * ldh);
             uint4* dst = reinterpret_cast<uint4*>(out.h + pos * out.pitch);
-#pragma unroll 4
+#pragma unroll 8
             for (int32_t i = lane; i < vecs; i += 32) dst[i] = src[i];
-            if (!hvec)
-                for (int32_t j = (vecs << 3) + lane; j < d; j += 32) out.h[pos * out.pitch + j] = hidden[r * ldh + j];
+            for (int32_t j = (vecs << 3) + lane; j < d; j += 32) out.h[pos * out.pitch + j] = hidden[r * ldh + j];
         } else if (grad_hidden) {
             for (int32_t j = lane; j < d; j += 32) grad_hidden[r * ldgh + j] = __float2bfloat16_rn(0.f);
         }
     }
-    if (blockIdx.x == gridDim.x - 1) {
-        const int32_t n = total_s, end = ce_m_tiles(n) * GM_TILE;
-        for (int32_t r = n + (tid >> 5); r < end; r += CE_GATHER_THREADS / 32)
-            for (int32_t j = tid & 31; j < out.pitch; j += 32) out.h[r * out.pitch + j] = __float2bfloat16_rn(0.f);
+    // zero rows up to the next whole tile (the pitch is a multiple of 8 elements)
+    const int32_t n = total_s, end = ce_m_tiles(n) * GM_TILE;
+    for (int32_t r = n + blockIdx.x; r < end; r += gridDim.x) {
+        uint4* dst = reinterpret_cast<uint4*>(out.h + r * out.pitch);
+        for (int32_t i = tid; i < out.pitch / 8; i += CE_GATHER_THREADS) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    if (blockIdx.x == 0) {
         if (tid == 0) *out.n = n;
-        if (lse) {
-            float m = 0.f;
-#pragma unroll 4
-            for (int32_t i = tid; i < rows; i += CE_GATHER_THREADS) {
-                const int32_t t = targets[i];
-                const float g = fabsf(grad_loss[i]);
-                if (t >= 0 && t < V && g < INFINITY) m = fmaxf(m, g);
-            }
-            // non-negative floats order as their bits
-            const uint32_t w = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
-            if ((tid & 31) == 0) atomicMax(&gmax_s, w);
-            __syncthreads();
-            if (tid == 0) *out.gmax = __uint_as_float(gmax_s);
+        for (int32_t i = tid; i < n_counters; i += CE_GATHER_THREADS) counters[i] = 0;
+    }
+    if (lse && blockIdx.x == gridDim.x - 1) {
+        float m = 0.f;
+#pragma unroll 8
+        for (int32_t i = tid; i < rows; i += CE_GATHER_THREADS) {
+            const float g = fabsf(grad_loss[i]);
+            if ((uint32_t)targets[i] < (uint32_t)V && g < INFINITY) m = fmaxf(m, g);
         }
+        // non-negative floats order as their bits
+        const uint32_t w = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+        if (lane == 0) atomicMax(&gmax_s, w);
+        __syncthreads();
+        if (tid == 0) *out.gmax = __uint_as_float(gmax_s);
     }
 }
 
 struct CeLoss {
-    static constexpr bool I8 = false, STAGED = false;
+    static constexpr bool I8 = false, STAGED = false, DYNAMIC = false;
     static constexpr int STAGES = 7;
     struct Tile {
         int nk, m0, n0;
@@ -181,11 +185,13 @@ struct CeLoss {
         const int32_t n = *rows.n;
         return {n, n ? ce_m_tiles(n) : 0};
     }
-    __device__ __forceinline__ bool tile(const State& st, int64_t pair, int64_t pairs, int i, Tile& t) const {
-        const int64_t g = pair + i * pairs;
+    __device__ __forceinline__ int32_t* counter() const { return nullptr; }
+    __device__ __forceinline__ bool tile(const State& st, int64_t g, Tile& t) const {
         if (g >= (int64_t)st.m_tiles * n_tiles) return false;
-        t.m0 = (int)(g % st.m_tiles) * GM_TILE;
-        t.n0 = (int)(g / st.m_tiles) * GM_TILE;
+        int32_t m, n;
+        gm_grouped(g, st.m_tiles, n_tiles, m, n);
+        t.m0 = m * GM_TILE;
+        t.n0 = n * GM_TILE;
         t.nk = k_blocks;
         t.idesc = gm_idesc(false);
         return true;
@@ -247,7 +253,7 @@ __global__ void __launch_bounds__(256) k_ce_combine(const float2* __restrict__ p
 // G in buffer `buf`) and the G tiles of the next (tokens [w0, w1), buffer
 // buf ^ 1).  Empty ranges leave their part out.
 struct CeGrad {
-    static constexpr bool I8 = false, STAGED = true;
+    static constexpr bool I8 = false, STAGED = true, DYNAMIC = true;
     static constexpr int STAGES = 6;
     enum { DH, DW, GT };
     struct Tile {
@@ -255,7 +261,8 @@ struct CeGrad {
         uint32_t idesc;
     };
     struct State {
-        int32_t n, m_tiles, dh_tiles, dw_tiles, g_tiles, extra, dw_nk;
+        int32_t n, m_tiles, dh_tiles, dw_tiles, g_tiles, dw_nk, dh_per;
+        bool dw_first;
         float gmax, ginv;
     };
     CUtensorMap map_h_k, map_h_mn;   // packed rows: K-major (128 x 64) and MN-major (64 x 64) boxes
@@ -264,6 +271,7 @@ struct CeGrad {
     CUtensorMap map_g_out;           // G of the piece whose tiles are computed: 32 x 64 boxes
     CUtensorMap map_dw;              // the caller's dW, where its rows start on 16 bytes: 32 x 64 boxes
     CeRows rows;
+    int32_t* next_tile;              // tiles taken so far beyond the pairs' first two
     int32_t V, d, d_tiles, splits, first;
     int32_t v0, v1, w0, w1;
     CUtensorMap map_dh;              // [splits, dh_rows] rows of fp32 partials: 32 x 32 boxes
@@ -282,33 +290,25 @@ struct CeGrad {
         st.dw_tiles = dw && v1 > v0 ? (v1 - v0 + GM_TILE - 1) / GM_TILE * d_tiles : 0;
         st.g_tiles = w1 > w0 ? (w1 - w0 + GM_TILE - 1) / GM_TILE * st.m_tiles : 0;
         st.dw_nk = max((st.n + 63) / 64, 1);
-        st.extra = st.dw_nk / ((d + 63) / 64);
+        st.dh_per = ((v1 - v0 + 63) / 64 + splits - 1) / splits;
+        st.dw_first = st.dw_nk > st.dh_per;
         return st;
     }
-    // The pairs take the long tiles (dh, dW) in turn, then the G tiles.  Where
-    // the long ones do not come out even, the pairs that have one less first
-    // take as many G tiles as make up for it (3% of a piece of 8,192 tokens x
-    // 7,782 rows on 74 pairs).
-    __device__ __forceinline__ bool tile(const State& st, int64_t pair, int64_t pairs, int i, Tile& t) const {
-        const int P = (int)pairs, p = (int)pair, longs = st.dh_tiles + st.dw_tiles;
-        const int mine = (longs - p + P - 1) / P;
-        int g = p + i * P;
-        if (i >= mine) {
-            const int even = longs % P;  // pairs [even, P) have one less (none if 0)
-            const int less = even ? P - even : 0;
-            const int extra = less ? min(st.extra, st.g_tiles / less) : 0;
-            const int own = p >= even ? extra : 0;
-            const int k = i - mine;
-            g = k < own ? (p - even) * extra + k : less * extra + (P - 1 - p) + (k - own) * P;
-            g += longs;
-        }
+    __device__ __forceinline__ int32_t* counter() const { return next_tile; }
+    // The longest tiles first (dh or dW by their K stages, then G), so that the
+    // short ones even out the pairs' ends.
+    __device__ __forceinline__ bool tile(const State& st, int64_t at, Tile& t) const {
+        if (at >= (int64_t)st.dh_tiles + st.dw_tiles + st.g_tiles) return false;
+        int g = (int)at;
+        if (st.dw_first && g < st.dh_tiles + st.dw_tiles) g += g < st.dw_tiles ? st.dh_tiles : -st.dw_tiles;
         if (g < st.dh_tiles) {
-            const int kb = (v1 - v0 + 63) / 64, per = (kb + splits - 1) / splits;
+            const int kb = (v1 - v0 + 63) / 64, per = st.dh_per;
             t.type = DH;
-            t.m0 = g % st.m_tiles * GM_TILE;
-            g /= st.m_tiles;
+            // d fastest: pairs running together read each row of G once
             t.n0 = g % d_tiles * GM_TILE;
-            t.split = g / d_tiles;
+            g /= d_tiles;
+            t.m0 = g % st.m_tiles * GM_TILE;
+            t.split = g / st.m_tiles;
             t.k0 = t.split * per;
             t.nk = max(min(per, kb - t.k0), 0);
             t.idesc = gm_idesc(false, false, true);
@@ -325,16 +325,15 @@ struct CeGrad {
             return true;
         }
         g -= st.dw_tiles;
-        if (g < st.g_tiles) {
-            t.type = GT;
-            t.m0 = g % st.m_tiles * GM_TILE;
-            t.n0 = g / st.m_tiles * GM_TILE;
-            t.k0 = 0;
-            t.nk = (d + 63) / 64;
-            t.idesc = gm_idesc(false);
-            return true;
-        }
-        return false;
+        t.type = GT;
+        int32_t m, n;
+        gm_grouped(g, st.m_tiles, (w1 - w0 + GM_TILE - 1) / GM_TILE, m, n);
+        t.m0 = m * GM_TILE;
+        t.n0 = n * GM_TILE;
+        t.k0 = 0;
+        t.nk = (d + 63) / 64;
+        t.idesc = gm_idesc(false);
+        return true;
     }
     __device__ __forceinline__ bool a_mn(const Tile& t) const { return t.type == DW; }
     __device__ __forceinline__ bool b_mn(const Tile& t) const { return t.type != GT; }
@@ -412,20 +411,20 @@ __global__ void __launch_bounds__(GM_THREADS, 1) k_ce_grad(const __grid_constant
     gm_run(p, ctl);
 }
 
-// A warp per packed row: the splits' partials in split order, one rounding.
+// A CTA per packed row: the splits' partials in split order, one rounding.
 __global__ void __launch_bounds__(256) k_ce_finish(const float* __restrict__ dh, int64_t dh_split, int32_t splits,
                                                    int32_t d, CeRows rows, __nv_bfloat16* __restrict__ grad_hidden,
                                                    int64_t ldgh, int32_t vec) {
     griddep_wait();
     griddep_launch_dependents();
-    const int64_t c = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int64_t c = blockIdx.x;
     if (c >= *rows.n) return;
     const float gmax = *rows.gmax;
     const float* src = dh + c * rows.pitch;
     __nv_bfloat16* dst = grad_hidden + rows.idx[c] * ldgh;
-    for (int32_t j = (threadIdx.x & 31) * 4; j < d; j += 128) {
+    for (int32_t j = threadIdx.x * 4; j < d; j += 1024) {
         float4 x = *reinterpret_cast<const float4*>(src + j);
-#pragma unroll 4
+#pragma unroll 8
         for (int k = 1; k < splits; ++k) {
             const float4 y = *reinterpret_cast<const float4*>(src + k * dh_split + j);
             x.x += y.x;
@@ -452,10 +451,10 @@ __global__ void __launch_bounds__(256) k_ce_finish(const float* __restrict__ dh,
 
 int64_t ce_round(int64_t x, int64_t q) { return (x + q - 1) / q * q; }
 
-// Splits of dh's token axis within a piece: enough tiles for every pair of
-// SMs when there are few rows.
+// Splits of dh's token axis within a piece: about four tiles for every pair of
+// SMs when there are few rows (then dh's tiles are few and long).
 int32_t ce_splits(int32_t pairs, int64_t m_tiles, int64_t d_tiles) {
-    return (int32_t)std::max<int64_t>(1, std::min<int64_t>(16, pairs / (m_tiles * d_tiles)));
+    return (int32_t)std::max<int64_t>(1, std::min<int64_t>(16, 4 * pairs / (m_tiles * d_tiles)));
 }
 
 }  // namespace
@@ -469,8 +468,9 @@ struct fr_ce {
     float* xt = nullptr;             // [cap]
     __nv_bfloat16* g[2] = {};        // [cap, piece] each
     float* dh = nullptr;             // fp32 partials of dh
+    int32_t* counters = nullptr;     // [pieces + 1] tile counters of the gradient's launches
     int32_t* err = nullptr;
-    CUtensorMap map_h_k, map_h_mn, map_g_k[2], map_g_mn[2], map_g_out[2];
+    CUtensorMap map_g_k[2], map_g_mn[2], map_g_out[2];
     cudaStream_t last_stream = nullptr;
     uint64_t wait_ns = FR_WAIT_LIMIT_NS;
     int32_t starve = 0;
@@ -526,10 +526,10 @@ extern "C" fr_status fr_ce_init(int32_t V, int32_t d, int32_t max_rows, fr_ce** 
         return FR_ERR_CUDA;
     }
     const size_t cap = (size_t)h->cap, pitch = (size_t)h->rows.pitch, d_tiles = (d + fr::GM_TILE - 1) / fr::GM_TILE;
-    // dh partials: one plane of all rows, or, with few rows, at most one tile row per SM
-    const size_t dh_rows = std::max(cap, std::max<size_t>(h->sms / d_tiles, 1) * fr::GM_TILE);
+    // dh partials: splits x tile rows is at most 4 * pairs / d_tiles where there is more than one split
+    const size_t dh_rows = std::max(cap, std::max<size_t>(2 * h->sms / d_tiles, 1) * fr::GM_TILE);
     cudaError_t e = cudaMalloc(&h->rows.h, cap * pitch * 2);
-    if (e == cudaSuccess) e = cudaMalloc(&h->rows.tgt, cap * 4 * 5 + 8);
+    if (e == cudaSuccess) e = cudaMalloc(&h->rows.tgt, cap * 4 * 5 + 8 + ((V + h->piece - 1) / h->piece + 1) * 4);
     if (e == cudaSuccess) e = cudaMalloc(&h->partial, cap * 2 * h->n_tiles * sizeof(float2));
     if (e == cudaSuccess) e = cudaMalloc(&h->g[0], cap * h->piece * 2 * 2);
     if (e == cudaSuccess) e = cudaMalloc(&h->dh, dh_rows * pitch * 4);
@@ -546,10 +546,10 @@ extern "C" fr_status fr_ce_init(int32_t V, int32_t d, int32_t max_rows, fr_ce** 
     h->rows.idx = reinterpret_cast<int32_t*>(h->xt + cap);
     h->rows.n = h->rows.idx + cap;
     h->rows.gmax = reinterpret_cast<float*>(h->rows.n + 1);
+    h->counters = h->rows.n + 2;
     h->g[1] = h->g[0] + cap * h->piece;
     const int64_t gp = (int64_t)h->piece * 2;
-    bool ok = fr::gm_encode(&h->map_h_k, 2, h->rows.h, h->cap, d, h->rows.pitch * 2, fr::GM_HALF) &&
-              fr::gm_encode(&h->map_h_mn, 2, h->rows.h, h->cap, d, h->rows.pitch * 2, 64);
+    bool ok = true;
     for (int b = 0; b < 2; ++b)
         ok = ok && fr::gm_encode(&h->map_g_k[b], 2, h->g[b], h->cap, h->piece, gp, fr::GM_HALF) &&
              fr::gm_encode(&h->map_g_mn[b], 2, h->g[b], h->cap, h->piece, gp, 64) &&
@@ -573,17 +573,18 @@ extern "C" fr_status fr_ce_loss(fr_ce* h, const void* hidden_dev, int64_t ldh, c
     if (rows == 0) return FR_OK;
     fr::CeLoss p{};
     if (!fr::gm_encode(&p.map_w, 2, weight_dev, h->V, h->d, ldw * 2, fr::GM_HALF)) return FR_ERR_CUDA;
-    p.map_h = h->map_h_k;
+    // rows behind the last are filled in by the copies, without being read
+    if (!fr::gm_encode(&p.map_h, 2, h->rows.h, rows, h->d, h->rows.pitch * 2, fr::GM_HALF)) return FR_ERR_CUDA;
     p.rows = h->rows;
     p.V = h->V;
     p.k_blocks = (h->d + 63) / 64;
     p.n_tiles = h->n_tiles;
     p.partial = h->partial;
     p.xt = h->xt;
-    const int32_t gather = (rows + fr::CE_GATHER_ROWS - 1) / fr::CE_GATHER_ROWS;
+    const int32_t gather = std::max((rows + fr::CE_GATHER_ROWS - 1) / fr::CE_GATHER_ROWS, fr::CE_GATHER_CTAS);
     FR_CUDA_TRY(fr::launch_pdl(fr::k_ce_gather, gather, fr::CE_GATHER_THREADS, 0, s, (const __nv_bfloat16*)hidden_dev, ldh,
                                targets_dev, (const float*)nullptr, (const float*)nullptr, rows, h->V, h->d, h->rows,
-                               loss_dev, lse_dev, (__nv_bfloat16*)nullptr, (int64_t)0, h->err));
+                               loss_dev, lse_dev, (__nv_bfloat16*)nullptr, (int64_t)0, (int32_t*)nullptr, 0, h->err));
     fr::GmCtl ctl{h->err, h->wait_ns, h->starve};
     FR_CUDA_TRY(fr::gm_launch(fr::k_ce_loss, fr::ce_round(rows, fr::GM_TILE) / fr::GM_TILE * h->n_tiles, h->sms, s, p, ctl));
     FR_CUDA_TRY(fr::launch_pdl(fr::k_ce_combine, ((int64_t)rows + 7) / 8, 256, 0, s, (const float2*)h->partial, 2 * h->n_tiles,
@@ -609,8 +610,11 @@ extern "C" fr_status fr_ce_grad(fr_ce* h, const void* hidden_dev, int64_t ldh, c
         return FR_ERR_CUDA;
     __nv_bfloat16* gh = (__nv_bfloat16*)grad_hidden_dev;
     const int64_t m_tiles = fr::ce_round(std::max(rows, 1), fr::GM_TILE) / fr::GM_TILE;  // no rows: dW is still written (zeros)
-    p.map_h_k = h->map_h_k;
-    p.map_h_mn = h->map_h_mn;
+    const int32_t pieces = (h->V + h->piece - 1) / h->piece;
+    // rows behind the last are filled in by the copies, without being read
+    if (!fr::gm_encode(&p.map_h_k, 2, h->rows.h, std::max(rows, 1), h->d, h->rows.pitch * 2, fr::GM_HALF) ||
+        !fr::gm_encode(&p.map_h_mn, 2, h->rows.h, std::max(rows, 1), h->d, h->rows.pitch * 2, 64))
+        return FR_ERR_CUDA;
     p.rows = h->rows;
     p.V = h->V;
     p.d = h->d;
@@ -625,12 +629,11 @@ extern "C" fr_status fr_ce_grad(fr_ce* h, const void* hidden_dev, int64_t ldh, c
     if (p.dw && (reinterpret_cast<uintptr_t>(grad_weight_dev) & 15u) == 0 && (ldgw & 7) == 0)
         p.dw_staged = fr::gm_staged_columns(h->d, 2);
     if (p.dw_staged && !fr::gm_encode(&p.map_dw, 2, grad_weight_dev, h->V, h->d, ldgw * 2, 32)) return FR_ERR_CUDA;
-    const int32_t gather = std::max((rows + fr::CE_GATHER_ROWS - 1) / fr::CE_GATHER_ROWS, 1);
+    const int32_t gather = std::max((rows + fr::CE_GATHER_ROWS - 1) / fr::CE_GATHER_ROWS, fr::CE_GATHER_CTAS);
     FR_CUDA_TRY(fr::launch_pdl(fr::k_ce_gather, gather, fr::CE_GATHER_THREADS, 0, s, (const __nv_bfloat16*)hidden_dev, ldh,
                                targets_dev, lse_dev, grad_loss_dev, rows, h->V, h->d, h->rows, (float*)nullptr,
-                               (float*)nullptr, gh, ldgh, h->err));
+                               (float*)nullptr, gh, ldgh, h->counters, pieces + 1, h->err));
     fr::GmCtl ctl{h->err, h->wait_ns, h->starve};
-    const int32_t pieces = (h->V + h->piece - 1) / h->piece;
     for (int32_t k = 0; k <= pieces; ++k) {
         p.v0 = p.v1 = p.w0 = p.w1 = 0;
         int64_t tiles = 0;
@@ -649,10 +652,11 @@ extern "C" fr_status fr_ce_grad(fr_ce* h, const void* hidden_dev, int64_t ldh, c
             p.map_g_out = h->map_g_out[k & 1];
             tiles += (int64_t)(p.w1 - p.w0 + fr::GM_TILE - 1) / fr::GM_TILE * m_tiles;
         }
+        p.next_tile = h->counters + k;
         FR_CUDA_TRY(fr::gm_launch(fr::k_ce_grad, tiles, h->sms, s, p, ctl));
     }
     if (gh && rows > 0)
-        FR_CUDA_TRY(fr::launch_pdl(fr::k_ce_finish, ((int64_t)rows + 7) / 8, 256, 0, s, (const float*)h->dh,
+        FR_CUDA_TRY(fr::launch_pdl(fr::k_ce_finish, (int64_t)rows, 256, 0, s, (const float*)h->dh,
                                    p.dh_rows * h->rows.pitch,
                                    p.splits, h->d, h->rows, gh, ldgh,
                                    (int32_t)((reinterpret_cast<uintptr_t>(gh) & 7u) == 0 && (ldgh & 3) == 0)));

@@ -20,10 +20,12 @@
 //     static constexpr bool I8;            // 8-bit integers (int32 sums) or bf16 (fp32 sums)
 //     static constexpr bool STAGED;        // the epilogue stores through shared memory
 //     static constexpr int STAGES;         // ring depth
+//     static constexpr bool DYNAMIC;       // tiles of unequal length: the pairs take the next one from a counter
 //     struct Tile { int nk; uint32_t idesc; ... };   // K stages; instruction descriptor
 //     struct State { ... };                          // what begin() read after the previous kernel
 //     __device__ State begin() const;
-//     __device__ bool tile(const State&, int64_t pair, int64_t pairs, int i, Tile&) const;  // the pair's i-th tile
+//     __device__ bool tile(const State&, int64_t g, Tile&) const;   // tile g of the launch; false behind the last
+//     __device__ int32_t* counter() const;           // DYNAMIC: zero before the launch; tiles fit an int32
 //     __device__ void load(const Tile&, int kb, int rank, uint8_t* a, uint8_t* b, uint32_t bar) const;
 //     __device__ bool a_mn(const Tile&) const, b_mn(const Tile&) const;  // operand stored MN-major
 //     // columns [c0, c0 + 128) of one row
@@ -168,6 +170,39 @@ struct GmStage {
     }
 };
 
+// Bounded wait that also acquires what the other CTA of the pair wrote.
+__device__ __forceinline__ bool gm_wait_pair(uint64_t* bar, uint32_t parity, volatile int32_t* abort_flag, int32_t* err,
+                                             uint64_t limit_ns) {
+    uint64_t t0 = 0;
+    for (uint32_t it = 0;; ++it) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if (*abort_flag) return false;
+        if (it == 0) t0 = tc_now_ns();
+        if ((it & 63u) == 63u && tc_now_ns() - t0 > limit_ns) {
+            *abort_flag = 1;
+            set_error(err, FR_ERR_DEVICE);
+            return false;
+        }
+    }
+}
+
+// Address of `p`'s counterpart in the pair's CTA `rank`.
+__device__ __forceinline__ uint32_t gm_in_cta(const void* p, uint32_t rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    return a;
+}
+
+constexpr int GM_SLOTS = 4;  // tiles published ahead of the last reader
+
 template <int STAGES>
 struct GmSmem {
     uint64_t full[STAGES];      // used in the first CTA: both CTAs' copies of a stage have landed
@@ -175,9 +210,22 @@ struct GmSmem {
     uint64_t tmem_full[2];
     uint64_t tmem_empty[2];     // used in the first CTA: both CTAs' epilogues have read the accumulator
     uint64_t mma_done;          // every product the pair issued has completed
+    uint64_t tile_full[GM_SLOTS];   // DYNAMIC: the slot's tile has been published
+    uint64_t tile_empty[GM_SLOTS];  // used in the first CTA: everyone has read the slot
+    int32_t tile_id[GM_SLOTS];
     uint32_t tmem_base;
     int32_t abort_flag;
 };
+
+// Tile g of an m_tiles x n_tiles grid, m fastest within groups of 32 tile rows:
+// pairs running together share the B tile, and the A tiles of a group (8,192
+// rows) stay in L2 while B passes by.
+__device__ __forceinline__ void gm_grouped(int64_t g, int32_t m_tiles, int32_t n_tiles, int32_t& m, int32_t& n) {
+    const int32_t group = (int32_t)(g / (32 * (int64_t)n_tiles)), m0 = group * 32, rows = min(32, m_tiles - m0);
+    const int32_t at = (int32_t)(g - (int64_t)m0 * n_tiles);
+    m = m0 + at % rows;
+    n = at / rows;
+}
 
 // What every policy's kernel passes along.
 struct GmCtl {
@@ -215,6 +263,10 @@ __device__ __forceinline__ void gm_run(const P& p, const GmCtl& ctl) {
             tc_mbar_init(&sm->tmem_empty[i], 2 * GM_EPI_WARPS);
         }
         tc_mbar_init(&sm->mma_done, 1);
+        for (int i = 0; i < GM_SLOTS; ++i) {
+            tc_mbar_init(&sm->tile_full[i], 1);
+            tc_mbar_init(&sm->tile_empty[i], 2 * GM_EPI_WARPS + 2);  // the epilogue warps, the products, the other producer
+        }
         sm->abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -233,12 +285,57 @@ __device__ __forceinline__ void gm_run(const P& p, const GmCtl& ctl) {
     griddep_launch_dependents();
     const typename P::State st = p.begin();
 
+    // The i-th tile of this pair.  Taken in turn, or published by the first
+    // CTA's producer: `whole` warps read it together, else one lane does.
     typename P::Tile t;
+    const auto next = [&](int i, bool whole) -> bool {
+        if (!P::DYNAMIC) return p.tile(st, pair + i * pairs, t);
+        const int s = i % GM_SLOTS;
+        // only the second CTA's readers need to synchronise with another CTA
+        if (!(rank == 0 ? tc_wait(&sm->tile_full[s], (i / GM_SLOTS) & 1, abort_flag, ctl.err, ctl.wait_ns)
+                        : gm_wait_pair(&sm->tile_full[s], (i / GM_SLOTS) & 1, abort_flag, ctl.err, ctl.wait_ns)))
+            return false;
+        const int32_t g = *(volatile int32_t*)&sm->tile_id[s];
+        if (whole) __syncwarp();
+        if (!whole || lane == 0) {
+            if (rank == 0)
+                tc_arrive(&sm->tile_empty[s]);
+            else
+                gm_arrive_remote(gm_in_first(&sm->tile_empty[s]));
+        }
+        return p.tile(st, g, t);
+    };
+    // The first CTA's producer publishes the tile after the one that it takes
+    // itself, so that nobody waits for it, and asks for the one behind that,
+    // whose answer comes while this one is copied.  The first two are static.
+    int64_t cur = pair, coming = pair + pairs;
+    const auto publish = [&](int i, int64_t g) -> bool {
+        const int s = i % GM_SLOTS;
+        if (i >= GM_SLOTS &&
+            !gm_wait_pair(&sm->tile_empty[s], ((i / GM_SLOTS) & 1) ^ 1, abort_flag, ctl.err, ctl.wait_ns))
+            return false;
+        *(volatile int32_t*)&sm->tile_id[s] = (int32_t)g;
+        tc_arrive(&sm->tile_full[s]);
+        asm volatile("st.relaxed.cluster.shared::cluster.s32 [%0], %1;" ::"r"(gm_in_cta(&sm->tile_id[s], 1)), "r"((int32_t)g)
+                     : "memory");
+        gm_arrive_remote(gm_in_cta(&sm->tile_full[s], 1));
+        return true;
+    };
+    const auto take = [&](int i) -> bool {
+        if (!P::DYNAMIC) return p.tile(st, pair + i * pairs, t);
+        if (rank != 0) return next(i, false);
+        if (i == 0 && !publish(0, cur)) return false;
+        if (!p.tile(st, cur, t)) return false;
+        if (!publish(i + 1, coming)) return false;
+        cur = coming;
+        coming = atomicAdd(p.counter(), 1) + 2 * pairs;
+        return true;
+    };
     if (warp == 0) {
         if (lane == 0 && !ctl.starve) {
             uint32_t it = 0;
             bool ok = true;
-            for (int i = 0; ok && p.tile(st, pair, pairs, i, t); ++i) {
+            for (int i = 0; ok && take(i); ++i) {
                 for (int kb = 0; kb < t.nk; ++kb, ++it) {
                     const uint32_t s = it % STAGES;
                     if (it >= (uint32_t)STAGES &&
@@ -267,7 +364,7 @@ __device__ __forceinline__ void gm_run(const P& p, const GmCtl& ctl) {
         if (lane == 0 && rank == 0) {
             uint32_t it = 0;
             bool ok = true;
-            for (int i = 0; ok && p.tile(st, pair, pairs, i, t); ++i) {
+            for (int i = 0; ok && next(i, false); ++i) {
                 const int acc = i & 1;
                 if (i >= 2 && !tc_wait(&sm->tmem_empty[acc], ((i >> 1) & 1) ^ 1, abort_flag, ctl.err, ctl.wait_ns)) break;
                 tc_fence_after();
@@ -302,7 +399,7 @@ __device__ __forceinline__ void gm_run(const P& p, const GmCtl& ctl) {
         const int q = warp & 3, c0 = ((warp - 4) >> 2) * GM_EPI_COLS;
         GmStage sg{stage + (warp - 4) * GM_STAGE_BUF};
         const uint32_t empty0 = gm_in_first(&sm->tmem_empty[0]), empty1 = gm_in_first(&sm->tmem_empty[1]);
-        for (int i = 0; p.tile(st, pair, pairs, i, t); ++i) {
+        for (int i = 0; next(i, true); ++i) {
             const int acc = i & 1;
             if (!tc_wait(&sm->tmem_full[acc], (i >> 1) & 1, abort_flag, ctl.err, ctl.wait_ns)) break;
             tc_fence_after();
@@ -364,29 +461,24 @@ __device__ __forceinline__ void gm_lse_fold(const float (&v)[32], float& m, floa
     }
 }
 
-// A warp's log-sum-exp of one row's n (max, scaled sum) partials, combined in
-// lane order (every lane returns it).
+// A warp's log-sum-exp of one row's n (max, scaled sum) partials (every lane
+// returns it).  Two passes: the terms of the second do not wait for one another.
 __device__ __forceinline__ float gm_lse_combine(const float2* p, int32_t n) {
     constexpr float L2E = 1.4426950408889634f;
     const int lane = threadIdx.x & 31;
     float m = -INFINITY, s = 0.f;
+#pragma unroll 8
+    for (int i = lane; i < n; i += 32) m = gm_max_nan(m, p[i].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = gm_max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (m == -INFINITY) return m;
+#pragma unroll 8
     for (int i = lane; i < n; i += 32) {
         const float2 q = p[i];
-        const float M = gm_max_nan(m, q.x);
-        if (M != -INFINITY) {
-            s = (m == M ? s : s * tc_ex2((m - M) * L2E)) + (q.x == M ? q.y : q.y * tc_ex2((q.x - M) * L2E));
-            m = M;
-        }
+        s += q.y * tc_ex2((q.x - m) * L2E);
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
-        const float M = gm_max_nan(m, m2);
-        if (M != -INFINITY) {
-            s = (m == M ? s : s * tc_ex2((m - M) * L2E)) + (m2 == M ? s2 : s2 * tc_ex2((m2 - M) * L2E));
-            m = M;
-        }
-    }
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     return m + logf(s);
 }
 

@@ -69,10 +69,10 @@ __global__ void __launch_bounds__(256) k_i8_quantize(const T* __restrict__ x, in
     if (lane == 0) scale[r] = s;
 }
 
-// Tile walk shared by the two products: m fastest, so pairs running together
-// share the weight tile and the activations stay in L2.
+// Tile walk shared by the two products.
 struct I8Base {
-    static constexpr bool I8 = true;
+    static constexpr bool I8 = true, DYNAMIC = false;
+    __device__ __forceinline__ int32_t* counter() const { return nullptr; }
     struct Tile {
         int nk, m0, n0;
         uint32_t idesc;
@@ -85,11 +85,12 @@ struct I8Base {
     int32_t ws_vec;  // ws starts on 16 bytes
 
     __device__ __forceinline__ State begin() const { return {}; }
-    __device__ __forceinline__ bool tile(const State&, int64_t pair, int64_t pairs, int i, Tile& t) const {
-        const int64_t g = pair + i * pairs;
+    __device__ __forceinline__ bool tile(const State&, int64_t g, Tile& t) const {
         if (g >= (int64_t)m_tiles * n_tiles) return false;
-        t.m0 = (int)(g % m_tiles) * GM_TILE;
-        t.n0 = (int)(g / m_tiles) * GM_TILE;
+        int32_t m, n;
+        gm_grouped(g, m_tiles, n_tiles, m, n);
+        t.m0 = m * GM_TILE;
+        t.n0 = n * GM_TILE;
         t.nk = k_blocks;
         t.idesc = gm_idesc(true);
         return true;
