@@ -82,7 +82,9 @@ def test_quantize_rows_that_are_not_finite():
     assert torch.all(q[:2] == 0) and torch.all(q[2] == 127)
 
 
-SHAPES = [(1, 1, 1), (1, 300, 64), (2, 77, 130), (5, 1000, 2048), (16, 513, 96), (33, 64, 16), (100, 1003, 521), (128, 256, 128),
+# up to 4 rows stream the weight; the others run on tiles of 256, 128 or 64 columns
+SHAPES = [(1, 1, 1), (1, 300, 64), (2, 77, 130), (3, 2001, 1000), (4, 41, 7), (4, 300, 9000), (4, 130, 20000), (5, 1000, 2048), (9, 130, 50),
+          (16, 513, 96), (20, 15001, 40), (33, 64, 16), (100, 1003, 521), (128, 256, 128),
           (129, 2500, 333), (300, 700, 4096)]
 
 

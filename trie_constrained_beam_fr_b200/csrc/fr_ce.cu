@@ -196,13 +196,15 @@ struct CeLoss {
         t.idesc = gm_idesc(false);
         return true;
     }
+    __device__ __forceinline__ uint32_t stage_bytes() const { return 2 * GM_OP_BYTES; }
     __device__ __forceinline__ bool a_mn(const Tile&) const { return false; }
     __device__ __forceinline__ bool b_mn(const Tile&) const { return false; }
     __device__ __forceinline__ void load(const Tile& t, int kb, int rank, uint8_t* a, uint8_t* b, uint32_t bar) const {
         gm_tma_load(&map_h, a, bar, kb * 64, t.m0 + rank * GM_HALF);
         gm_tma_load(&map_w, b, bar, kb * 64, t.n0 + rank * GM_HALF);
     }
-    __device__ __forceinline__ void epilogue(const State& st, const Tile& t, uint32_t taddr, int r, int c0, const GmStage&) const {
+    __device__ __forceinline__ void epilogue(const State& st, const Tile& t, uint32_t taddr, int r, int half, const GmStage&) const {
+        const int c0 = half * GM_EPI_COLS;
         const int row = t.m0 + r;
         const int32_t tgt = row < st.n ? rows.tgt[row] : -1;
         float m = -INFINITY, s = 0.f;
@@ -335,6 +337,7 @@ struct CeGrad {
         t.idesc = gm_idesc(false);
         return true;
     }
+    __device__ __forceinline__ uint32_t stage_bytes() const { return 2 * GM_OP_BYTES; }
     __device__ __forceinline__ bool a_mn(const Tile& t) const { return t.type == DW; }
     __device__ __forceinline__ bool b_mn(const Tile& t) const { return t.type != GT; }
     __device__ __forceinline__ void load(const Tile& t, int kb, int rank, uint8_t* a, uint8_t* b, uint32_t bar) const {
@@ -353,7 +356,8 @@ struct CeGrad {
             gm_tma_load(&map_h_mn, b + 8192, bar, n + 64, k);
         }
     }
-    __device__ __forceinline__ void epilogue(const State& st, const Tile& t, uint32_t taddr, int r, int c0, const GmStage& sg) const {
+    __device__ __forceinline__ void epilogue(const State& st, const Tile& t, uint32_t taddr, int r, int half, const GmStage& sg) const {
+        const int c0 = half * GM_EPI_COLS;
         const int row = t.m0 + r, lane = threadIdx.x & 31, row0 = row - lane;
         if (t.type == GT) {
             const bool live = row < st.n;
@@ -389,7 +393,7 @@ struct CeGrad {
                     gm_stage32<true>(sg, &map_dh, lane, v, t.n0 + c, t.split * dh_rows + row0);
             }
         } else {
-            const int v = v0 + row;
+            const int v = v0 + row0;  // the warp's first row
 #pragma unroll 1
             for (int c = c0; c < c0 + GM_EPI_COLS && t.n0 + c < d; c += 64) {
                 float x[64];
@@ -397,10 +401,12 @@ struct CeGrad {
                 gm_ld32(taddr + (uint32_t)c + 32, x + 32);
 #pragma unroll
                 for (int i = 0; i < 64; ++i) x[i] *= st.gmax;
+                if (v >= v1) continue;
                 if (t.n0 + c < dw_staged) {
-                    if (v0 + row0 < v1) gm_stage64(sg, &map_dw, lane, x, t.n0 + c, v0 + row0);
-                } else if (v < v1) {
-                    gm_store(dw + v * ldw + t.n0 + c, x, min(64, d - t.n0 - c));
+                    gm_stage64(sg, &map_dw, lane, x, t.n0 + c, v);
+                } else {
+                    gm_put(sg, lane, x);
+                    gm_write_plain(sg, lane, dw + v * ldw + t.n0 + c, ldw, min(32, v1 - v), min(64, d - t.n0 - c));
                 }
             }
         }

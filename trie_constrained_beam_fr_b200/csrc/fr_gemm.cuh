@@ -27,9 +27,10 @@
 //     __device__ bool tile(const State&, int64_t g, Tile&) const;   // tile g of the launch; false behind the last
 //     __device__ int32_t* counter() const;           // DYNAMIC: zero before the launch; tiles fit an int32
 //     __device__ void load(const Tile&, int kb, int rank, uint8_t* a, uint8_t* b, uint32_t bar) const;
+//     __device__ uint32_t stage_bytes() const;       // that load() copies per CTA
 //     __device__ bool a_mn(const Tile&) const, b_mn(const Tile&) const;  // operand stored MN-major
-//     // columns [c0, c0 + 128) of one row
-//     __device__ void epilogue(const State&, const Tile&, uint32_t taddr, int row_in_tile, int c0, GmStage&) const;
+//     // the first or second half of one row's columns
+//     __device__ void epilogue(const State&, const Tile&, uint32_t taddr, int row_in_tile, int half, const GmStage&) const;
 //   };
 //
 // Every wait on a barrier is bounded; on expiry the kernel records
@@ -60,9 +61,9 @@ constexpr uint32_t GM_TMEM_COLS = 2 * GM_TILE;      // two accumulators
 // A and B types at bits 7-9 and 10-12 (kind::f16: 1 = bf16; kind::i8: 1 =
 // signed), "MN-major" flags of A and B at bits 15 and 16, N >> 3 at bits
 // 17-22, M >> 4 at bits 24-28.
-__host__ __device__ constexpr uint32_t gm_idesc(bool i8, bool a_mn = false, bool b_mn = false) {
+__host__ __device__ constexpr uint32_t gm_idesc(bool i8, bool a_mn = false, bool b_mn = false, int n = GM_TILE) {
     return ((i8 ? 2u : 1u) << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
-           ((uint32_t)(GM_TILE >> 3) << 17) | ((uint32_t)(GM_TILE >> 4) << 24);
+           ((uint32_t)(n >> 3) << 17) | ((uint32_t)(GM_TILE >> 4) << 24);
 }
 
 // Shared-memory descriptor of an MN-major bf16 tile with the 128-byte
@@ -344,7 +345,7 @@ __device__ __forceinline__ void gm_run(const P& p, const GmCtl& ctl) {
                         break;
                     }
                     // the first CTA's barrier counts both CTAs' bytes
-                    if (rank == 0) tc_arrive_expect_tx(&sm->full[s], (uint32_t)(4 * GM_OP_BYTES));
+                    if (rank == 0) tc_arrive_expect_tx(&sm->full[s], 2 * p.stage_bytes());
                     p.load(t, kb, (int)rank, ringA + s * GM_OP_BYTES, ringB + s * GM_OP_BYTES, gm_in_first(&sm->full[s]));
                 }
             }
@@ -396,7 +397,7 @@ __device__ __forceinline__ void gm_run(const P& p, const GmCtl& ctl) {
         // in both CTAs: the commits' arrivals reach no CTA that has ended
         if (lane == 0) tc_wait_drain(&sm->mma_done, 0);
     } else if (warp >= 4) {
-        const int q = warp & 3, c0 = ((warp - 4) >> 2) * GM_EPI_COLS;
+        const int q = warp & 3, half = (warp - 4) >> 2;
         GmStage sg{stage + (warp - 4) * GM_STAGE_BUF};
         const uint32_t empty0 = gm_in_first(&sm->tmem_empty[0]), empty1 = gm_in_first(&sm->tmem_empty[1]);
         for (int i = 0; next(i, true); ++i) {
@@ -404,7 +405,7 @@ __device__ __forceinline__ void gm_run(const P& p, const GmCtl& ctl) {
             if (!tc_wait(&sm->tmem_full[acc], (i >> 1) & 1, abort_flag, ctl.err, ctl.wait_ns)) break;
             tc_fence_after();
             p.epilogue(st, t, tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * GM_TILE), (int)rank * GM_HALF + q * 32 + lane,
-                       c0, sg);
+                       half, sg);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) gm_arrive_remote(acc ? empty1 : empty0);
@@ -492,36 +493,45 @@ __device__ __forceinline__ uint4 gm_pack8(const float* v) {
     return o;
 }
 
-// Stores the first n of CW values of one row whose start has no alignment.
-template <int CW>
-__device__ __forceinline__ void gm_store(__nv_bfloat16* dst, const float (&v)[CW], int n) {
+// Puts 64 values as bf16, or 32 as fp32, into this lane's row of the buffer.
+__device__ __forceinline__ void gm_put(const GmStage& sg, int lane, const float (&v)[64]) {
+    uint8_t* row = sg.row(lane);
 #pragma unroll
-    for (int i = 0; i < CW; ++i)
-        if (i < n) dst[i] = __float2bfloat16_rn(v[i]);
+    for (int j = 0; j < 8; ++j) sg.put(row, lane, j, gm_pack8(v + 8 * j));
 }
-template <int CW>
-__device__ __forceinline__ void gm_store(float* dst, const float (&v)[CW], int n) {
+__device__ __forceinline__ void gm_put(const GmStage& sg, int lane, const float (&v)[32]) {
+    uint8_t* row = sg.row(lane);
 #pragma unroll
-    for (int i = 0; i < CW; ++i)
-        if (i < n) dst[i] = v[i];
+    for (int j = 0; j < 8; ++j)
+        sg.put(row, lane, j, make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]), __float_as_uint(v[4 * j + 2]),
+                                        __float_as_uint(v[4 * j + 3])));
+}
+
+// Writes the buffer's first `rows` rows and `cols` columns of T to dst with
+// plain stores, a row at a time: for rows that TMA cannot address (15 us of 29
+// on 333 x 1,003 fp32 values were a lane's stores to its own row).
+template <class T>
+__device__ __forceinline__ void gm_write_plain(const GmStage& sg, int lane, T* dst, int64_t ld, int rows, int cols) {
+    __syncwarp();
+    for (int r = 0; r < rows; ++r) {
+#pragma unroll
+        for (int c = lane; c < 128 / (int)sizeof(T); c += 32) {
+            const int at = c * (int)sizeof(T);
+            if (c < cols) dst[r * ld + c] = *reinterpret_cast<const T*>(sg.buf + r * 128 + (((at >> 4) ^ (r & 7)) << 4) + (at & 15));
+        }
+    }
 }
 
 // Sends 64 bf16 columns of the warp's 32 rows to (x, y) of `map`.
 __device__ __forceinline__ void gm_stage64(const GmStage& sg, const CUtensorMap* map, int lane, const float (&v)[64], int x, int y) {
-    uint8_t* row = sg.row(lane);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) sg.put(row, lane, j, gm_pack8(v + 8 * j));
+    gm_put(sg, lane, v);
     sg.send<false>(map, lane, x, y);
 }
 
 // Sends (or adds) 32 fp32 columns of the warp's 32 rows to (x, y) of `map`.
 template <bool ADD>
 __device__ __forceinline__ void gm_stage32(const GmStage& sg, const CUtensorMap* map, int lane, const float (&v)[32], int x, int y) {
-    uint8_t* row = sg.row(lane);
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        sg.put(row, lane, j, make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]), __float_as_uint(v[4 * j + 2]),
-                                        __float_as_uint(v[4 * j + 3])));
+    gm_put(sg, lane, v);
     sg.send<ADD>(map, lane, x, y);
 }
 

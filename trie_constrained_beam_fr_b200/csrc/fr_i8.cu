@@ -8,7 +8,8 @@
 // scales round.  The row and channel scales factor out of the sum, which is
 // why the whole product runs on integers.
 //
-//   k_i8_quantize  a warp per row; reads the row twice (maximum, then values).
+//   k_i8_quantize  a CTA per row: maximum, then values, held in registers.
+//   k_i8_few       up to 4 tokens: a stream over the weight (__dp4a).
 //   k_i8<I8Out>    tcgen05 kind::i8 tiles of 256 rows x 256 channels; the
 //                  epilogue scales and writes logits (bf16 or fp32).
 //   k_i8<I8Lse>    the same product whose epilogue reduces each row to
@@ -30,43 +31,209 @@
 namespace fr {
 namespace {
 
-template <class T>
-__device__ __forceinline__ float i8_load(const T* p);
-template <>
-__device__ __forceinline__ float i8_load(const float* p) { return *p; }
-template <>
-__device__ __forceinline__ float i8_load(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-
 // q of one value: the quotient and its rounding are IEEE (nearest even); a
 // row whose scale is zero or not finite quantises to zeros (a scale that is
 // not finite makes every product of the row NaN or infinite).
-__device__ __forceinline__ int8_t i8_quant(float x, float scale, bool live) {
-    return live ? (int8_t)__float2int_rn(fminf(fmaxf(__fdiv_rn(x, scale), -127.f), 127.f)) : (int8_t)0;
+__device__ __forceinline__ int32_t i8_quant(float x, float scale, bool live) {
+    return live ? __float2int_rn(fminf(fmaxf(__fdiv_rn(x, scale), -127.f), 127.f)) : 0;
 }
 
-template <class T>
-__global__ void __launch_bounds__(256) k_i8_quantize(const T* __restrict__ x, int64_t ldx, int32_t rows, int32_t d,
-                                                     int8_t* __restrict__ q, int64_t ldq, float* __restrict__ scale) {
+__device__ __forceinline__ void i8_load8(const float* p, float (&v)[8]) {
+    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+__device__ __forceinline__ void i8_load8(const __nv_bfloat16* p, float (&v)[8]) {
+    const uint4 a = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+__device__ __forceinline__ float i8_load1(const float* p) { return *p; }
+__device__ __forceinline__ float i8_load1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+
+constexpr int QT_THREADS = 128;
+constexpr int QT_HELD = 4;  // groups of 8 values that a thread keeps between the two passes (d <= 4,096)
+
+// A CTA per row.  VEC: rows start on 16 bytes (x) and 8 bytes (q), so 8 values
+// move at once.
+template <class T, bool VEC>
+__global__ void __launch_bounds__(QT_THREADS) k_i8_quantize(const T* __restrict__ x, int64_t ldx, int32_t d,
+                                                            int8_t* __restrict__ q, int64_t ldq, float* __restrict__ scale) {
+    __shared__ uint32_t max_s[QT_THREADS / 32];
     griddep_wait();
     griddep_launch_dependents();
-    const int lane = threadIdx.x & 31;
-    const int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (r >= rows) return;
+    const int tid = threadIdx.x;
+    const int64_t r = blockIdx.x;
     const T* xr = x + r * ldx;
-    float m = 0.f;
-    bool nan = false;
-    for (int j = lane; j < d; j += 32) {
-        const float v = i8_load(xr + j);
-        nan |= v != v;
-        m = fmaxf(m, fabsf(v));
-    }
+    int8_t* qr = q + r * ldq;
+    const int32_t groups = VEC ? d >> 3 : 0, rest = groups << 3;
+    float held[QT_HELD][8];
+    // absolute values order as their bits, a NaN above infinity
+    uint32_t m = 0u;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (__any_sync(0xffffffffu, nan)) m = NAN;
-    const float s = __fdiv_rn(m, 127.f);
+    for (int k = 0; k < QT_HELD; ++k) {
+        const int32_t g = k * QT_THREADS + tid;
+        if (VEC && g < groups) {
+            i8_load8(xr + 8 * (int64_t)g, held[k]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(held[k][i]) & 0x7FFFFFFFu);
+        }
+    }
+    for (int32_t g = QT_HELD * QT_THREADS + tid; VEC && g < groups; g += QT_THREADS) {
+        float v[8];
+        i8_load8(xr + 8 * (int64_t)g, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    }
+#pragma unroll 4
+    for (int32_t j = rest + tid; j < d; j += QT_THREADS) m = max(m, __float_as_uint(i8_load1(xr + j)) & 0x7FFFFFFFu);
+    m = __reduce_max_sync(0xffffffffu, m);
+    if ((tid & 31) == 0) max_s[tid >> 5] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < QT_THREADS / 32; ++w) m = max(m, max_s[w]);
+    const float s = __fdiv_rn(__uint_as_float(m), 127.f);
     const bool live = s > 0.f && isfinite(s);
-    for (int j = lane; j < d; j += 32) q[r * ldq + j] = i8_quant(i8_load(xr + j), s, live);
-    if (lane == 0) scale[r] = s;
+    const auto put8 = [&](int32_t g, const float (&v)[8]) {
+        uint32_t lo = 0u, hi = 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            lo |= (uint32_t)(i8_quant(v[i], s, live) & 0xFF) << (8 * i);
+            hi |= (uint32_t)(i8_quant(v[4 + i], s, live) & 0xFF) << (8 * i);
+        }
+        *reinterpret_cast<uint2*>(qr + 8 * (int64_t)g) = make_uint2(lo, hi);
+    };
+#pragma unroll
+    for (int k = 0; k < QT_HELD; ++k) {
+        const int32_t g = k * QT_THREADS + tid;
+        if (VEC && g < groups) put8(g, held[k]);
+    }
+    for (int32_t g = QT_HELD * QT_THREADS + tid; VEC && g < groups; g += QT_THREADS) {
+        float v[8];
+        i8_load8(xr + 8 * (int64_t)g, v);
+        put8(g, v);
+    }
+#pragma unroll 4
+    for (int32_t j = rest + tid; j < d; j += QT_THREADS) qr[j] = (int8_t)i8_quant(i8_load1(xr + j), s, live);
+    if (tid == 0) scale[r] = s;
+}
+
+// The product for up to 4 tokens: bound by the weight's bytes, which go straight
+// to registers (16 bytes a lane, 4 channels x 2,048 values per warp in flight);
+// the tokens lie in shared memory (zeros behind d), __dp4a multiplies and one
+// warp reduction per value adds the lanes.  A warp takes 4 channels at a time,
+// so the channels spread evenly over the SMs.  151,936 channels x 2,048 values:
+// 52 us for 1 to 4 tokens (6.0 TB/s) where the tiles take 68 to 86; 8 tokens
+// (bound by __dp4a) took 85 us against 80 on tiles.
+constexpr int FEW_ROWS = 4;
+constexpr int FEW_THREADS = 256;
+constexpr int FEW_CH = 4;
+constexpr int FEW_STEPS = 4;
+constexpr int FEW_SMEM = 64 * 1024;  // most bytes of tokens
+
+// 16 bytes of the weight, read once.
+__device__ __forceinline__ int4 few_load(const int8_t* p) {
+    int4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.s32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
+template <int R, class T>
+__global__ void __launch_bounds__(FEW_THREADS) k_i8_few(const int8_t* __restrict__ xq, int64_t ldx,
+                                                        const float* __restrict__ xs, const int8_t* __restrict__ wq,
+                                                        int64_t ldw, const float* __restrict__ ws, int32_t rows, int32_t N,
+                                                        int32_t d, T* __restrict__ out, int64_t ldo) {
+    extern __shared__ __align__(16) int8_t few_x[];  // [R][pitch]
+    const int32_t pieces = (d + 15) >> 4, pitch = pieces << 4;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    griddep_wait();
+    griddep_launch_dependents();
+    for (int32_t i = threadIdx.x; i < R * pieces; i += FEW_THREADS) {
+        const int32_t r = i / pieces, k = (i - r * pieces) << 4;
+        const int8_t* src = xq + r * ldx + k;
+        int4 v = make_int4(0, 0, 0, 0);
+        if (r < rows) {
+            if (k + 16 <= d) {
+                v = *reinterpret_cast<const int4*>(src);
+            } else {
+                int8_t* b = reinterpret_cast<int8_t*>(&v);
+                for (int j = 0; j < d - k; ++j) b[j] = src[j];
+            }
+        }
+        *reinterpret_cast<int4*>(few_x + r * pitch + k) = v;
+    }
+    __syncthreads();
+    const int32_t groups = (N + FEW_CH - 1) / FEW_CH;
+    for (int32_t g = blockIdx.x * (FEW_THREADS / 32) + warp; g < groups; g += gridDim.x * (FEW_THREADS / 32)) {
+        const int32_t n0 = g * FEW_CH;
+        int32_t acc[FEW_CH][R];
+#pragma unroll
+        for (int c = 0; c < FEW_CH; ++c)
+#pragma unroll
+            for (int r = 0; r < R; ++r) acc[c][r] = 0;
+        const int8_t* src[FEW_CH];
+#pragma unroll
+        for (int c = 0; c < FEW_CH; ++c) src[c] = wq + min(n0 + c, N - 1) * ldw;
+        const auto add = [&](const int4 (&w)[FEW_CH], int32_t k) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int4 x = *reinterpret_cast<const int4*>(few_x + r * pitch + k);
+#pragma unroll
+                for (int c = 0; c < FEW_CH; ++c) {
+                    acc[c][r] = __dp4a(w[c].x, x.x, acc[c][r]);
+                    acc[c][r] = __dp4a(w[c].y, x.y, acc[c][r]);
+                    acc[c][r] = __dp4a(w[c].z, x.z, acc[c][r]);
+                    acc[c][r] = __dp4a(w[c].w, x.w, acc[c][r]);
+                }
+            }
+        };
+        // whole pieces, FEW_STEPS x 512 values with all their loads in flight
+        int32_t k = lane << 4;
+        for (; k - (lane << 4) + FEW_STEPS * 512 <= d; k += FEW_STEPS * 512) {
+            int4 w[FEW_STEPS][FEW_CH];
+#pragma unroll
+            for (int u = 0; u < FEW_STEPS; ++u)
+#pragma unroll
+                for (int c = 0; c < FEW_CH; ++c) w[u][c] = few_load(src[c] + k + u * 512);
+#pragma unroll
+            for (int u = 0; u < FEW_STEPS; ++u) add(w[u], k + u * 512);
+        }
+        for (; k < pitch; k += 512) {
+            int4 w[FEW_CH];
+#pragma unroll
+            for (int c = 0; c < FEW_CH; ++c) {
+                if (k + 16 <= d) {
+                    w[c] = few_load(src[c] + k);
+                } else {  // a row's last piece: nothing is read behind d
+                    w[c] = make_int4(0, 0, 0, 0);
+                    int8_t* b = reinterpret_cast<int8_t*>(&w[c]);
+#pragma unroll
+                    for (int j = 0; j < 15; ++j)
+                        if (k + j < d) b[j] = src[c][k + j];
+                }
+            }
+            add(w, k);
+        }
+        int32_t mine = 0;  // lane r * FEW_CH + c keeps token r's channel c
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int c = 0; c < FEW_CH; ++c) {
+                const int32_t sum = __reduce_add_sync(0xffffffffu, acc[c][r]);
+                if (lane == r * FEW_CH + c) mine = sum;
+            }
+        const int32_t r = lane / FEW_CH, n = n0 + lane % FEW_CH;
+        if (r < rows && r < R && n < N) {
+            const float y = (float)mine * xs[r] * __ldg(ws + n);
+            if constexpr (sizeof(T) == 4)
+                out[r * ldo + n] = y;
+            else
+                out[r * ldo + n] = __float2bfloat16_rn(y);
+        }
+    }
 }
 
 // Tile walk shared by the two products.
@@ -80,6 +247,7 @@ struct I8Base {
     struct State {};
     CUtensorMap map_x, map_w;
     int32_t rows, N, k_blocks, m_tiles, n_tiles;
+    int32_t bn;  // columns of a tile: 256, or fewer where that leaves SMs without one
     const float* xs;
     const float* ws;
     int32_t ws_vec;  // ws starts on 16 bytes
@@ -90,16 +258,17 @@ struct I8Base {
         int32_t m, n;
         gm_grouped(g, m_tiles, n_tiles, m, n);
         t.m0 = m * GM_TILE;
-        t.n0 = n * GM_TILE;
+        t.n0 = n * bn;
         t.nk = k_blocks;
-        t.idesc = gm_idesc(true);
+        t.idesc = gm_idesc(true, false, false, bn);
         return true;
     }
+    __device__ __forceinline__ uint32_t stage_bytes() const { return GM_OP_BYTES + bn / 2 * GM_KB_BYTES; }
     __device__ __forceinline__ bool a_mn(const Tile&) const { return false; }
     __device__ __forceinline__ bool b_mn(const Tile&) const { return false; }
     __device__ __forceinline__ void load(const Tile& t, int kb, int rank, uint8_t* a, uint8_t* b, uint32_t bar) const {
         gm_tma_load(&map_x, a, bar, kb * GM_KB_BYTES, t.m0 + rank * GM_HALF);
-        gm_tma_load(&map_w, b, bar, kb * GM_KB_BYTES, t.n0 + rank * GM_HALF);
+        gm_tma_load(&map_w, b, bar, kb * GM_KB_BYTES, t.n0 + rank * (bn / 2));
     }
     // y of 32 columns from n on: the row's scale first, then the channel's
     __device__ __forceinline__ void scaled(uint32_t taddr, int n, float xscale, float* v) const {
@@ -132,27 +301,22 @@ struct I8Out : I8Base {
     // rows start on 16 bytes; all when rows are whole 16-byte pieces, else the
     // whole groups of columns (a clipped TMA store fills its last 16 bytes).
     int32_t staged;
-    __device__ __forceinline__ void epilogue(const State&, const Tile& t, uint32_t taddr, int r, int c0, const GmStage& sg) const {
+    __device__ __forceinline__ void epilogue(const State&, const Tile& t, uint32_t taddr, int r, int half, const GmStage& sg) const {
         constexpr int CW = 128 / sizeof(T);  // columns per staged store
-        const int row = t.m0 + r, lane = threadIdx.x & 31, row0 = row - lane;
+        const int row = t.m0 + r, lane = threadIdx.x & 31, row0 = row - lane, cols = max(bn / 2, 64);
         const float xscale = row < rows ? xs[row] : 0.f;
 #pragma unroll 1
-        for (int c = c0; c < c0 + GM_EPI_COLS && t.n0 + c < N; c += CW) {
+        for (int c = half * cols; c < min((half + 1) * cols, bn) && t.n0 + c < N; c += CW) {
             float v[CW];
 #pragma unroll
             for (int k = 0; k < CW; k += 32) scaled(taddr + (uint32_t)(c + k), t.n0 + c + k, xscale, v + k);
-            if (t.n0 + c < staged) {
-                if (row0 < rows) put(sg, lane, v, t.n0 + c, row0);
-            } else if (row < rows) {
-                gm_store(out + row * ldo + t.n0 + c, v, min(CW, N - t.n0 - c));
-            }
+            if (row0 >= rows) continue;
+            gm_put(sg, lane, v);
+            if (t.n0 + c < staged)
+                sg.send<false>(&map_out, lane, t.n0 + c, row0);
+            else
+                gm_write_plain(sg, lane, out + row0 * ldo + t.n0 + c, ldo, min(32, rows - row0), min(CW, N - t.n0 - c));
         }
-    }
-    __device__ __forceinline__ void put(const GmStage& sg, int lane, const float (&v)[64], int x, int y) const {
-        gm_stage64(sg, &map_out, lane, v, x, y);
-    }
-    __device__ __forceinline__ void put(const GmStage& sg, int lane, const float (&v)[32], int x, int y) const {
-        gm_stage32<false>(sg, &map_out, lane, v, x, y);
     }
 };
 
@@ -163,7 +327,8 @@ struct I8Lse : I8Base {
     int32_t n_parts;
     float* slice;     // [rows, sid_span]
     int32_t sid_base, sid_span;
-    __device__ __forceinline__ void epilogue(const State&, const Tile& t, uint32_t taddr, int r, int c0, const GmStage&) const {
+    __device__ __forceinline__ void epilogue(const State&, const Tile& t, uint32_t taddr, int r, int half, const GmStage&) const {
+        const int c0 = half * GM_EPI_COLS;
         const int row = t.m0 + r;
         const float xscale = row < rows ? xs[row] : 0.f;
         float m = -INFINITY, s = 0.f;
@@ -214,8 +379,9 @@ __global__ void __launch_bounds__(256) k_i8_combine(const float2* __restrict__ p
 struct fr_i8 {
     const int8_t* wq = nullptr;
     const float* ws = nullptr;
+    int64_t ldw = 0;
     int32_t N = 0, d = 0, max_rows = 0, sid_base = 0, sid_span = 0, n_tiles = 0, sms = 0, device = 0;
-    CUtensorMap map_w;
+    CUtensorMap map_w[3];  // boxes of 128, 64 and 32 rows: tiles of 256, 128 and 64 columns
     float2* partial = nullptr;  // [max_rows, 2 * n_tiles]
     int32_t* err = nullptr;
     cudaStream_t last_stream = nullptr;
@@ -230,14 +396,24 @@ bool i8_on_device(const fr_i8* h) {
     return cudaGetDevice(&dev) == cudaSuccess && dev == h->device;
 }
 
-fr_status i8_base(fr_i8* h, const int8_t* xq, int64_t ldx, const float* xs, int32_t rows, fr::I8Base* b) {
+fr_status i8_base(fr_i8* h, const int8_t* xq, int64_t ldx, const float* xs, int32_t rows, bool any_width, fr::I8Base* b) {
     if (!fr::gm_encode(&b->map_x, 1, xq, rows, h->d, ldx, fr::GM_HALF)) return FR_ERR_CUDA;
-    b->map_w = h->map_w;
+    // Tile width: the rounds that the pairs need times a tile's cost (its columns,
+    // and about 64 columns' worth of start and end).
+    const int64_t pairs = h->sms / 2, m_tiles = (rows + fr::GM_TILE - 1) / fr::GM_TILE;
+    int best = 0;
+    int64_t cost = INT64_MAX;
+    for (int k = 0; k < (any_width ? 3 : 1); ++k) {
+        const int64_t bn = fr::GM_TILE >> k, tiles = m_tiles * ((h->N + bn - 1) / bn), c = (tiles + pairs - 1) / pairs * (bn + 64);
+        if (c < cost) cost = c, best = k;
+    }
+    b->bn = fr::GM_TILE >> best;
+    b->map_w = h->map_w[best];
     b->rows = rows;
     b->N = h->N;
     b->k_blocks = (h->d + fr::GM_KB_BYTES - 1) / fr::GM_KB_BYTES;
-    b->m_tiles = (rows + fr::GM_TILE - 1) / fr::GM_TILE;
-    b->n_tiles = h->n_tiles;
+    b->m_tiles = (int32_t)m_tiles;
+    b->n_tiles = (h->N + b->bn - 1) / b->bn;
     b->xs = xs;
     b->ws = h->ws;
     b->ws_vec = (reinterpret_cast<uintptr_t>(h->ws) & 15u) == 0;
@@ -254,8 +430,20 @@ fr_status i8_launch(fr_i8* h, const P& p, cudaStream_t s) {
 template <class T>
 fr_status i8_out(fr_i8* h, const int8_t* xq, int64_t ldx, const float* xs, int32_t rows, void* out, int64_t ldo,
                  cudaStream_t s) {
+    if (rows <= fr::FEW_ROWS) {
+        // 1, 2 or 4 tokens at a time, as long as they fit into shared memory
+        const int R = rows <= 1 ? 1 : rows <= 2 ? 2 : 4;
+        const size_t smem = (size_t)R * ((h->d + 15) / 16 * 16);
+        if (smem <= (size_t)fr::FEW_SMEM) {
+            auto k = R == 1 ? fr::k_i8_few<1, T> : R == 2 ? fr::k_i8_few<2, T> : fr::k_i8_few<4, T>;
+            const int64_t groups = (h->N + fr::FEW_CH - 1) / fr::FEW_CH, warps = fr::FEW_THREADS / 32;
+            FR_CUDA_TRY(fr::launch_pdl(k, std::min<int64_t>((groups + warps - 1) / warps, 3 * (int64_t)h->sms), fr::FEW_THREADS,
+                                       smem, s, xq, ldx, xs, h->wq, h->ldw, h->ws, rows, h->N, h->d, (T*)out, ldo));
+            return FR_OK;
+        }
+    }
     fr::I8Out<T> p{};
-    const fr_status st = i8_base(h, xq, ldx, xs, rows, &p);
+    const fr_status st = i8_base(h, xq, ldx, xs, rows, true, &p);
     if (st != FR_OK) return st;
     p.out = (T*)out;
     p.ldo = ldo;
@@ -263,6 +451,15 @@ fr_status i8_out(fr_i8* h, const int8_t* xq, int64_t ldx, const float* xs, int32
         p.staged = fr::gm_staged_columns(h->N, sizeof(T));
     if (p.staged && !fr::gm_encode(&p.map_out, sizeof(T), out, rows, h->N, ldo * sizeof(T), 32)) return FR_ERR_CUDA;
     return i8_launch(h, p, s);
+}
+
+template <class T>
+cudaError_t i8_setup_few() {
+    for (auto k : {fr::k_i8_few<1, T>, fr::k_i8_few<2, T>, fr::k_i8_few<4, T>}) {
+        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, fr::FEW_SMEM);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 bool i8_bad_x(const fr_i8* h, const int8_t* xq, int64_t ldx, const float* xs, int32_t rows) {
@@ -281,13 +478,14 @@ extern "C" fr_status fr_i8_quantize(const void* x_dev, int64_t ldx, fr_dtype dty
         return FR_ERR_INVALID_ARG;
     if (rows == 0) return FR_OK;
     const cudaStream_t s = (cudaStream_t)stream;
-    const int64_t grid = ((int64_t)rows + 7) / 8;
+    const uintptr_t bytes = reinterpret_cast<uintptr_t>(x_dev) | (uintptr_t)(ldx * (dtype == FR_F32 ? 4 : 2));
+    const bool vec = bytes % 16 == 0 && (reinterpret_cast<uintptr_t>(q_dev) | (uintptr_t)ldq) % 8 == 0;
     if (dtype == FR_F32)
-        FR_CUDA_TRY(fr::launch_pdl(fr::k_i8_quantize<float>, grid, 256, 0, s, (const float*)x_dev, ldx, rows, d, q_dev,
-                                   ldq, scale_dev));
+        FR_CUDA_TRY(fr::launch_pdl(vec ? fr::k_i8_quantize<float, true> : fr::k_i8_quantize<float, false>, rows,
+                                   fr::QT_THREADS, 0, s, (const float*)x_dev, ldx, d, q_dev, ldq, scale_dev));
     else
-        FR_CUDA_TRY(fr::launch_pdl(fr::k_i8_quantize<__nv_bfloat16>, grid, 256, 0, s, (const __nv_bfloat16*)x_dev, ldx,
-                                   rows, d, q_dev, ldq, scale_dev));
+        FR_CUDA_TRY(fr::launch_pdl(vec ? fr::k_i8_quantize<__nv_bfloat16, true> : fr::k_i8_quantize<__nv_bfloat16, false>, rows,
+                                   fr::QT_THREADS, 0, s, (const __nv_bfloat16*)x_dev, ldx, d, q_dev, ldq, scale_dev));
     return FR_OK;
 }
 
@@ -304,6 +502,7 @@ extern "C" fr_status fr_i8_init(const int8_t* weight_dev, int64_t ldw, const flo
     if (!h) return FR_ERR_OOM;
     h->wq = weight_dev;
     h->ws = wscale_dev;
+    h->ldw = ldw;
     h->N = N;
     h->d = d;
     h->max_rows = max_rows;
@@ -312,7 +511,10 @@ extern "C" fr_status fr_i8_init(const int8_t* weight_dev, int64_t ldw, const flo
     h->n_tiles = (N + fr::GM_TILE - 1) / fr::GM_TILE;
     if (cudaGetDevice(&h->device) != cudaSuccess ||
         cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, h->device) != cudaSuccess ||
-        !fr::gm_encode(&h->map_w, 1, weight_dev, N, d, ldw, fr::GM_HALF) ||
+        !fr::gm_encode(&h->map_w[0], 1, weight_dev, N, d, ldw, fr::GM_HALF) ||
+        !fr::gm_encode(&h->map_w[1], 1, weight_dev, N, d, ldw, fr::GM_HALF / 2) ||
+        !fr::gm_encode(&h->map_w[2], 1, weight_dev, N, d, ldw, fr::GM_HALF / 4) ||
+        i8_setup_few<float>() != cudaSuccess || i8_setup_few<__nv_bfloat16>() != cudaSuccess ||
         fr::gm_setup(fr::k_i8<fr::I8Out<float>>) != cudaSuccess ||
         fr::gm_setup(fr::k_i8<fr::I8Out<__nv_bfloat16>>) != cudaSuccess || fr::gm_setup(fr::k_i8<fr::I8Lse>) != cudaSuccess) {
         (void)cudaGetLastError();
@@ -358,7 +560,7 @@ extern "C" fr_status fr_i8_lse(fr_i8* h, const int8_t* xq_dev, int64_t ldx, cons
     h->last_stream = s;
     if (rows == 0) return FR_OK;
     fr::I8Lse p{};
-    fr_status st = i8_base(h, xq_dev, ldx, xscale_dev, rows, &p);
+    fr_status st = i8_base(h, xq_dev, ldx, xscale_dev, rows, false, &p);
     if (st != FR_OK) return st;
     p.partial = h->partial;
     p.n_parts = 2 * h->n_tiles;
