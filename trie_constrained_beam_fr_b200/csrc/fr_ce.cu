@@ -186,8 +186,8 @@ struct CeLoss {
         return {n, n ? ce_m_tiles(n) : 0};
     }
     __device__ __forceinline__ int32_t* counter() const { return nullptr; }
-    __device__ __forceinline__ bool tile(const State& st, int64_t g, Tile& t) const {
-        if (g >= (int64_t)st.m_tiles * n_tiles) return false;
+    __device__ __forceinline__ bool tile(const State& st, uint32_t g, Tile& t) const {
+        if (g >= (uint32_t)st.m_tiles * (uint32_t)n_tiles) return false;
         int32_t m, n;
         gm_grouped(g, st.m_tiles, n_tiles, m, n);
         t.m0 = m * GM_TILE;
@@ -299,8 +299,8 @@ struct CeGrad {
     __device__ __forceinline__ int32_t* counter() const { return next_tile; }
     // The longest tiles first (dh or dW by their K stages, then G), so that the
     // short ones even out the pairs' ends.
-    __device__ __forceinline__ bool tile(const State& st, int64_t at, Tile& t) const {
-        if (at >= (int64_t)st.dh_tiles + st.dw_tiles + st.g_tiles) return false;
+    __device__ __forceinline__ bool tile(const State& st, uint32_t at, Tile& t) const {
+        if (at >= (uint32_t)(st.dh_tiles + st.dw_tiles + st.g_tiles)) return false;
         int g = (int)at;
         if (st.dw_first && g < st.dh_tiles + st.dw_tiles) g += g < st.dw_tiles ? st.dh_tiles : -st.dw_tiles;
         if (g < st.dh_tiles) {
@@ -513,7 +513,7 @@ bool ce_on_device(const fr_ce* h) {
 extern "C" fr_status fr_ce_init(int32_t V, int32_t d, int32_t max_rows, fr_ce** out) {
     if (!out) return FR_ERR_INVALID_ARG;
     *out = nullptr;
-    if (V < 1 || d < 1 || max_rows < 1 || max_rows > (1 << 24)) return FR_ERR_INVALID_ARG;
+    if (V < 1 || d < 1 || max_rows < 1 || max_rows > (1 << 24) || V > (1 << 24)) return FR_ERR_INVALID_ARG;
     fr_ce* h = new (std::nothrow) fr_ce();
     if (!h) return FR_ERR_OOM;
     h->V = V;

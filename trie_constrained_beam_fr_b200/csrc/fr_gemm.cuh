@@ -24,7 +24,7 @@
 //     struct Tile { int nk; uint32_t idesc; ... };   // K stages; instruction descriptor
 //     struct State { ... };                          // what begin() read after the previous kernel
 //     __device__ State begin() const;
-//     __device__ bool tile(const State&, int64_t g, Tile&) const;   // tile g of the launch; false behind the last
+//     __device__ bool tile(const State&, uint32_t g, Tile&) const;  // tile g (< 2^31) of the launch; false behind the last
 //     __device__ int32_t* counter() const;           // DYNAMIC: zero before the launch; tiles fit an int32
 //     __device__ void load(const Tile&, int kb, int rank, uint8_t* a, uint8_t* b, uint32_t bar) const;
 //     __device__ uint32_t stage_bytes() const;       // that load() copies per CTA
@@ -221,11 +221,11 @@ struct GmSmem {
 // Tile g of an m_tiles x n_tiles grid, m fastest within groups of 32 tile rows:
 // pairs running together share the B tile, and the A tiles of a group (8,192
 // rows) stay in L2 while B passes by.
-__device__ __forceinline__ void gm_grouped(int64_t g, int32_t m_tiles, int32_t n_tiles, int32_t& m, int32_t& n) {
-    const int32_t group = (int32_t)(g / (32 * (int64_t)n_tiles)), m0 = group * 32, rows = min(32, m_tiles - m0);
-    const int32_t at = (int32_t)(g - (int64_t)m0 * n_tiles);
-    m = m0 + at % rows;
-    n = at / rows;
+__device__ __forceinline__ void gm_grouped(uint32_t g, uint32_t m_tiles, uint32_t n_tiles, int32_t& m, int32_t& n) {
+    const uint32_t group = m_tiles <= 32 ? 0 : g / (32 * n_tiles), m0 = group * 32, rows = min(32u, m_tiles - m0);
+    const uint32_t at = g - m0 * n_tiles, q = at / rows;
+    m = (int32_t)(m0 + at - q * rows);
+    n = (int32_t)q;
 }
 
 // What every policy's kernel passes along.
@@ -252,7 +252,7 @@ __device__ __forceinline__ void gm_run(const P& p, const GmCtl& ctl) {
     volatile int32_t* abort_flag = &sm->abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = gm_cta_rank();
-    const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const uint32_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -309,8 +309,8 @@ __device__ __forceinline__ void gm_run(const P& p, const GmCtl& ctl) {
     // The first CTA's producer publishes the tile after the one that it takes
     // itself, so that nobody waits for it, and asks for the one behind that,
     // whose answer comes while this one is copied.  The first two are static.
-    int64_t cur = pair, coming = pair + pairs;
-    const auto publish = [&](int i, int64_t g) -> bool {
+    uint32_t cur = pair, coming = pair + pairs;
+    const auto publish = [&](int i, uint32_t g) -> bool {
         const int s = i % GM_SLOTS;
         if (i >= GM_SLOTS &&
             !gm_wait_pair(&sm->tile_empty[s], ((i / GM_SLOTS) & 1) ^ 1, abort_flag, ctl.err, ctl.wait_ns))
@@ -329,7 +329,7 @@ __device__ __forceinline__ void gm_run(const P& p, const GmCtl& ctl) {
         if (!p.tile(st, cur, t)) return false;
         if (!publish(i + 1, coming)) return false;
         cur = coming;
-        coming = atomicAdd(p.counter(), 1) + 2 * pairs;
+        coming = (uint32_t)atomicAdd(p.counter(), 1) + 2 * pairs;
         return true;
     };
     if (warp == 0) {
@@ -365,15 +365,17 @@ __device__ __forceinline__ void gm_run(const P& p, const GmCtl& ctl) {
         if (lane == 0 && rank == 0) {
             uint32_t it = 0;
             bool ok = true;
-            for (int i = 0; ok && next(i, false); ++i) {
+            bool more = next(0, false);
+            for (int i = 0; ok && more; ++i) {
+                const typename P::Tile now = t;
                 const int acc = i & 1;
                 if (i >= 2 && !tc_wait(&sm->tmem_empty[acc], ((i >> 1) & 1) ^ 1, abort_flag, ctl.err, ctl.wait_ns)) break;
                 tc_fence_after();
                 const uint32_t d_tmem = tmem + (uint32_t)(acc * GM_TILE);
-                const bool amn = p.a_mn(t), bmn = p.b_mn(t);
+                const bool amn = p.a_mn(now), bmn = p.b_mn(now);
                 // address fields count 16-byte units: the K slices are 32 bytes (K-major) or 2,048 (MN-major) apart
                 const uint32_t ia = amn ? 2048 >> 4 : 32 >> 4, ib = bmn ? 2048 >> 4 : 32 >> 4;
-                for (int kb = 0; kb < t.nk; ++kb, ++it) {
+                for (int kb = 0; kb < now.nk; ++kb, ++it) {
                     const uint32_t s = it % STAGES;
                     if (!tc_wait(&sm->full[s], (it / STAGES) & 1u, abort_flag, ctl.err, ctl.wait_ns)) {
                         ok = false;
@@ -385,10 +387,13 @@ __device__ __forceinline__ void gm_run(const P& p, const GmCtl& ctl) {
                     const uint64_t db = bmn ? smem_desc_mn_sw128(sb) : smem_desc_sw128(sb);
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        gm_umma<P::I8>(d_tmem, da + (uint64_t)(kk * ia), db + (uint64_t)(kk * ib), t.idesc,
+                        gm_umma<P::I8>(d_tmem, da + (uint64_t)(kk * ia), db + (uint64_t)(kk * ib), now.idesc,
                                        (kb | kk) != 0 ? 1u : 0u);
                     gm_commit_both(&sm->empty[s]);  // the stage is free in both CTAs once these products are done
+                    // worked out while this tile's products run
+                    if (!P::DYNAMIC && kb == 0) more = next(i + 1, false);
                 }
+                if (P::DYNAMIC || now.nk == 0) more = ok && next(i + 1, false);
                 gm_commit_both(&sm->tmem_full[acc]);  // the accumulators are complete (or, on abort, quiet)
             }
             // the tensor memory is freed only after every product issued here is done

@@ -253,8 +253,8 @@ struct I8Base {
     int32_t ws_vec;  // ws starts on 16 bytes
 
     __device__ __forceinline__ State begin() const { return {}; }
-    __device__ __forceinline__ bool tile(const State&, int64_t g, Tile& t) const {
-        if (g >= (int64_t)m_tiles * n_tiles) return false;
+    __device__ __forceinline__ bool tile(const State&, uint32_t g, Tile& t) const {
+        if (g >= (uint32_t)m_tiles * (uint32_t)n_tiles) return false;
         int32_t m, n;
         gm_grouped(g, m_tiles, n_tiles, m, n);
         t.m0 = m * GM_TILE;
@@ -272,21 +272,18 @@ struct I8Base {
     }
     // y of 32 columns from n on: the row's scale first, then the channel's
     __device__ __forceinline__ void scaled(uint32_t taddr, int n, float xscale, float* v) const {
-        int32_t acc[32];
-        gm_ld32_i32(taddr, acc);
+        float4 w[8];  // loaded before the accumulator is waited for
         if (ws_vec && n + 32 <= N) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-                const float4 w = __ldg(reinterpret_cast<const float4*>(ws + n + i));
-                v[i] = (float)acc[i] * xscale * w.x;
-                v[i + 1] = (float)acc[i + 1] * xscale * w.y;
-                v[i + 2] = (float)acc[i + 2] * xscale * w.z;
-                v[i + 3] = (float)acc[i + 3] * xscale * w.w;
-            }
+            for (int i = 0; i < 8; ++i) w[i] = __ldg(reinterpret_cast<const float4*>(ws + n) + i);
         } else {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = n + i < N ? (float)acc[i] * xscale * __ldg(ws + n + i) : 0.f;
+            for (int i = 0; i < 32; ++i) (&w[i / 4].x)[i % 4] = n + i < N ? __ldg(ws + n + i) : 0.f;
         }
+        int32_t acc[32];
+        gm_ld32_i32(taddr, acc);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = (float)acc[i] * xscale * (&w[i / 4].x)[i % 4];
     }
 };
 
@@ -494,7 +491,7 @@ extern "C" fr_status fr_i8_init(const int8_t* weight_dev, int64_t ldw, const flo
     if (!out) return FR_ERR_INVALID_ARG;
     *out = nullptr;
     if (!weight_dev || !wscale_dev || N < 1 || d < 1 || d > 131071 || ldw < d || max_rows < 1 || sid_base < 0 ||
-        sid_span < 0 || (int64_t)sid_base + sid_span > N)
+        sid_span < 0 || (int64_t)sid_base + sid_span > N || max_rows > (1 << 24) || N > (1 << 24))
         return FR_ERR_INVALID_ARG;
     if ((reinterpret_cast<uintptr_t>(weight_dev) & 15u) || (ldw & 15) || (reinterpret_cast<uintptr_t>(wscale_dev) & 3u))
         return FR_ERR_INVALID_ARG;
