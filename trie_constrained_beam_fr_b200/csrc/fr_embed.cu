@@ -11,8 +11,8 @@
 //   k_em_small    the gradient of up to 1,024 tokens in one kernel.
 //   k_em_hist / k_em_scatter   otherwise a stable radix sort of the tokens with
 //                 their positions, 9 bits a pass (two passes for V < 2^18).
-//   k_em_sum      the sorted positions in chunks of EM_CHUNK: a CTA adds the
-//                 rows of a chunk, a column group per thread, and writes the
+//   k_em_sum      the sorted positions in chunks of EM_CHUNK: a CTA adds a
+//                 chunk's rows, a column group per thread, and writes the
 //                 finished tokens; a token that reaches over a chunk's edge
 //                 leaves fp32 partials, which the last of its chunks adds in
 //                 order.  More CTAs zero the rows that no token fell on.
@@ -40,7 +40,8 @@ constexpr int EM_TILE = 1024;       // tokens that a sorting CTA ranks at a time
 constexpr int EM_BITS = 9;          // most digit bits of a sort pass
 constexpr int EM_SORT_CTAS = 128;   // most CTAs of a sort pass
 constexpr int EM_CHUNK = 32;        // sorted positions per CTA of the sum
-constexpr int EM_UNROLL = 4;        // rows in flight per thread of the sum
+template <int VEC>
+constexpr int EM_UNROLL = VEC == 8 ? 4 : 16;  // rows in flight per thread of the sum
 constexpr int EM_ZERO_ROWS = 128;   // table rows per CTA that zeros
 constexpr int EM_SMALL = 1024;      // most tokens of the gradient in one kernel
 constexpr int EM_SMALL_THREADS = 128;
@@ -137,13 +138,13 @@ __device__ __forceinline__ uint32_t em_match(uint32_t digit, int bits, bool live
 __global__ void __launch_bounds__(EM_THREADS) k_em_hist(const int32_t* __restrict__ tokens,
                                                         const uint32_t* __restrict__ kin, int32_t n, int32_t per, int32_t V,
                                                         int32_t shift, int32_t bits, int32_t* __restrict__ counts,
-                                                        int32_t* __restrict__ err, int32_t* __restrict__ arrived, int32_t chunks) {
+                                                        int32_t* __restrict__ err, int32_t* __restrict__ arrived, int64_t n_arrived) {
     __shared__ int32_t h[1 << EM_BITS];
     griddep_wait();
     griddep_launch_dependents();
     const int bins = 1 << bits;
     for (int b = threadIdx.x; b < bins; b += EM_THREADS) h[b] = 0;
-    for (int32_t c = blockIdx.x * EM_THREADS + threadIdx.x; c < chunks; c += gridDim.x * EM_THREADS) arrived[c] = 0;
+    for (int64_t c = blockIdx.x * EM_THREADS + threadIdx.x; c < n_arrived; c += gridDim.x * EM_THREADS) arrived[c] = 0;
     __syncthreads();
     const int64_t i0 = (int64_t)blockIdx.x * per, i1 = min(i0 + per, (int64_t)n);
 #pragma unroll 4
@@ -291,20 +292,20 @@ __device__ __forceinline__ int32_t em_lower_bound(const uint32_t* __restrict__ k
 // begins here and goes on.  The last of a run's chunks to arrive adds its
 // partials in chunk order, so the sum does not depend on which that is.  The
 // CTAs behind the chunks' zero the rows that no token fell on, beside the
-// sums' reads.
+// sums' reads.  Grid: chunks x column blocks, then the zeroing CTAs.
 template <class TG, class TT, int VEC>
 __global__ void __launch_bounds__(EM_THREADS)
     k_em_sum(const TG* __restrict__ grad, int64_t ldg, int32_t d, const uint32_t* __restrict__ keys,
              const int32_t* __restrict__ order, int32_t n, int32_t V, float scale, TT* __restrict__ table, int64_t ldt,
-             int32_t accumulate, float* part, int64_t pitch, int32_t* arrived, int32_t chunks) {
+             int32_t accumulate, float* part, int64_t pitch, int32_t* arrived, int32_t chunks, int32_t blocks) {
     __shared__ uint8_t touched[EM_ZERO_ROWS];
     __shared__ uint32_t key_s[EM_CHUNK + 2];  // the chunk's keys between its neighbours'
     __shared__ int32_t ord_s[EM_CHUNK];
     __shared__ int32_t last_s;
     griddep_wait();
     griddep_launch_dependents();
-    if ((int)blockIdx.x >= chunks) {
-        const int32_t v0 = (blockIdx.x - chunks) * EM_ZERO_ROWS, v1 = min(v0 + EM_ZERO_ROWS, V);
+    if (blockIdx.x >= (uint32_t)chunks * blocks) {
+        const int32_t v0 = (blockIdx.x - chunks * blocks) * EM_ZERO_ROWS, v1 = min(v0 + EM_ZERO_ROWS, V);
         for (int k = threadIdx.x; k < EM_ZERO_ROWS; k += EM_THREADS) touched[k] = 0;
         __syncthreads();
         const int32_t end = em_lower_bound(keys, n, (uint32_t)v1);
@@ -313,7 +314,9 @@ __global__ void __launch_bounds__(EM_THREADS)
         em_zero_rows<TT, VEC>(table, ldt, d, v0, v1, touched);
         return;
     }
-    const int64_t i0 = (int64_t)blockIdx.x * EM_CHUNK;
+    const int32_t chunk = blockIdx.x / blocks, block = blockIdx.x - chunk * blocks;
+    const int64_t i0 = (int64_t)chunk * EM_CHUNK;
+    const int32_t j = (block * EM_THREADS + threadIdx.x) * VEC;  // this thread's columns
     for (int k = threadIdx.x; k < EM_CHUNK + 2; k += EM_THREADS) {
         const int64_t i = i0 + k - 1;
         key_s[k] = i >= 0 && i < n ? keys[i] : 0xFFFFFFFFu;
@@ -324,18 +327,19 @@ __global__ void __launch_bounds__(EM_THREADS)
     while (m > 0 && key_s[m] >= (uint32_t)V) --m;  // tokens that do not count are sorted last
     if (m == 0) return;
     const bool head = key_s[0] == key_s[1], tail = key_s[m + 1] == key_s[m];
-    for (int32_t j = threadIdx.x * VEC; j < d; j += EM_THREADS * VEC) {
+    if (j < d) {
         float sum[VEC];
 #pragma unroll
         for (int q = 0; q < VEC; ++q) sum[q] = 0.f;
         bool from_before = head;
-        for (int k0 = 0; k0 < m; k0 += EM_UNROLL) {
-            float v[EM_UNROLL][VEC];
+        constexpr int U = EM_UNROLL<VEC>;
+        for (int k0 = 0; k0 < m; k0 += U) {
+            float v[U][VEC];
 #pragma unroll
-            for (int u = 0; u < EM_UNROLL; ++u)
+            for (int u = 0; u < U; ++u)
                 if (k0 + u < m) em_load<VEC>(grad + (int64_t)ord_s[k0 + u] * ldg + j, v[u]);
 #pragma unroll
-            for (int u = 0; u < EM_UNROLL; ++u) {
+            for (int u = 0; u < U; ++u) {
                 const int k = k0 + u;
                 if (k >= m) break;
                 const uint32_t key = key_s[k + 1];
@@ -346,7 +350,7 @@ __global__ void __launch_bounds__(EM_THREADS)
                     if (ends && !from_before)
                         em_write<TT, VEC>(table + (int64_t)key * ldt + j, sum, scale, accumulate != 0);
                     else
-                        em_store<VEC>(part + (2 * (int64_t)blockIdx.x + (from_before ? 0 : 1)) * pitch + j, sum);
+                        em_store<VEC>(part + (2 * (int64_t)chunk + (from_before ? 0 : 1)) * pitch + j, sum);
                     from_before = false;
 #pragma unroll
                     for (int q = 0; q < VEC; ++q) sum[q] = 0.f;
@@ -363,14 +367,14 @@ __global__ void __launch_bounds__(EM_THREADS)
         const int64_t c = em_lower_bound(keys, n, key) / EM_CHUNK, e = (em_lower_bound(keys, n, key + 1) - 1) / EM_CHUNK;
         __threadfence();
         __syncthreads();
-        if (threadIdx.x == 0) last_s = atomicAdd(&arrived[c], 1) == (int32_t)(e - c);
+        if (threadIdx.x == 0) last_s = atomicAdd(&arrived[c * blocks + block], 1) == (int32_t)(e - c);
         __syncthreads();
         if (!last_s) continue;
         __threadfence();
-        for (int32_t j = threadIdx.x * VEC; j < d; j += EM_THREADS * VEC) {
+        if (j < d) {
             float sum[VEC];
             em_load<VEC>(part + (2 * c + 1) * pitch + j, sum);
-#pragma unroll 4
+#pragma unroll 8
             for (int64_t k = c + 1; k <= e; ++k) {
                 float v[VEC];
                 em_load<VEC>(part + 2 * k * pitch + j, v);
@@ -469,7 +473,7 @@ struct fr_embed {
     int32_t* pos[2] = {};
     int32_t* counts = nullptr;
     float* part = nullptr;       // [2 * chunks, pitch]
-    int32_t* arrived = nullptr;  // [chunks] chunks of a run that have arrived, at its first chunk
+    int32_t* arrived = nullptr;  // [chunks, column blocks] chunks of a run that have arrived, at its first chunk
     int64_t pitch = 0;
     int32_t* err = nullptr;
     cudaStream_t last_stream = nullptr;
@@ -522,7 +526,7 @@ cudaError_t em_sort(fr_embed* h, const int32_t* tokens, int32_t n, const uint32_
         const uint32_t* kin = p ? h->keys[(p - 1) & 1] : nullptr;
         const int32_t* pin = p ? h->pos[(p - 1) & 1] : nullptr;
         cudaError_t e = fr::launch_pdl(fr::k_em_hist, ctas, fr::EM_THREADS, 0, s, tokens, kin, n, per, h->V, p * bits, bits,
-                                       h->counts, h->err, h->arrived, p ? 0 : (int32_t)em_ceil(n, fr::EM_CHUNK));
+                                       h->counts, h->err, h->arrived, p ? 0 : em_ceil(n, fr::EM_CHUNK) * em_ceil(h->d, fr::EM_THREADS));
         if (e != cudaSuccess) return e;
         e = fr::launch_pdl(fr::k_em_scatter, ctas, fr::EM_THREADS, 0, s, tokens, kin, pin, n, per, h->V, p * bits, bits,
                            (const int32_t*)h->counts, h->keys[p & 1], h->pos[p & 1], h->err);
@@ -547,9 +551,9 @@ cudaError_t em_grad(fr_embed* h, const void* grad, int64_t ldg, const int32_t* t
     const int32_t* order;
     cudaError_t e = em_sort(h, tokens, n, &keys, &order, s);
     if (e != cudaSuccess) return e;
-    const int64_t chunks = em_ceil(n, fr::EM_CHUNK);
-    return fr::launch_pdl(fr::k_em_sum<TG, TT, VEC>, chunks + zeros, fr::EM_THREADS, 0, s, (const TG*)grad, ldg, h->d, keys,
-                          order, n, h->V, scale, (TT*)table, ldt, accumulate, h->part, h->pitch, h->arrived, (int32_t)chunks);
+    const int64_t chunks = em_ceil(n, fr::EM_CHUNK), wide = em_ceil(h->d, fr::EM_THREADS * VEC);
+    return fr::launch_pdl(fr::k_em_sum<TG, TT, VEC>, chunks * wide + zeros, fr::EM_THREADS, 0, s, (const TG*)grad, ldg, h->d, keys,
+                          order, n, h->V, scale, (TT*)table, ldt, accumulate, h->part, h->pitch, h->arrived, (int32_t)chunks, (int32_t)wide);
 }
 
 template <class TG, class TT>
@@ -579,7 +583,7 @@ extern "C" fr_status fr_embed_init(int32_t V, int32_t d, int32_t max_tokens, fr_
     }
     const int64_t n = max_tokens;
     cudaError_t e = cudaMalloc(&h->keys[0], n * 16);
-    if (e == cudaSuccess) e = cudaMalloc(&h->counts, ((fr::EM_SORT_CTAS << fr::EM_BITS) + em_ceil(n, fr::EM_CHUNK)) * sizeof(int32_t));
+    if (e == cudaSuccess) e = cudaMalloc(&h->counts, ((size_t)(fr::EM_SORT_CTAS << fr::EM_BITS) + em_ceil(n, fr::EM_CHUNK) * em_ceil(d, fr::EM_THREADS)) * sizeof(int32_t));
     if (e == cudaSuccess) e = cudaMalloc(&h->part, (size_t)em_ceil(n, fr::EM_CHUNK) * 2 * h->pitch * 4);
     if (e == cudaSuccess) e = cudaMalloc(&h->err, sizeof(int32_t));
     if (e == cudaSuccess) e = cudaMemset(h->err, 0, sizeof(int32_t));
