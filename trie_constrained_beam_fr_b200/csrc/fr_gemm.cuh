@@ -118,7 +118,15 @@ __device__ __forceinline__ uint32_t gm_in_first(const void* p) {
     return a;
 }
 
+// Arrives on the other CTA's barrier after reads (of tensor memory, of a slot):
+// releasing this CTA's writes to the cluster as well would wait for its stores
+// on their way (a quarter of a dW tile's time with few rows).
 __device__ __forceinline__ void gm_arrive_remote(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// Arrives on the other CTA's barrier and publishes this thread's writes.
+__device__ __forceinline__ void gm_publish_remote(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
@@ -319,7 +327,7 @@ __device__ __forceinline__ void gm_run(const P& p, const GmCtl& ctl) {
         tc_arrive(&sm->tile_full[s]);
         asm volatile("st.relaxed.cluster.shared::cluster.s32 [%0], %1;" ::"r"(gm_in_cta(&sm->tile_id[s], 1)), "r"((int32_t)g)
                      : "memory");
-        gm_arrive_remote(gm_in_cta(&sm->tile_full[s], 1));
+        gm_publish_remote(gm_in_cta(&sm->tile_full[s], 1));
         return true;
     };
     const auto take = [&](int i) -> bool {
