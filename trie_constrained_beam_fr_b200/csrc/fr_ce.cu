@@ -165,9 +165,28 @@ __global__ void __launch_bounds__(CE_GATHER_THREADS)
     }
 }
 
+// Rows of a tile: a pair's, or a single CTA's where there are at most 128 rows.
+template <bool PAIR_>
+constexpr int CE_TM = PAIR_ ? GM_TILE : GM_HALF;
+
+// A copy of 256 rows of a K-major B operand: a CTA's half, or all of them.
+template <bool PAIR_>
+__device__ __forceinline__ void ce_load_b(const CUtensorMap* map, uint8_t* b, uint32_t bar, int k, int n, int rank) {
+    gm_tma_load<PAIR_>(map, b, bar, k, n + rank * GM_HALF);
+    if constexpr (!PAIR_) gm_tma_load<PAIR_>(map, b + GM_OP_BYTES, bar, k, n + GM_HALF);
+}
+
+// The same of an MN-major B operand: 64 columns a box.
+template <bool PAIR_>
+__device__ __forceinline__ void ce_load_b_mn(const CUtensorMap* map, uint8_t* b, uint32_t bar, int n, int k, int rank) {
+#pragma unroll
+    for (int j = 0; j < (PAIR_ ? 2 : 4); ++j) gm_tma_load<PAIR_>(map, b + j * 8192, bar, n + rank * GM_HALF + j * 64, k);
+}
+
+template <bool PAIR_>
 struct CeLoss {
-    static constexpr bool I8 = false, STAGED = false, DYNAMIC = false;
-    static constexpr int STAGES = 7;
+    static constexpr bool I8 = false, STAGED = false, DYNAMIC = false, PAIR = PAIR_;
+    static constexpr int STAGES = PAIR ? 7 : 4, TM = CE_TM<PAIR_>;
     struct Tile {
         int nk, m0, n0;
         uint32_t idesc;
@@ -183,25 +202,25 @@ struct CeLoss {
 
     __device__ __forceinline__ State begin() const {
         const int32_t n = *rows.n;
-        return {n, n ? ce_m_tiles(n) : 0};
+        return {n, (n + TM - 1) / TM};
     }
     __device__ __forceinline__ int32_t* counter() const { return nullptr; }
     __device__ __forceinline__ bool tile(const State& st, uint32_t g, Tile& t) const {
         if (g >= (uint32_t)st.m_tiles * (uint32_t)n_tiles) return false;
         int32_t m, n;
         gm_grouped(g, st.m_tiles, n_tiles, m, n);
-        t.m0 = m * GM_TILE;
+        t.m0 = m * TM;
         t.n0 = n * GM_TILE;
         t.nk = k_blocks;
-        t.idesc = gm_idesc(false);
+        t.idesc = gm_idesc(false, PAIR);
         return true;
     }
-    __device__ __forceinline__ uint32_t stage_bytes() const { return 2 * GM_OP_BYTES; }
+    __device__ __forceinline__ uint32_t stage_bytes() const { return (PAIR ? 2 : 3) * GM_OP_BYTES; }
     __device__ __forceinline__ bool a_mn(const Tile&) const { return false; }
     __device__ __forceinline__ bool b_mn(const Tile&) const { return false; }
     __device__ __forceinline__ void load(const Tile& t, int kb, int rank, uint8_t* a, uint8_t* b, uint32_t bar) const {
-        gm_tma_load(&map_h, a, bar, kb * 64, t.m0 + rank * GM_HALF);
-        gm_tma_load(&map_w, b, bar, kb * 64, t.n0 + rank * GM_HALF);
+        gm_tma_load<PAIR>(&map_h, a, bar, kb * 64, t.m0 + rank * GM_HALF);
+        ce_load_b<PAIR>(&map_w, b, bar, kb * 64, t.n0, rank);
     }
     __device__ __forceinline__ void epilogue(const State& st, const Tile& t, uint32_t taddr, int r, int half, const GmStage&) const {
         const int c0 = half * GM_EPI_COLS;
@@ -231,7 +250,8 @@ struct CeLoss {
     }
 };
 
-__global__ void __launch_bounds__(GM_THREADS, 1) k_ce_loss(const __grid_constant__ CeLoss p, const GmCtl ctl) {
+template <class P>
+__global__ void __launch_bounds__(GM_THREADS, 1) k_ce_loss(const __grid_constant__ P p, const GmCtl ctl) {
     gm_run(p, ctl);
 }
 
@@ -254,9 +274,10 @@ __global__ void __launch_bounds__(256) k_ce_combine(const float2* __restrict__ p
 // One launch of the gradient: the products of one piece (tokens [v0, v1),
 // G in buffer `buf`) and the G tiles of the next (tokens [w0, w1), buffer
 // buf ^ 1).  Empty ranges leave their part out.
+template <bool PAIR_>
 struct CeGrad {
-    static constexpr bool I8 = false, STAGED = true, DYNAMIC = true;
-    static constexpr int STAGES = 6;
+    static constexpr bool I8 = false, STAGED = true, DYNAMIC = true, PAIR = PAIR_;
+    static constexpr int STAGES = PAIR ? 6 : 4, TM = CE_TM<PAIR_>;
     enum { DH, DW, GT };
     struct Tile {
         int nk, type, m0, n0, k0, split;
@@ -287,9 +308,9 @@ struct CeGrad {
         st.n = *rows.n;
         st.gmax = *rows.gmax;
         st.ginv = st.gmax > 0.f ? 1.f / st.gmax : 0.f;
-        st.m_tiles = ce_m_tiles(st.n);
+        st.m_tiles = max((st.n + TM - 1) / TM, 1);
         st.dh_tiles = dh && v1 > v0 && st.n ? st.m_tiles * d_tiles * splits : 0;
-        st.dw_tiles = dw && v1 > v0 ? (v1 - v0 + GM_TILE - 1) / GM_TILE * d_tiles : 0;
+        st.dw_tiles = dw && v1 > v0 ? (v1 - v0 + TM - 1) / TM * d_tiles : 0;
         st.g_tiles = w1 > w0 ? (w1 - w0 + GM_TILE - 1) / GM_TILE * st.m_tiles : 0;
         st.dw_nk = max((st.n + 63) / 64, 1);
         st.dh_per = ((v1 - v0 + 63) / 64 + splits - 1) / splits;
@@ -309,51 +330,49 @@ struct CeGrad {
             // d fastest: pairs running together read each row of G once
             t.n0 = g % d_tiles * GM_TILE;
             g /= d_tiles;
-            t.m0 = g % st.m_tiles * GM_TILE;
+            t.m0 = g % st.m_tiles * TM;
             t.split = g / st.m_tiles;
             t.k0 = t.split * per;
             t.nk = max(min(per, kb - t.k0), 0);
-            t.idesc = gm_idesc(false, false, true);
+            t.idesc = gm_idesc(false, PAIR, false, true);
             return true;
         }
         g -= st.dh_tiles;
         if (g < st.dw_tiles) {
             t.type = DW;
             t.n0 = g % d_tiles * GM_TILE;
-            t.m0 = g / d_tiles * GM_TILE;
+            t.m0 = g / d_tiles * TM;
             t.k0 = 0;
             t.nk = st.dw_nk;
-            t.idesc = gm_idesc(false, true, true);
+            t.idesc = gm_idesc(false, PAIR, true, true);
             return true;
         }
         g -= st.dw_tiles;
         t.type = GT;
         int32_t m, n;
         gm_grouped(g, st.m_tiles, (w1 - w0 + GM_TILE - 1) / GM_TILE, m, n);
-        t.m0 = m * GM_TILE;
+        t.m0 = m * TM;
         t.n0 = n * GM_TILE;
         t.k0 = 0;
         t.nk = (d + 63) / 64;
-        t.idesc = gm_idesc(false);
+        t.idesc = gm_idesc(false, PAIR);
         return true;
     }
-    __device__ __forceinline__ uint32_t stage_bytes() const { return 2 * GM_OP_BYTES; }
+    __device__ __forceinline__ uint32_t stage_bytes() const { return (PAIR ? 2 : 3) * GM_OP_BYTES; }
     __device__ __forceinline__ bool a_mn(const Tile& t) const { return t.type == DW; }
     __device__ __forceinline__ bool b_mn(const Tile& t) const { return t.type != GT; }
     __device__ __forceinline__ void load(const Tile& t, int kb, int rank, uint8_t* a, uint8_t* b, uint32_t bar) const {
-        const int k = (t.k0 + kb) * 64, m = t.m0 + rank * GM_HALF, n = t.n0 + rank * GM_HALF;
+        const int k = (t.k0 + kb) * 64, m = t.m0 + rank * GM_HALF;
         if (t.type == GT) {
-            gm_tma_load(&map_h_k, a, bar, k, m);
-            gm_tma_load(&map_w_k, b, bar, k, w0 + n);
+            gm_tma_load<PAIR>(&map_h_k, a, bar, k, m);
+            ce_load_b<PAIR>(&map_w_k, b, bar, k, w0 + t.n0, rank);
         } else if (t.type == DH) {
-            gm_tma_load(&map_g_k, a, bar, k, m);
-            gm_tma_load(&map_w_mn, b, bar, n, v0 + k);
-            gm_tma_load(&map_w_mn, b + 8192, bar, n + 64, v0 + k);
+            gm_tma_load<PAIR>(&map_g_k, a, bar, k, m);
+            ce_load_b_mn<PAIR>(&map_w_mn, b, bar, t.n0, v0 + k, rank);
         } else {
-            gm_tma_load(&map_g_mn, a, bar, m, k);
-            gm_tma_load(&map_g_mn, a + 8192, bar, m + 64, k);
-            gm_tma_load(&map_h_mn, b, bar, n, k);
-            gm_tma_load(&map_h_mn, b + 8192, bar, n + 64, k);
+            gm_tma_load<PAIR>(&map_g_mn, a, bar, m, k);
+            gm_tma_load<PAIR>(&map_g_mn, a + 8192, bar, m + 64, k);
+            ce_load_b_mn<PAIR>(&map_h_mn, b, bar, t.n0, k, rank);
         }
     }
     __device__ __forceinline__ void epilogue(const State& st, const Tile& t, uint32_t taddr, int r, int half, const GmStage& sg) const {
@@ -413,7 +432,8 @@ struct CeGrad {
     }
 };
 
-__global__ void __launch_bounds__(GM_THREADS, 1) k_ce_grad(const __grid_constant__ CeGrad p, const GmCtl ctl) {
+template <class P>
+__global__ void __launch_bounds__(GM_THREADS, 1) k_ce_grad(const __grid_constant__ P p, const GmCtl ctl) {
     gm_run(p, ctl);
 }
 
@@ -457,10 +477,10 @@ __global__ void __launch_bounds__(256) k_ce_finish(const float* __restrict__ dh,
 
 int64_t ce_round(int64_t x, int64_t q) { return (x + q - 1) / q * q; }
 
-// Splits of dh's token axis within a piece: about four tiles for every pair of
-// SMs when there are few rows (then dh's tiles are few and long).
-int32_t ce_splits(int32_t pairs, int64_t m_tiles, int64_t d_tiles) {
-    return (int32_t)std::max<int64_t>(1, std::min<int64_t>(16, 4 * pairs / (m_tiles * d_tiles)));
+// Splits of dh's token axis within a piece: about four tiles for every unit (pair
+// or single CTA) when there are few rows (then dh's tiles are few and long).
+int32_t ce_splits(int32_t units, int64_t m_tiles, int64_t d_tiles) {
+    return (int32_t)std::max<int64_t>(1, std::min<int64_t>(32, 4 * units / (m_tiles * d_tiles)));
 }
 
 }  // namespace
@@ -508,12 +528,103 @@ bool ce_on_device(const fr_ce* h) {
     return cudaGetDevice(&dev) == cudaSuccess && dev == h->device;
 }
 
+template <bool PAIR>
+fr_status ce_run_loss(fr_ce* h, const void* hidden_dev, int64_t ldh, const void* weight_dev, int64_t ldw,
+                      const int32_t* targets_dev, int32_t rows, float* loss_dev, float* lse_dev, cudaStream_t s) {
+    constexpr int TM = fr::CE_TM<PAIR>;
+    fr::CeLoss<PAIR> p{};
+    if (!fr::gm_encode(&p.map_w, 2, weight_dev, h->V, h->d, ldw * 2, fr::GM_HALF)) return FR_ERR_CUDA;
+    // rows behind the last are filled in by the copies, without being read
+    if (!fr::gm_encode(&p.map_h, 2, h->rows.h, rows, h->d, h->rows.pitch * 2, fr::GM_HALF)) return FR_ERR_CUDA;
+    p.rows = h->rows;
+    p.V = h->V;
+    p.k_blocks = (h->d + 63) / 64;
+    p.n_tiles = h->n_tiles;
+    p.partial = h->partial;
+    p.xt = h->xt;
+    const int32_t gather = std::max((rows + fr::CE_GATHER_ROWS - 1) / fr::CE_GATHER_ROWS, fr::CE_GATHER_CTAS);
+    FR_CUDA_TRY(fr::launch_pdl(fr::k_ce_gather, gather, fr::CE_GATHER_THREADS, 0, s, (const __nv_bfloat16*)hidden_dev, ldh,
+                               targets_dev, (const float*)nullptr, (const float*)nullptr, rows, h->V, h->d, h->rows,
+                               loss_dev, lse_dev, (__nv_bfloat16*)nullptr, (int64_t)0, (int32_t*)nullptr, 0, h->err));
+    fr::GmCtl ctl{h->err, h->wait_ns, h->starve};
+    FR_CUDA_TRY(fr::gm_launch(fr::k_ce_loss<fr::CeLoss<PAIR>>, fr::ce_round(rows, TM) / TM * h->n_tiles, h->sms, s, p, ctl));
+    FR_CUDA_TRY(fr::launch_pdl(fr::k_ce_combine, ((int64_t)rows + 7) / 8, 256, 0, s, (const float2*)h->partial, 2 * h->n_tiles,
+                               h->rows, (const float*)h->xt, loss_dev, lse_dev, h->err));
+    return FR_OK;
+}
+
+template <bool PAIR>
+fr_status ce_run_grad(fr_ce* h, const void* hidden_dev, int64_t ldh, const void* weight_dev, int64_t ldw,
+                      const int32_t* targets_dev, const float* lse_dev, const float* grad_loss_dev, int32_t rows,
+                      void* grad_hidden_dev, int64_t ldgh, void* grad_weight_dev, int64_t ldgw, cudaStream_t s) {
+    constexpr int TM = fr::CE_TM<PAIR>;
+    fr::CeGrad<PAIR> p{};
+    if (!fr::gm_encode(&p.map_w_k, 2, weight_dev, h->V, h->d, ldw * 2, fr::GM_HALF) ||
+        !fr::gm_encode(&p.map_w_mn, 2, weight_dev, h->V, h->d, ldw * 2, 64))
+        return FR_ERR_CUDA;
+    __nv_bfloat16* gh = (__nv_bfloat16*)grad_hidden_dev;
+    const int64_t m_tiles = fr::ce_round(std::max(rows, 1), TM) / TM;  // no rows: dW is still written (zeros)
+    const int32_t pieces = (h->V + h->piece - 1) / h->piece;
+    // rows behind the last are filled in by the copies, without being read
+    if (!fr::gm_encode(&p.map_h_k, 2, h->rows.h, std::max(rows, 1), h->d, h->rows.pitch * 2, fr::GM_HALF) ||
+        !fr::gm_encode(&p.map_h_mn, 2, h->rows.h, std::max(rows, 1), h->d, h->rows.pitch * 2, 64))
+        return FR_ERR_CUDA;
+    p.rows = h->rows;
+    p.V = h->V;
+    p.d = h->d;
+    p.d_tiles = (h->d + fr::GM_TILE - 1) / fr::GM_TILE;
+    p.splits = fr::ce_splits(PAIR ? h->sms / 2 : h->sms, m_tiles, p.d_tiles);
+    p.dh = gh != nullptr;
+    p.dh_rows = (int32_t)(m_tiles * TM);
+    if (!fr::gm_encode(&p.map_dh, 4, h->dh, (int64_t)p.splits * p.dh_rows, h->rows.pitch, h->rows.pitch * 4, 32))
+        return FR_ERR_CUDA;
+    p.dw = (__nv_bfloat16*)grad_weight_dev;
+    p.ldw = ldgw;
+    if (p.dw && (reinterpret_cast<uintptr_t>(grad_weight_dev) & 15u) == 0 && (ldgw & 7) == 0)
+        p.dw_staged = fr::gm_staged_columns(h->d, 2);
+    if (p.dw_staged && !fr::gm_encode(&p.map_dw, 2, grad_weight_dev, h->V, h->d, ldgw * 2, 32)) return FR_ERR_CUDA;
+    const int32_t gather = std::max((rows + fr::CE_GATHER_ROWS - 1) / fr::CE_GATHER_ROWS, fr::CE_GATHER_CTAS);
+    FR_CUDA_TRY(fr::launch_pdl(fr::k_ce_gather, gather, fr::CE_GATHER_THREADS, 0, s, (const __nv_bfloat16*)hidden_dev, ldh,
+                               targets_dev, lse_dev, grad_loss_dev, rows, h->V, h->d, h->rows, (float*)nullptr,
+                               (float*)nullptr, gh, ldgh, h->counters, pieces + 1, h->err));
+    fr::GmCtl ctl{h->err, h->wait_ns, h->starve};
+    for (int32_t k = 0; k <= pieces; ++k) {
+        p.v0 = p.v1 = p.w0 = p.w1 = 0;
+        int64_t tiles = 0;
+        if (k > 0) {
+            p.v0 = (k - 1) * h->piece;
+            p.v1 = std::min(h->V, k * h->piece);
+            p.first = k == 1;
+            p.map_g_k = h->map_g_k[(k - 1) & 1];
+            p.map_g_mn = h->map_g_mn[(k - 1) & 1];
+            if (gh) tiles += m_tiles * p.d_tiles * p.splits;
+            if (p.dw) tiles += (int64_t)(p.v1 - p.v0 + TM - 1) / TM * p.d_tiles;
+        }
+        if (k < pieces) {
+            p.w0 = k * h->piece;
+            p.w1 = std::min(h->V, (k + 1) * h->piece);
+            p.map_g_out = h->map_g_out[k & 1];
+            tiles += (int64_t)(p.w1 - p.w0 + fr::GM_TILE - 1) / fr::GM_TILE * m_tiles;
+        }
+        p.next_tile = h->counters + k;
+        FR_CUDA_TRY(fr::gm_launch(fr::k_ce_grad<fr::CeGrad<PAIR>>, tiles, h->sms, s, p, ctl));
+    }
+    if (gh && rows > 0)
+        FR_CUDA_TRY(fr::launch_pdl(fr::k_ce_finish, (int64_t)rows, 256, 0, s, (const float*)h->dh,
+                                   p.dh_rows * h->rows.pitch,
+                                   p.splits, h->d, h->rows, gh, ldgh,
+                                   (int32_t)((reinterpret_cast<uintptr_t>(gh) & 7u) == 0 && (ldgh & 3) == 0)));
+    return FR_OK;
+}
+
 }  // namespace
 
 extern "C" fr_status fr_ce_init(int32_t V, int32_t d, int32_t max_rows, fr_ce** out) {
     if (!out) return FR_ERR_INVALID_ARG;
     *out = nullptr;
-    if (V < 1 || d < 1 || max_rows < 1 || max_rows > (1 << 24) || V > (1 << 24)) return FR_ERR_INVALID_ARG;
+    if (V < 1 || d < 1 || max_rows < 1 || max_rows > (1 << 24) || V > (1 << 24) ||
+        (int64_t)max_rows * V > ((int64_t)1 << 44))
+        return FR_ERR_INVALID_ARG;
     fr_ce* h = new (std::nothrow) fr_ce();
     if (!h) return FR_ERR_OOM;
     h->V = V;
@@ -526,14 +637,18 @@ extern "C" fr_status fr_ce_init(int32_t V, int32_t d, int32_t max_rows, fr_ce** 
     h->rows.pitch = fr::ce_round(d, 8);
     if (cudaGetDevice(&h->device) != cudaSuccess ||
         cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, h->device) != cudaSuccess ||
-        fr::gm_setup(fr::k_ce_loss) != cudaSuccess || fr::gm_setup(fr::k_ce_grad) != cudaSuccess) {
+        fr::gm_setup(fr::k_ce_loss<fr::CeLoss<true>>) != cudaSuccess ||
+        fr::gm_setup(fr::k_ce_loss<fr::CeLoss<false>>) != cudaSuccess ||
+        fr::gm_setup(fr::k_ce_grad<fr::CeGrad<true>>) != cudaSuccess ||
+        fr::gm_setup(fr::k_ce_grad<fr::CeGrad<false>>) != cudaSuccess) {
         (void)cudaGetLastError();
         delete h;
         return FR_ERR_CUDA;
     }
     const size_t cap = (size_t)h->cap, pitch = (size_t)h->rows.pitch, d_tiles = (d + fr::GM_TILE - 1) / fr::GM_TILE;
-    // dh partials: splits x tile rows is at most 4 * pairs / d_tiles where there is more than one split
-    const size_t dh_rows = std::max(cap, std::max<size_t>(2 * h->sms / d_tiles, 1) * fr::GM_TILE);
+    // dh partials: one plane of all rows, or, where there are more splits, at most
+    // 4 * units / d_tiles tiles (ce_splits) of pairs or single CTAs
+    const size_t dh_rows = std::max({cap, 2 * h->sms / d_tiles * fr::GM_TILE, 4 * h->sms / d_tiles * fr::GM_HALF});
     cudaError_t e = cudaMalloc(&h->rows.h, cap * pitch * 2);
     if (e == cudaSuccess) e = cudaMalloc(&h->rows.tgt, cap * 4 * 5 + 8 + ((V + h->piece - 1) / h->piece + 1) * 4);
     if (e == cudaSuccess) e = cudaMalloc(&h->partial, cap * 2 * h->n_tiles * sizeof(float2));
@@ -577,25 +692,8 @@ extern "C" fr_status fr_ce_loss(fr_ce* h, const void* hidden_dev, int64_t ldh, c
     const cudaStream_t s = (cudaStream_t)stream;
     h->last_stream = s;
     if (rows == 0) return FR_OK;
-    fr::CeLoss p{};
-    if (!fr::gm_encode(&p.map_w, 2, weight_dev, h->V, h->d, ldw * 2, fr::GM_HALF)) return FR_ERR_CUDA;
-    // rows behind the last are filled in by the copies, without being read
-    if (!fr::gm_encode(&p.map_h, 2, h->rows.h, rows, h->d, h->rows.pitch * 2, fr::GM_HALF)) return FR_ERR_CUDA;
-    p.rows = h->rows;
-    p.V = h->V;
-    p.k_blocks = (h->d + 63) / 64;
-    p.n_tiles = h->n_tiles;
-    p.partial = h->partial;
-    p.xt = h->xt;
-    const int32_t gather = std::max((rows + fr::CE_GATHER_ROWS - 1) / fr::CE_GATHER_ROWS, fr::CE_GATHER_CTAS);
-    FR_CUDA_TRY(fr::launch_pdl(fr::k_ce_gather, gather, fr::CE_GATHER_THREADS, 0, s, (const __nv_bfloat16*)hidden_dev, ldh,
-                               targets_dev, (const float*)nullptr, (const float*)nullptr, rows, h->V, h->d, h->rows,
-                               loss_dev, lse_dev, (__nv_bfloat16*)nullptr, (int64_t)0, (int32_t*)nullptr, 0, h->err));
-    fr::GmCtl ctl{h->err, h->wait_ns, h->starve};
-    FR_CUDA_TRY(fr::gm_launch(fr::k_ce_loss, fr::ce_round(rows, fr::GM_TILE) / fr::GM_TILE * h->n_tiles, h->sms, s, p, ctl));
-    FR_CUDA_TRY(fr::launch_pdl(fr::k_ce_combine, ((int64_t)rows + 7) / 8, 256, 0, s, (const float2*)h->partial, 2 * h->n_tiles,
-                               h->rows, (const float*)h->xt, loss_dev, lse_dev, h->err));
-    return FR_OK;
+    const auto run = rows <= fr::GM_HALF ? ce_run_loss<false> : ce_run_loss<true>;
+    return run(h, hidden_dev, ldh, weight_dev, ldw, targets_dev, rows, loss_dev, lse_dev, s);
 }
 
 extern "C" fr_status fr_ce_grad(fr_ce* h, const void* hidden_dev, int64_t ldh, const void* weight_dev, int64_t ldw,
@@ -610,63 +708,9 @@ extern "C" fr_status fr_ce_grad(fr_ce* h, const void* hidden_dev, int64_t ldh, c
         return FR_ERR_INVALID_ARG;
     const cudaStream_t s = (cudaStream_t)stream;
     h->last_stream = s;
-    fr::CeGrad p{};
-    if (!fr::gm_encode(&p.map_w_k, 2, weight_dev, h->V, h->d, ldw * 2, fr::GM_HALF) ||
-        !fr::gm_encode(&p.map_w_mn, 2, weight_dev, h->V, h->d, ldw * 2, 64))
-        return FR_ERR_CUDA;
-    __nv_bfloat16* gh = (__nv_bfloat16*)grad_hidden_dev;
-    const int64_t m_tiles = fr::ce_round(std::max(rows, 1), fr::GM_TILE) / fr::GM_TILE;  // no rows: dW is still written (zeros)
-    const int32_t pieces = (h->V + h->piece - 1) / h->piece;
-    // rows behind the last are filled in by the copies, without being read
-    if (!fr::gm_encode(&p.map_h_k, 2, h->rows.h, std::max(rows, 1), h->d, h->rows.pitch * 2, fr::GM_HALF) ||
-        !fr::gm_encode(&p.map_h_mn, 2, h->rows.h, std::max(rows, 1), h->d, h->rows.pitch * 2, 64))
-        return FR_ERR_CUDA;
-    p.rows = h->rows;
-    p.V = h->V;
-    p.d = h->d;
-    p.d_tiles = (h->d + fr::GM_TILE - 1) / fr::GM_TILE;
-    p.splits = fr::ce_splits(h->sms / 2, m_tiles, p.d_tiles);
-    p.dh = gh != nullptr;
-    p.dh_rows = (int32_t)(m_tiles * fr::GM_TILE);
-    if (!fr::gm_encode(&p.map_dh, 4, h->dh, (int64_t)p.splits * p.dh_rows, h->rows.pitch, h->rows.pitch * 4, 32))
-        return FR_ERR_CUDA;
-    p.dw = (__nv_bfloat16*)grad_weight_dev;
-    p.ldw = ldgw;
-    if (p.dw && (reinterpret_cast<uintptr_t>(grad_weight_dev) & 15u) == 0 && (ldgw & 7) == 0)
-        p.dw_staged = fr::gm_staged_columns(h->d, 2);
-    if (p.dw_staged && !fr::gm_encode(&p.map_dw, 2, grad_weight_dev, h->V, h->d, ldgw * 2, 32)) return FR_ERR_CUDA;
-    const int32_t gather = std::max((rows + fr::CE_GATHER_ROWS - 1) / fr::CE_GATHER_ROWS, fr::CE_GATHER_CTAS);
-    FR_CUDA_TRY(fr::launch_pdl(fr::k_ce_gather, gather, fr::CE_GATHER_THREADS, 0, s, (const __nv_bfloat16*)hidden_dev, ldh,
-                               targets_dev, lse_dev, grad_loss_dev, rows, h->V, h->d, h->rows, (float*)nullptr,
-                               (float*)nullptr, gh, ldgh, h->counters, pieces + 1, h->err));
-    fr::GmCtl ctl{h->err, h->wait_ns, h->starve};
-    for (int32_t k = 0; k <= pieces; ++k) {
-        p.v0 = p.v1 = p.w0 = p.w1 = 0;
-        int64_t tiles = 0;
-        if (k > 0) {
-            p.v0 = (k - 1) * h->piece;
-            p.v1 = std::min(h->V, k * h->piece);
-            p.first = k == 1;
-            p.map_g_k = h->map_g_k[(k - 1) & 1];
-            p.map_g_mn = h->map_g_mn[(k - 1) & 1];
-            if (gh) tiles += m_tiles * p.d_tiles * p.splits;
-            if (p.dw) tiles += (int64_t)(p.v1 - p.v0 + fr::GM_TILE - 1) / fr::GM_TILE * p.d_tiles;
-        }
-        if (k < pieces) {
-            p.w0 = k * h->piece;
-            p.w1 = std::min(h->V, (k + 1) * h->piece);
-            p.map_g_out = h->map_g_out[k & 1];
-            tiles += (int64_t)(p.w1 - p.w0 + fr::GM_TILE - 1) / fr::GM_TILE * m_tiles;
-        }
-        p.next_tile = h->counters + k;
-        FR_CUDA_TRY(fr::gm_launch(fr::k_ce_grad, tiles, h->sms, s, p, ctl));
-    }
-    if (gh && rows > 0)
-        FR_CUDA_TRY(fr::launch_pdl(fr::k_ce_finish, (int64_t)rows, 256, 0, s, (const float*)h->dh,
-                                   p.dh_rows * h->rows.pitch,
-                                   p.splits, h->d, h->rows, gh, ldgh,
-                                   (int32_t)((reinterpret_cast<uintptr_t>(gh) & 7u) == 0 && (ldgh & 3) == 0)));
-    return FR_OK;
+    const auto run = rows <= fr::GM_HALF ? ce_run_grad<false> : ce_run_grad<true>;
+    return run(h, hidden_dev, ldh, weight_dev, ldw, targets_dev, lse_dev, grad_loss_dev, rows, grad_hidden_dev, ldgh,
+               grad_weight_dev, ldgw, s);
 }
 
 extern "C" fr_status fr_ce_status(fr_ce* h) {

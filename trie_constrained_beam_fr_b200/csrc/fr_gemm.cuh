@@ -18,6 +18,7 @@
 //
 //   struct P {
 //     static constexpr bool I8;            // 8-bit integers (int32 sums) or bf16 (fp32 sums)
+//     static constexpr bool PAIR;          // CTA pairs or single CTAs
 //     static constexpr bool STAGED;        // the epilogue stores through shared memory
 //     static constexpr int STAGES;         // ring depth
 //     static constexpr bool DYNAMIC;       // tiles of unequal length: the pairs take the next one from a counter
@@ -47,13 +48,13 @@
 
 namespace fr {
 
-constexpr int GM_TILE = 256;         // rows and columns of a pair's tile
-constexpr int GM_HALF = 128;         // rows of A and of B that one CTA stages: the tensor-memory lanes
+constexpr int GM_TILE = 256;         // columns of a tile, and rows of a pair's
+constexpr int GM_HALF = 128;         // rows of A that one CTA stages, and of a single CTA's tile: the tensor-memory lanes
 constexpr int GM_KB_BYTES = 128;     // K bytes per stage: one 128-byte swizzle span
 constexpr int GM_THREADS = 384;      // 12 warps, 8 of them for the epilogue
 constexpr int GM_EPI_WARPS = 8;
 constexpr int GM_EPI_COLS = 128;     // columns of a tile that one epilogue warp takes
-constexpr int GM_OP_BYTES = GM_HALF * GM_KB_BYTES;  // one operand's half tile per stage
+constexpr int GM_OP_BYTES = GM_HALF * GM_KB_BYTES;  // 128 rows of an operand per stage
 constexpr int GM_STAGE_BUF = 32 * 128;              // one staged store: 32 rows x 128 bytes
 constexpr uint32_t GM_TMEM_COLS = 2 * GM_TILE;      // two accumulators
 
@@ -61,9 +62,9 @@ constexpr uint32_t GM_TMEM_COLS = 2 * GM_TILE;      // two accumulators
 // A and B types at bits 7-9 and 10-12 (kind::f16: 1 = bf16; kind::i8: 1 =
 // signed), "MN-major" flags of A and B at bits 15 and 16, N >> 3 at bits
 // 17-22, M >> 4 at bits 24-28.
-__host__ __device__ constexpr uint32_t gm_idesc(bool i8, bool a_mn = false, bool b_mn = false, int n = GM_TILE) {
+__host__ __device__ constexpr uint32_t gm_idesc(bool i8, bool pair, bool a_mn = false, bool b_mn = false, int n = GM_TILE) {
     return ((i8 ? 2u : 1u) << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
-           ((uint32_t)(n >> 3) << 17) | ((uint32_t)(GM_TILE >> 4) << 24);
+           ((uint32_t)(n >> 3) << 17) | ((uint32_t)((pair ? GM_TILE : GM_HALF) >> 4) << 24);
 }
 
 // Shared-memory descriptor of an MN-major bf16 tile with the 128-byte
@@ -76,28 +77,35 @@ __device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr) {
            ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
-template <bool I8>
+#define GM_UMMA(GROUP, KIND)                                                                           \
+    asm volatile(                                                                                      \
+        "{\n\t.reg .pred p;\n\t"                                                                        \
+        "setp.ne.b32 p, %4, 0;\n\t"                                                                    \
+        "tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),       \
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)                                            \
+        : "memory")
+template <bool I8, bool PAIR>
 __device__ __forceinline__ void gm_umma(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                         uint32_t accumulate) {
-    if (I8)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "setp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
-            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "setp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
-            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-            : "memory");
+    if constexpr (PAIR) {
+        if constexpr (I8)
+            GM_UMMA("2", "i8");
+        else
+            GM_UMMA("2", "f16");
+    } else {
+        if constexpr (I8)
+            GM_UMMA("1", "i8");
+        else
+            GM_UMMA("1", "f16");
+    }
 }
+#undef GM_UMMA
 
-// Arrives on the barrier at this offset in both CTAs once every product issued
-// so far by this thread has completed.
-__device__ __forceinline__ void gm_commit_both(uint64_t* bar) {
+// Arrives on the barrier (of a pair: at this offset in both CTAs) once every
+// product issued so far by this thread has completed.
+template <bool PAIR>
+__device__ __forceinline__ void gm_commit(uint64_t* bar) {
+    if constexpr (!PAIR) return tc_umma_commit(bar);
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
             smem_u32(bar)),
@@ -134,8 +142,17 @@ __device__ __forceinline__ void gm_cluster_sync() {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
-// 2-D tiled TMA load into this CTA that arrives on the first CTA's barrier.
+// 2-D tiled TMA load into this CTA that arrives on the first (or only) CTA's barrier.
+template <bool PAIR>
 __device__ __forceinline__ void gm_tma_load(const CUtensorMap* map, void* dst, uint32_t bar, int32_t x, int32_t y) {
+    if constexpr (!PAIR) {
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+                smem_u32(dst)),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+            : "memory");
+        return;
+    }
     asm volatile(
         "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
         "[%4];" ::"r"(smem_u32(dst)),
@@ -245,22 +262,24 @@ struct GmCtl {
 
 template <class P>
 __host__ __device__ constexpr size_t gm_smem_bytes() {
-    return 1024 + (size_t)P::STAGES * 2 * GM_OP_BYTES + (P::STAGED ? GM_EPI_WARPS * GM_STAGE_BUF : 0) + sizeof(GmSmem<P::STAGES>);
+    return 1024 + (size_t)P::STAGES * (P::PAIR ? 2 : 3) * GM_OP_BYTES + (P::STAGED ? GM_EPI_WARPS * GM_STAGE_BUF : 0) + sizeof(GmSmem<P::STAGES>);
 }
 
 template <class P>
 __device__ __forceinline__ void gm_run(const P& p, const GmCtl& ctl) {
     extern __shared__ uint8_t gm_smem_raw[];
     constexpr int STAGES = P::STAGES;
+    constexpr bool PAIR = P::PAIR;
+    constexpr int B_BYTES = (PAIR ? 1 : 2) * GM_OP_BYTES;  // 128 or 256 rows of B
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(gm_smem_raw) + 1023) & ~(uintptr_t)1023);
     uint8_t* ringA = base;
     uint8_t* ringB = base + STAGES * GM_OP_BYTES;
-    uint8_t* stage = ringB + STAGES * GM_OP_BYTES;
+    uint8_t* stage = ringB + STAGES * B_BYTES;
     GmSmem<STAGES>* sm = reinterpret_cast<GmSmem<STAGES>*>(stage + (P::STAGED ? GM_EPI_WARPS * GM_STAGE_BUF : 0));
     volatile int32_t* abort_flag = &sm->abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = gm_cta_rank();
-    const uint32_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const uint32_t rank = PAIR ? gm_cta_rank() : 0;
+    const uint32_t pair = PAIR ? blockIdx.x >> 1 : blockIdx.x, pairs = PAIR ? gridDim.x >> 1 : gridDim.x;  // (or single CTAs)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -269,25 +288,33 @@ __device__ __forceinline__ void gm_run(const P& p, const GmCtl& ctl) {
         }
         for (int i = 0; i < 2; ++i) {
             tc_mbar_init(&sm->tmem_full[i], 1);
-            tc_mbar_init(&sm->tmem_empty[i], 2 * GM_EPI_WARPS);
+            tc_mbar_init(&sm->tmem_empty[i], (PAIR ? 2 : 1) * GM_EPI_WARPS);
         }
         tc_mbar_init(&sm->mma_done, 1);
         for (int i = 0; i < GM_SLOTS; ++i) {
             tc_mbar_init(&sm->tile_full[i], 1);
-            tc_mbar_init(&sm->tile_empty[i], 2 * GM_EPI_WARPS + 2);  // the epilogue warps, the products, the other producer
+            // the epilogue warps, the products, the other producer
+            tc_mbar_init(&sm->tile_empty[i], PAIR ? 2 * GM_EPI_WARPS + 2 : GM_EPI_WARPS + 1);
         }
         sm->abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 2) {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm->tmem_base)),
-                     "r"(GM_TMEM_COLS)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        if constexpr (PAIR) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm->tmem_base)),
+                         "r"(GM_TMEM_COLS)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm->tmem_base)),
+                         "r"(GM_TMEM_COLS)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        }
     }
     tc_fence_before();
     __syncthreads();
-    gm_cluster_sync();
+    if constexpr (PAIR) gm_cluster_sync();
     tc_fence_after();
     const uint32_t tmem = sm->tmem_base;
     griddep_wait();
@@ -325,6 +352,7 @@ __device__ __forceinline__ void gm_run(const P& p, const GmCtl& ctl) {
             return false;
         *(volatile int32_t*)&sm->tile_id[s] = (int32_t)g;
         tc_arrive(&sm->tile_full[s]);
+        if constexpr (!PAIR) return true;
         asm volatile("st.relaxed.cluster.shared::cluster.s32 [%0], %1;" ::"r"(gm_in_cta(&sm->tile_id[s], 1)), "r"((int32_t)g)
                      : "memory");
         gm_publish_remote(gm_in_cta(&sm->tile_full[s], 1));
@@ -353,8 +381,8 @@ __device__ __forceinline__ void gm_run(const P& p, const GmCtl& ctl) {
                         break;
                     }
                     // the first CTA's barrier counts both CTAs' bytes
-                    if (rank == 0) tc_arrive_expect_tx(&sm->full[s], 2 * p.stage_bytes());
-                    p.load(t, kb, (int)rank, ringA + s * GM_OP_BYTES, ringB + s * GM_OP_BYTES, gm_in_first(&sm->full[s]));
+                    if (rank == 0) tc_arrive_expect_tx(&sm->full[s], (PAIR ? 2 : 1) * p.stage_bytes());
+                    p.load(t, kb, (int)rank, ringA + s * GM_OP_BYTES, ringB + s * B_BYTES, PAIR ? gm_in_first(&sm->full[s]) : smem_u32(&sm->full[s]));
                 }
             }
             // The last copies land before the CTAs end.  Normally the first
@@ -390,29 +418,29 @@ __device__ __forceinline__ void gm_run(const P& p, const GmCtl& ctl) {
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t sa = smem_u32(ringA + s * GM_OP_BYTES), sb = smem_u32(ringB + s * GM_OP_BYTES);
+                    const uint32_t sa = smem_u32(ringA + s * GM_OP_BYTES), sb = smem_u32(ringB + s * B_BYTES);
                     const uint64_t da = amn ? smem_desc_mn_sw128(sa) : smem_desc_sw128(sa);
                     const uint64_t db = bmn ? smem_desc_mn_sw128(sb) : smem_desc_sw128(sb);
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        gm_umma<P::I8>(d_tmem, da + (uint64_t)(kk * ia), db + (uint64_t)(kk * ib), now.idesc,
+                        gm_umma<P::I8, PAIR>(d_tmem, da + (uint64_t)(kk * ia), db + (uint64_t)(kk * ib), now.idesc,
                                        (kb | kk) != 0 ? 1u : 0u);
-                    gm_commit_both(&sm->empty[s]);  // the stage is free in both CTAs once these products are done
+                    gm_commit<PAIR>(&sm->empty[s]);  // the stage is free in both CTAs once these products are done
                     // worked out while this tile's products run
                     if (!P::DYNAMIC && kb == 0) more = next(i + 1, false);
                 }
                 if (P::DYNAMIC || now.nk == 0) more = ok && next(i + 1, false);
-                gm_commit_both(&sm->tmem_full[acc]);  // the accumulators are complete (or, on abort, quiet)
+                gm_commit<PAIR>(&sm->tmem_full[acc]);  // the accumulators are complete (or, on abort, quiet)
             }
             // the tensor memory is freed only after every product issued here is done
-            gm_commit_both(&sm->mma_done);
+            gm_commit<PAIR>(&sm->mma_done);
         }
         // in both CTAs: the commits' arrivals reach no CTA that has ended
         if (lane == 0) tc_wait_drain(&sm->mma_done, 0);
     } else if (warp >= 4) {
         const int q = warp & 3, half = (warp - 4) >> 2;
         GmStage sg{stage + (warp - 4) * GM_STAGE_BUF};
-        const uint32_t empty0 = gm_in_first(&sm->tmem_empty[0]), empty1 = gm_in_first(&sm->tmem_empty[1]);
+        const uint32_t empty0 = PAIR ? gm_in_first(&sm->tmem_empty[0]) : 0, empty1 = PAIR ? gm_in_first(&sm->tmem_empty[1]) : 0;
         for (int i = 0; next(i, true); ++i) {
             const int acc = i & 1;
             if (!tc_wait(&sm->tmem_full[acc], (i >> 1) & 1, abort_flag, ctl.err, ctl.wait_ns)) break;
@@ -421,16 +449,24 @@ __device__ __forceinline__ void gm_run(const P& p, const GmCtl& ctl) {
                        half, sg);
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) gm_arrive_remote(acc ? empty1 : empty0);
+            if (lane == 0) {
+                if constexpr (PAIR)
+                    gm_arrive_remote(acc ? empty1 : empty0);
+                else
+                    tc_arrive(&sm->tmem_empty[acc]);
+            }
         }
         if (P::STAGED && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
     tc_fence_before();
     __syncthreads();
-    gm_cluster_sync();  // nobody's copies, products or arrivals reach a CTA that has ended
+    if constexpr (PAIR) gm_cluster_sync();  // nobody's copies, products or arrivals reach a CTA that has ended
     if (warp == 2) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(GM_TMEM_COLS) : "memory");
+        if constexpr (PAIR)
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(GM_TMEM_COLS) : "memory");
+        else
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(GM_TMEM_COLS) : "memory");
     }
 }
 
@@ -598,13 +634,14 @@ inline cudaError_t gm_setup(void (*kernel)(P, GmCtl)) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)gm_smem_bytes<P>());
 }
 
-// A gm_run kernel over `tiles` tiles: clusters of two CTAs, at most one CTA per SM.
+// A gm_run kernel over `tiles` tiles: CTA pairs (clusters of two) or single CTAs,
+// at most one CTA per SM.
 template <class P>
 inline cudaError_t gm_launch(void (*kernel)(P, GmCtl), int64_t tiles, int32_t sms, cudaStream_t s, const P& p,
                              const GmCtl& ctl) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
-    cfg.gridDim = dim3((unsigned)(2 * std::min<int64_t>(tiles, sms / 2)));
+    cfg.gridDim = dim3((unsigned)(P::PAIR ? 2 * std::min<int64_t>(tiles, sms / 2) : std::min<int64_t>(tiles, sms)));
     cfg.blockDim = dim3(GM_THREADS);
     cfg.dynamicSmemBytes = gm_smem_bytes<P>();
     cfg.stream = s;
@@ -615,7 +652,7 @@ inline cudaError_t gm_launch(void (*kernel)(P, GmCtl), int64_t tiles, int32_t sm
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = P::PAIR ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, p, ctl);
 }
 

@@ -237,8 +237,10 @@ __global__ void __launch_bounds__(FEW_THREADS) k_i8_few(const int8_t* __restrict
 }
 
 // Tile walk shared by the two products.
+template <bool PAIR_>
 struct I8Base {
-    static constexpr bool I8 = true, DYNAMIC = false;
+    static constexpr bool I8 = true, DYNAMIC = false, PAIR = PAIR_;
+    static constexpr int TM = PAIR ? GM_TILE : GM_HALF;  // rows of a tile
     __device__ __forceinline__ int32_t* counter() const { return nullptr; }
     struct Tile {
         int nk, m0, n0;
@@ -257,18 +259,20 @@ struct I8Base {
         if (g >= (uint32_t)m_tiles * (uint32_t)n_tiles) return false;
         int32_t m, n;
         gm_grouped(g, m_tiles, n_tiles, m, n);
-        t.m0 = m * GM_TILE;
+        t.m0 = m * TM;
         t.n0 = n * bn;
         t.nk = k_blocks;
-        t.idesc = gm_idesc(true, false, false, bn);
+        t.idesc = gm_idesc(true, PAIR, false, false, bn);
         return true;
     }
-    __device__ __forceinline__ uint32_t stage_bytes() const { return GM_OP_BYTES + bn / 2 * GM_KB_BYTES; }
+    __device__ __forceinline__ uint32_t stage_bytes() const { return GM_OP_BYTES + (PAIR ? bn / 2 : bn) * GM_KB_BYTES; }
     __device__ __forceinline__ bool a_mn(const Tile&) const { return false; }
     __device__ __forceinline__ bool b_mn(const Tile&) const { return false; }
     __device__ __forceinline__ void load(const Tile& t, int kb, int rank, uint8_t* a, uint8_t* b, uint32_t bar) const {
-        gm_tma_load(&map_x, a, bar, kb * GM_KB_BYTES, t.m0 + rank * GM_HALF);
-        gm_tma_load(&map_w, b, bar, kb * GM_KB_BYTES, t.n0 + rank * (bn / 2));
+        gm_tma_load<PAIR>(&map_x, a, bar, kb * GM_KB_BYTES, t.m0 + rank * GM_HALF);
+        // a box is half a tile's columns: the CTA's, or both
+        gm_tma_load<PAIR>(&map_w, b, bar, kb * GM_KB_BYTES, t.n0 + rank * (bn / 2));
+        if constexpr (!PAIR) gm_tma_load<PAIR>(&map_w, b + bn / 2 * GM_KB_BYTES, bar, kb * GM_KB_BYTES, t.n0 + bn / 2);
     }
     // y of 32 columns from n on: the row's scale first, then the channel's
     __device__ __forceinline__ void scaled(uint32_t taddr, int n, float xscale, float* v) const {
@@ -287,10 +291,18 @@ struct I8Base {
     }
 };
 
-template <class T>
-struct I8Out : I8Base {
+template <class T, bool PAIR_>
+struct I8Out : I8Base<PAIR_> {
+    using Base = I8Base<PAIR_>;
+    using typename Base::State;
+    using typename Base::Tile;
+    using Base::bn;
+    using Base::N;
+    using Base::rows;
+    using Base::xs;
+    using Base::scaled;
     static constexpr bool STAGED = true;
-    static constexpr int STAGES = 6;
+    static constexpr int STAGES = PAIR_ ? 6 : 4;
     CUtensorMap map_out;
     T* out;
     int64_t ldo;
@@ -317,9 +329,17 @@ struct I8Out : I8Base {
     }
 };
 
-struct I8Lse : I8Base {
+template <bool PAIR_>
+struct I8Lse : I8Base<PAIR_> {
+    using Base = I8Base<PAIR_>;
+    using typename Base::State;
+    using typename Base::Tile;
+    using Base::N;
+    using Base::rows;
+    using Base::xs;
+    using Base::scaled;
     static constexpr bool STAGED = false;
-    static constexpr int STAGES = 7;
+    static constexpr int STAGES = PAIR_ ? 7 : 4;
     float2* partial;  // [rows, n_parts] (max, scaled sum) of 128 columns each
     int32_t n_parts;
     float* slice;     // [rows, sid_span]
@@ -393,15 +413,18 @@ bool i8_on_device(const fr_i8* h) {
     return cudaGetDevice(&dev) == cudaSuccess && dev == h->device;
 }
 
-fr_status i8_base(fr_i8* h, const int8_t* xq, int64_t ldx, const float* xs, int32_t rows, bool any_width, fr::I8Base* b) {
+template <bool PAIR>
+fr_status i8_base(fr_i8* h, const int8_t* xq, int64_t ldx, const float* xs, int32_t rows, bool any_width,
+                  fr::I8Base<PAIR>* b) {
     if (!fr::gm_encode(&b->map_x, 1, xq, rows, h->d, ldx, fr::GM_HALF)) return FR_ERR_CUDA;
-    // Tile width: the rounds that the pairs need times a tile's cost (its columns,
-    // and about 64 columns' worth of start and end).
-    const int64_t pairs = h->sms / 2, m_tiles = (rows + fr::GM_TILE - 1) / fr::GM_TILE;
+    // Tile width: the rounds that the pairs (or CTAs) need times a tile's cost (its
+    // columns, and about 64 columns' worth of start and end).
+    constexpr int TM = fr::I8Base<PAIR>::TM;
+    const int64_t units = PAIR ? h->sms / 2 : h->sms, m_tiles = (rows + TM - 1) / TM;
     int best = 0;
     int64_t cost = INT64_MAX;
     for (int k = 0; k < (any_width ? 3 : 1); ++k) {
-        const int64_t bn = fr::GM_TILE >> k, tiles = m_tiles * ((h->N + bn - 1) / bn), c = (tiles + pairs - 1) / pairs * (bn + 64);
+        const int64_t bn = fr::GM_TILE >> k, tiles = m_tiles * ((h->N + bn - 1) / bn), c = (tiles + units - 1) / units * (bn + 64);
         if (c < cost) cost = c, best = k;
     }
     b->bn = fr::GM_TILE >> best;
@@ -424,6 +447,20 @@ fr_status i8_launch(fr_i8* h, const P& p, cudaStream_t s) {
     return FR_OK;
 }
 
+template <class T, bool PAIR>
+fr_status i8_tiles(fr_i8* h, const int8_t* xq, int64_t ldx, const float* xs, int32_t rows, void* out, int64_t ldo,
+                   cudaStream_t s) {
+    fr::I8Out<T, PAIR> p{};
+    const fr_status st = i8_base<PAIR>(h, xq, ldx, xs, rows, true, &p);
+    if (st != FR_OK) return st;
+    p.out = (T*)out;
+    p.ldo = ldo;
+    if ((reinterpret_cast<uintptr_t>(out) & 15u) == 0 && (ldo * sizeof(T)) % 16 == 0)
+        p.staged = fr::gm_staged_columns(h->N, sizeof(T));
+    if (p.staged && !fr::gm_encode(&p.map_out, sizeof(T), out, rows, h->N, ldo * sizeof(T), 32)) return FR_ERR_CUDA;
+    return i8_launch(h, p, s);
+}
+
 template <class T>
 fr_status i8_out(fr_i8* h, const int8_t* xq, int64_t ldx, const float* xs, int32_t rows, void* out, int64_t ldo,
                  cudaStream_t s) {
@@ -439,14 +476,20 @@ fr_status i8_out(fr_i8* h, const int8_t* xq, int64_t ldx, const float* xs, int32
             return FR_OK;
         }
     }
-    fr::I8Out<T> p{};
-    const fr_status st = i8_base(h, xq, ldx, xs, rows, true, &p);
+    return rows <= fr::GM_HALF ? i8_tiles<T, false>(h, xq, ldx, xs, rows, out, ldo, s)
+                               : i8_tiles<T, true>(h, xq, ldx, xs, rows, out, ldo, s);
+}
+
+template <bool PAIR>
+fr_status i8_rows_lse(fr_i8* h, const int8_t* xq, int64_t ldx, const float* xs, int32_t rows, float* slice, cudaStream_t s) {
+    fr::I8Lse<PAIR> p{};
+    const fr_status st = i8_base<PAIR>(h, xq, ldx, xs, rows, false, &p);
     if (st != FR_OK) return st;
-    p.out = (T*)out;
-    p.ldo = ldo;
-    if ((reinterpret_cast<uintptr_t>(out) & 15u) == 0 && (ldo * sizeof(T)) % 16 == 0)
-        p.staged = fr::gm_staged_columns(h->N, sizeof(T));
-    if (p.staged && !fr::gm_encode(&p.map_out, sizeof(T), out, rows, h->N, ldo * sizeof(T), 32)) return FR_ERR_CUDA;
+    p.partial = h->partial;
+    p.n_parts = 2 * h->n_tiles;
+    p.slice = slice;
+    p.sid_base = h->sid_base;
+    p.sid_span = h->sid_span;
     return i8_launch(h, p, s);
 }
 
@@ -457,6 +500,14 @@ cudaError_t i8_setup_few() {
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
+}
+
+template <bool PAIR>
+cudaError_t i8_setup_tiles() {
+    cudaError_t e = fr::gm_setup(fr::k_i8<fr::I8Out<float, PAIR>>);
+    if (e == cudaSuccess) e = fr::gm_setup(fr::k_i8<fr::I8Out<__nv_bfloat16, PAIR>>);
+    if (e == cudaSuccess) e = fr::gm_setup(fr::k_i8<fr::I8Lse<PAIR>>);
+    return e;
 }
 
 bool i8_bad_x(const fr_i8* h, const int8_t* xq, int64_t ldx, const float* xs, int32_t rows) {
@@ -491,7 +542,8 @@ extern "C" fr_status fr_i8_init(const int8_t* weight_dev, int64_t ldw, const flo
     if (!out) return FR_ERR_INVALID_ARG;
     *out = nullptr;
     if (!weight_dev || !wscale_dev || N < 1 || d < 1 || d > 131071 || ldw < d || max_rows < 1 || sid_base < 0 ||
-        sid_span < 0 || (int64_t)sid_base + sid_span > N || max_rows > (1 << 24) || N > (1 << 24))
+        sid_span < 0 || (int64_t)sid_base + sid_span > N || max_rows > (1 << 24) || N > (1 << 24) ||
+        (int64_t)max_rows * N > ((int64_t)1 << 44))
         return FR_ERR_INVALID_ARG;
     if ((reinterpret_cast<uintptr_t>(weight_dev) & 15u) || (ldw & 15) || (reinterpret_cast<uintptr_t>(wscale_dev) & 3u))
         return FR_ERR_INVALID_ARG;
@@ -512,8 +564,7 @@ extern "C" fr_status fr_i8_init(const int8_t* weight_dev, int64_t ldw, const flo
         !fr::gm_encode(&h->map_w[1], 1, weight_dev, N, d, ldw, fr::GM_HALF / 2) ||
         !fr::gm_encode(&h->map_w[2], 1, weight_dev, N, d, ldw, fr::GM_HALF / 4) ||
         i8_setup_few<float>() != cudaSuccess || i8_setup_few<__nv_bfloat16>() != cudaSuccess ||
-        fr::gm_setup(fr::k_i8<fr::I8Out<float>>) != cudaSuccess ||
-        fr::gm_setup(fr::k_i8<fr::I8Out<__nv_bfloat16>>) != cudaSuccess || fr::gm_setup(fr::k_i8<fr::I8Lse>) != cudaSuccess) {
+        i8_setup_tiles<true>() != cudaSuccess || i8_setup_tiles<false>() != cudaSuccess) {
         (void)cudaGetLastError();
         delete h;
         return FR_ERR_CUDA;
@@ -556,15 +607,8 @@ extern "C" fr_status fr_i8_lse(fr_i8* h, const int8_t* xq_dev, int64_t ldx, cons
     const cudaStream_t s = (cudaStream_t)stream;
     h->last_stream = s;
     if (rows == 0) return FR_OK;
-    fr::I8Lse p{};
-    fr_status st = i8_base(h, xq_dev, ldx, xscale_dev, rows, false, &p);
-    if (st != FR_OK) return st;
-    p.partial = h->partial;
-    p.n_parts = 2 * h->n_tiles;
-    p.slice = slice_dev;
-    p.sid_base = h->sid_base;
-    p.sid_span = h->sid_span;
-    st = i8_launch(h, p, s);
+    const fr_status st = rows <= fr::GM_HALF ? i8_rows_lse<false>(h, xq_dev, ldx, xscale_dev, rows, slice_dev, s)
+                                             : i8_rows_lse<true>(h, xq_dev, ldx, xscale_dev, rows, slice_dev, s);
     if (st != FR_OK) return st;
     FR_CUDA_TRY(fr::launch_pdl(fr::k_i8_combine, ((int64_t)rows + 7) / 8, 256, 0, s, (const float2*)h->partial, rows,
                                2 * h->n_tiles, lse_dev, h->err));
