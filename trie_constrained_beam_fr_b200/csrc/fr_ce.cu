@@ -222,7 +222,8 @@ struct CeLoss {
         gm_tma_load<PAIR>(&map_h, a, bar, kb * 64, t.m0 + rank * GM_HALF);
         ce_load_b<PAIR>(&map_w, b, bar, kb * 64, t.n0, rank);
     }
-    __device__ __forceinline__ void epilogue(const State& st, const Tile& t, uint32_t taddr, int r, int half, const GmStage&) const {
+    __device__ __forceinline__ void epilogue(const State& st, const Tile& t, uint32_t taddr, int r, int half, const GmStage&,
+                                             GmRelease<PAIR>& release) const {
         const int c0 = half * GM_EPI_COLS;
         const int row = t.m0 + r;
         const int32_t tgt = row < st.n ? rows.tgt[row] : -1;
@@ -232,6 +233,7 @@ struct CeLoss {
             const int n = t.n0 + c;
             float v[32];
             tc_tmem_ld32(taddr + (uint32_t)c, v);
+            if (c + 32 == c0 + GM_EPI_COLS) release();
             if ((uint32_t)(tgt - n) < 32u) {
                 float x = 0.f;
 #pragma unroll
@@ -375,7 +377,8 @@ struct CeGrad {
             ce_load_b_mn<PAIR>(&map_h_mn, b, bar, t.n0, k, rank);
         }
     }
-    __device__ __forceinline__ void epilogue(const State& st, const Tile& t, uint32_t taddr, int r, int half, const GmStage& sg) const {
+    __device__ __forceinline__ void epilogue(const State& st, const Tile& t, uint32_t taddr, int r, int half, const GmStage& sg,
+                                             GmRelease<PAIR>& release) const {
         const int c0 = half * GM_EPI_COLS;
         const int row = t.m0 + r, lane = threadIdx.x & 31, row0 = row - lane;
         if (t.type == GT) {
@@ -386,8 +389,8 @@ struct CeGrad {
 #pragma unroll 1
             for (int c = c0; c < c0 + GM_EPI_COLS; c += 64) {
                 float v[64];
-                gm_ld32(taddr + (uint32_t)c, v);
-                gm_ld32(taddr + (uint32_t)c + 32, v + 32);
+                gm_ld64(taddr + (uint32_t)c, v);
+                if (c + 64 == c0 + GM_EPI_COLS) release();
 #pragma unroll
                 for (int i = 0; i < 64; ++i) {
                     const float p = tc_ex2(fmaf(v[i], CE_L2E, nl)) - (c + i == tgt ? 1.f : 0.f);
@@ -401,6 +404,7 @@ struct CeGrad {
             for (int c = c0; c < c0 + GM_EPI_COLS && t.n0 + c < d; c += 32) {
                 float v[32];
                 tc_tmem_ld32(taddr + (uint32_t)c, v);
+                if (c + 32 == c0 + GM_EPI_COLS) release();
                 if (t.nk == 0) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] = 0.f;
@@ -416,8 +420,8 @@ struct CeGrad {
 #pragma unroll 1
             for (int c = c0; c < c0 + GM_EPI_COLS && t.n0 + c < d; c += 64) {
                 float x[64];
-                gm_ld32(taddr + (uint32_t)c, x);
-                gm_ld32(taddr + (uint32_t)c + 32, x + 32);
+                gm_ld64(taddr + (uint32_t)c, x);
+                if (c + 64 == c0 + GM_EPI_COLS) release();
 #pragma unroll
                 for (int i = 0; i < 64; ++i) x[i] *= st.gmax;
                 if (v >= v1) continue;

@@ -30,8 +30,10 @@
 //     __device__ void load(const Tile&, int kb, int rank, uint8_t* a, uint8_t* b, uint32_t bar) const;
 //     __device__ uint32_t stage_bytes() const;       // that load() copies per CTA
 //     __device__ bool a_mn(const Tile&) const, b_mn(const Tile&) const;  // operand stored MN-major
-//     // the first or second half of one row's columns
-//     __device__ void epilogue(const State&, const Tile&, uint32_t taddr, int row_in_tile, int half, const GmStage&) const;
+//     // the first or second half of one row's columns; gives the accumulator back
+//     // as soon as it has been read
+//     __device__ void epilogue(const State&, const Tile&, uint32_t taddr, int row_in_tile, int half, const GmStage&,
+//                              GmRelease&) const;
 //   };
 //
 // Every wait on a barrier is bounded; on expiry the kernel records
@@ -228,6 +230,27 @@ __device__ __forceinline__ uint32_t gm_in_cta(const void* p, uint32_t rank) {
 }
 
 constexpr int GM_SLOTS = 4;  // tiles published ahead of the last reader
+
+// Gives an accumulator back to the products: an epilogue calls it (the whole warp)
+// after its last read of it, before it converts and stores what it read.
+template <bool PAIR>
+struct GmRelease {
+    uint64_t* bar;
+    uint32_t first_bar;  // the barrier in the pair's first CTA
+    int lane;
+    bool done;
+    __device__ __forceinline__ void operator()() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+            if constexpr (PAIR)
+                gm_arrive_remote(first_bar);
+            else
+                tc_arrive(bar);
+        }
+        done = true;
+    }
+};
 
 template <int STAGES>
 struct GmSmem {
@@ -445,16 +468,10 @@ __device__ __forceinline__ void gm_run(const P& p, const GmCtl& ctl) {
             const int acc = i & 1;
             if (!tc_wait(&sm->tmem_full[acc], (i >> 1) & 1, abort_flag, ctl.err, ctl.wait_ns)) break;
             tc_fence_after();
+            GmRelease<PAIR> release{&sm->tmem_empty[acc], acc ? empty1 : empty0, lane, false};
             p.epilogue(st, t, tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * GM_TILE), (int)rank * GM_HALF + q * 32 + lane,
-                       half, sg);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                if constexpr (PAIR)
-                    gm_arrive_remote(acc ? empty1 : empty0);
-                else
-                    tc_arrive(&sm->tmem_empty[acc]);
-            }
+                       half, sg, release);
+            if (!release.done) release();
         }
         if (P::STAGED && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
@@ -470,19 +487,26 @@ __device__ __forceinline__ void gm_run(const P& p, const GmCtl& ctl) {
     }
 }
 
-// 32 consecutive accumulator words of this thread's lane.
-__device__ __forceinline__ void gm_ld32_i32(uint32_t taddr, int32_t (&v)[32]) {
-    float f[32];
-    tc_tmem_ld32(taddr, f);
+// 64 consecutive columns: two loads, one wait.
+__device__ __forceinline__ void gm_ld64(uint32_t taddr, float (&v)[64]) {
+    uint32_t r[64];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __float_as_int(f[i]);
-}
-
-__device__ __forceinline__ void gm_ld32(uint32_t taddr, float* v) {
-    float f[32];
-    tc_tmem_ld32(taddr, f);
+    for (int h = 0; h < 2; ++h)
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+            "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+            "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+            : "=r"(r[32 * h + 0]), "=r"(r[32 * h + 1]), "=r"(r[32 * h + 2]), "=r"(r[32 * h + 3]), "=r"(r[32 * h + 4]),
+              "=r"(r[32 * h + 5]), "=r"(r[32 * h + 6]), "=r"(r[32 * h + 7]), "=r"(r[32 * h + 8]), "=r"(r[32 * h + 9]),
+              "=r"(r[32 * h + 10]), "=r"(r[32 * h + 11]), "=r"(r[32 * h + 12]), "=r"(r[32 * h + 13]), "=r"(r[32 * h + 14]),
+              "=r"(r[32 * h + 15]), "=r"(r[32 * h + 16]), "=r"(r[32 * h + 17]), "=r"(r[32 * h + 18]), "=r"(r[32 * h + 19]),
+              "=r"(r[32 * h + 20]), "=r"(r[32 * h + 21]), "=r"(r[32 * h + 22]), "=r"(r[32 * h + 23]), "=r"(r[32 * h + 24]),
+              "=r"(r[32 * h + 25]), "=r"(r[32 * h + 26]), "=r"(r[32 * h + 27]), "=r"(r[32 * h + 28]), "=r"(r[32 * h + 29]),
+              "=r"(r[32 * h + 30]), "=r"(r[32 * h + 31])
+            : "r"(taddr + 32 * h));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = f[i];
+    for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 // Maximum that keeps a NaN.

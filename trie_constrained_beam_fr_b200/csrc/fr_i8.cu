@@ -274,20 +274,25 @@ struct I8Base {
         gm_tma_load<PAIR>(&map_w, b, bar, kb * GM_KB_BYTES, t.n0 + rank * (bn / 2));
         if constexpr (!PAIR) gm_tma_load<PAIR>(&map_w, b + bn / 2 * GM_KB_BYTES, bar, kb * GM_KB_BYTES, t.n0 + bn / 2);
     }
-    // y of 32 columns from n on: the row's scale first, then the channel's
-    __device__ __forceinline__ void scaled(uint32_t taddr, int n, float xscale, float* v) const {
-        float4 w[8];  // loaded before the accumulator is waited for
-        if (ws_vec && n + 32 <= N) {
+    // y of CW columns from n on: the row's scale first, then the channel's
+    template <int CW>
+    __device__ __forceinline__ void scaled(uint32_t taddr, int n, float xscale, float (&v)[CW], bool last,
+                                           GmRelease<PAIR>& release) const {
+        float4 w[CW / 4];  // loaded before the accumulator is waited for
+        if (ws_vec && n + CW <= N) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = __ldg(reinterpret_cast<const float4*>(ws + n) + i);
+            for (int i = 0; i < CW / 4; ++i) w[i] = __ldg(reinterpret_cast<const float4*>(ws + n) + i);
         } else {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) (&w[i / 4].x)[i % 4] = n + i < N ? __ldg(ws + n + i) : 0.f;
+            for (int i = 0; i < CW; ++i) (&w[i / 4].x)[i % 4] = n + i < N ? __ldg(ws + n + i) : 0.f;
         }
-        int32_t acc[32];
-        gm_ld32_i32(taddr, acc);
+        if constexpr (CW == 64)
+            gm_ld64(taddr, v);
+        else
+            tc_tmem_ld32(taddr, v);
+        if (last) release();
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = (float)acc[i] * xscale * (&w[i / 4].x)[i % 4];
+        for (int i = 0; i < CW; ++i) v[i] = (float)__float_as_int(v[i]) * xscale * (&w[i / 4].x)[i % 4];
     }
 };
 
@@ -310,15 +315,15 @@ struct I8Out : I8Base<PAIR_> {
     // rows start on 16 bytes; all when rows are whole 16-byte pieces, else the
     // whole groups of columns (a clipped TMA store fills its last 16 bytes).
     int32_t staged;
-    __device__ __forceinline__ void epilogue(const State&, const Tile& t, uint32_t taddr, int r, int half, const GmStage& sg) const {
+    __device__ __forceinline__ void epilogue(const State&, const Tile& t, uint32_t taddr, int r, int half, const GmStage& sg,
+                                             GmRelease<PAIR_>& release) const {
         constexpr int CW = 128 / sizeof(T);  // columns per staged store
         const int row = t.m0 + r, lane = threadIdx.x & 31, row0 = row - lane, cols = max(bn / 2, 64);
         const float xscale = row < rows ? xs[row] : 0.f;
 #pragma unroll 1
         for (int c = half * cols; c < min((half + 1) * cols, bn) && t.n0 + c < N; c += CW) {
             float v[CW];
-#pragma unroll
-            for (int k = 0; k < CW; k += 32) scaled(taddr + (uint32_t)(c + k), t.n0 + c + k, xscale, v + k);
+            scaled(taddr + (uint32_t)c, t.n0 + c, xscale, v, c + CW == min((half + 1) * cols, bn), release);
             if (row0 >= rows) continue;
             gm_put(sg, lane, v);
             if (t.n0 + c < staged)
@@ -344,7 +349,8 @@ struct I8Lse : I8Base<PAIR_> {
     int32_t n_parts;
     float* slice;     // [rows, sid_span]
     int32_t sid_base, sid_span;
-    __device__ __forceinline__ void epilogue(const State&, const Tile& t, uint32_t taddr, int r, int half, const GmStage&) const {
+    __device__ __forceinline__ void epilogue(const State&, const Tile& t, uint32_t taddr, int r, int half, const GmStage&,
+                                             GmRelease<PAIR_>& release) const {
         const int c0 = half * GM_EPI_COLS;
         const int row = t.m0 + r;
         const float xscale = row < rows ? xs[row] : 0.f;
@@ -353,7 +359,7 @@ struct I8Lse : I8Base<PAIR_> {
         for (int c = c0; c < c0 + GM_EPI_COLS && t.n0 + c < N; c += 32) {
             const int n = t.n0 + c;
             float v[32];
-            scaled(taddr + (uint32_t)c, n, xscale, v);
+            scaled(taddr + (uint32_t)c, n, xscale, v, c + 32 == c0 + GM_EPI_COLS, release);
             const int lo = max(n, sid_base), hi = min(n + 32, sid_base + sid_span);
             if (row < rows && lo < hi) {
                 float* dst = slice + (int64_t)row * sid_span;
