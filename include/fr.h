@@ -363,9 +363,11 @@ void fr_embed_destroy(fr_embed* embed);
  *
  * h and W: base 16-byte aligned, pitches multiples of 8 elements (else
  * FR_ERR_INVALID_ARG).  The gradients' base and pitch only need the element's
- * alignment; 16-byte aligned ones are written faster.  init allocates about
- * max_rows * (32 KB + 6 d) bytes.  The kernels take one CTA per SM and all of
- * its tensor memory while they run, as fr_lmhead_run does. */
+ * alignment; 16-byte aligned ones are written faster.  Limits: d <= 2^20, V <=
+ * 2^24, max_rows * V <= 2^44.  init allocates max_rows * (6 d + V / 16) bytes and
+ * two pieces of G: 1 GB or 16 KB * max_rows, whichever is more, or less when V is
+ * one piece (2 V * max_rows).  The kernels take one CTA per SM and all of its
+ * tensor memory while they run, as fr_lmhead_run does. */
 typedef struct fr_ce fr_ce;
 fr_status fr_ce_init(int32_t V, int32_t d, int32_t max_rows, fr_ce** out);
 fr_status fr_ce_loss(fr_ce* ce, const void* hidden_dev, int64_t ldh, const void* weight_dev, int64_t ldw,
@@ -390,7 +392,8 @@ void fr_ce_destroy(fr_ce* ce);
  *
  * fr_i8_init keeps the weight: int8 [N, ldw] and fp32 channel scales [N]
  * (caller-owned, valid and unchanged for the handle's lifetime), d <= 131,071
- * (the int32 sums cannot overflow), and the SID range for fr_i8_lse.
+ * (the int32 sums cannot overflow), N and max_rows <= 2^24, N * max_rows <= 2^44,
+ * and the SID range for fr_i8_lse.
  *
  * fr_i8_matmul:  out[r][n] = (sum_j xq[r][j] * wq[n][j]) * xscale[r] * wscale[n]
  *   into out [rows, ldo] of FR_F32 or FR_BF16, ldo >= N: with the lm_head as the

@@ -169,6 +169,51 @@ def test_gradients_against_differences(handle):
         assert abs(diff - along) <= slack + third
 
 
+@pytest.mark.parametrize("scale", [1e-36, 1e-41, 1e34])
+def test_small_and_large_incoming_gradients(handle, scale):
+    """Gradients of tiny (normal and subnormal) and huge incoming values: bf16
+    has fp32's exponent range, so they are those of 1 times the scale; a result
+    below 2^-126 is off by at most a subnormal step of bf16 (2^-133)."""
+    rows, V, d = 50, 120, 32
+    h, w, t, gl = _inputs(rows, V, d, 13, ignored=0.1)
+    gl = (gl.sign() * scale).contiguous()  # one magnitude
+    ce = handle(V, d, rows)
+    loss, lse = _loss(ce, h, w, t)
+    dh, dw = _grad(ce, h, w, t, lse, gl)
+    ref = _reference(h, w, t, gl)
+    for got, name in ((dh, "dh"), (dw, "dw")):
+        want, bound = ref[name]
+        # fp32 products and sums below 2^-126 lose up to half a subnormal step each
+        slack = 2.0 ** -133 + (rows + V) * 2.0 ** -149
+        assert torch.all((got.double().cpu() - want).abs() <= bound + slack)
+
+
+def test_no_incoming_gradient(handle):
+    rows, V, d = 30, 70, 16
+    h, w, t, gl = _inputs(rows, V, d, 14)
+    ce = handle(V, d, rows)
+    loss, lse = _loss(ce, h, w, t)
+    dh, dw = _grad(ce, h, w, t, lse, torch.zeros_like(gl))
+    assert torch.all(dh == 0) and torch.all(dw == 0)
+
+
+def test_a_nan_in_one_row_stays_in_its_gradients(handle):
+    """A NaN or infinite incoming gradient of one row reaches that row's dh and,
+    as the formula says, dW; the other rows' dh are what they were."""
+    rows, V, d = 40, 90, 24
+    h, w, t, gl = _inputs(rows, V, d, 15, ignored=0.0)
+    ce = handle(V, d, rows)
+    loss, lse = _loss(ce, h, w, t)
+    ref = _reference(h, w, t, gl)
+    for bad in (float("nan"), float("inf")):
+        g2 = gl.clone()
+        g2[7] = bad
+        dh, dw = _grad(ce, h, w, t, lse, g2)
+        keep = [r for r in range(rows) if r != 7]
+        _close(dh[keep], tuple(x[keep] for x in ref["dh"]))
+        assert not torch.any(torch.isfinite(dh[7])) and not torch.all(torch.isfinite(dw))
+
+
 def test_rows_that_do_not_count_reach_nothing(handle):
     rows, V, d = 200, 500, 64
     h, w, t, gl = _inputs(rows, V, d, 11, ignored=0.4)
@@ -200,9 +245,9 @@ def test_no_row_counts(handle, rows):
 
 
 def test_fewer_rows_than_the_handle_holds(handle):
-    V, d = 700, 96
+    V, d = 9000, 96
     h, w, t, gl = _inputs(400, V, d, 21)
-    ce = handle(V, d, 400)
+    ce = handle(V, d, 20000)  # sized for far more: pieces and tiles go by the call's rows
     for n in (400, 3, 129):
         loss, lse = _loss(ce, h[:n], w, t[:n])
         dh, dw = _grad(ce, h[:n], w, t[:n], lse, gl[:n])

@@ -57,6 +57,17 @@ __device__ __forceinline__ void em_load(const float* p, float (&v)[VEC]) {
         v[0] = *p;
     }
 }
+// The same past L1: what other CTAs wrote.
+template <int VEC>
+__device__ __forceinline__ void em_load_cg(const float* p, float (&v)[VEC]) {
+    if (VEC == 8) {
+        const float4 a = __ldcg(reinterpret_cast<const float4*>(p)), b = __ldcg(reinterpret_cast<const float4*>(p + 4));
+        v[0] = a.x, v[1 % VEC] = a.y, v[2 % VEC] = a.z, v[3 % VEC] = a.w;
+        v[4 % VEC] = b.x, v[5 % VEC] = b.y, v[6 % VEC] = b.z, v[7 % VEC] = b.w;
+    } else {
+        v[0] = __ldcg(p);
+    }
+}
 template <int VEC>
 __device__ __forceinline__ void em_load(const __nv_bfloat16* p, float (&v)[VEC]) {
     if (VEC == 8) {
@@ -373,11 +384,11 @@ __global__ void __launch_bounds__(EM_THREADS)
         __threadfence();
         if (j < d) {
             float sum[VEC];
-            em_load<VEC>(part + (2 * c + 1) * pitch + j, sum);
+            em_load_cg<VEC>(part + (2 * c + 1) * pitch + j, sum);
 #pragma unroll 8
             for (int64_t k = c + 1; k <= e; ++k) {
                 float v[VEC];
-                em_load<VEC>(part + 2 * k * pitch + j, v);
+                em_load_cg<VEC>(part + 2 * k * pitch + j, v);
 #pragma unroll
                 for (int q = 0; q < VEC; ++q) sum[q] += v[q];
             }
