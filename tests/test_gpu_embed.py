@@ -100,6 +100,9 @@ def _grad_reference(grad, tok, V, scale, before):
     (1024, 500, 264, F32, BF16, False, 0, 0),     # the most tokens of the one-kernel form
     (1025, 500, 264, F32, BF16, False, 0, 0),     # the fewest of the sorted form
     (300000, 700, 8, F32, F32, False, 0, 0),      # several tiles per sorting CTA
+    (32769, 300001, 9, F32, F32, False, 0, 0),
+    (20000, 511, 16, F32, F32, False, 0, 0),      # keys that fill their digits
+    (5000, 262143, 16, F32, F32, False, 0, 0),
 ])
 def test_grad(handle, kind, n, V, d, tg, tt, add, pad, offset):
     g = torch.Generator().manual_seed(n + V)
