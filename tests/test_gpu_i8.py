@@ -73,6 +73,29 @@ def test_quantize(dtype, rows, d, pad):
     assert torch.all(q[:, d:] == 99)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_quantize_near_halves(dtype):
+    """Values on and next to the borders between two steps, at scales from
+    subnormal to large: the rounded IEEE quotients, bit for bit."""
+    g = torch.Generator().manual_seed(2)
+    rows, d = 400, 1024
+    x = torch.empty(rows, d)
+    top = torch.exp2(torch.linspace(-146, 127, rows))[:, None] * (1 + torch.rand(rows, 1, generator=g))
+    top = torch.where(torch.isfinite(top), top, torch.full_like(top, 3e38))
+    half = (torch.randint(-127, 127, (rows, d), generator=g) + 0.5) / 127
+    x = half.double() * top.double() * (1 + torch.randint(-3, 4, (rows, d), generator=g).double() * 2.0 ** -24)
+    x[:, 0] = top[:, 0].double()
+    x = x.float().to(dtype).cuda()
+    q, s = torch.empty(rows, d, dtype=torch.int8, device="cuda"), torch.empty(rows, device="cuda")
+    fr.fr_i8_quantize(x, q, s)
+    xf = x.float().cpu().numpy()
+    want_s = np.abs(xf).max(1) / np.float32(127)
+    live = want_s > 0  # below 127 subnormal steps the scale itself may round to zero
+    want = np.clip(np.rint(xf / np.where(live, want_s, np.float32(1))[:, None]), -127, 127) * live[:, None]
+    assert np.array_equal(s.cpu().numpy(), want_s)
+    assert np.array_equal(q.cpu().numpy(), want.astype(np.int8))
+
+
 def test_quantize_rows_that_are_not_finite():
     x = torch.ones(3, 40, device="cuda")
     x[0, 7], x[1, 39] = float("nan"), float("-inf")
