@@ -354,9 +354,12 @@ struct CeGrad {
         g -= st.dw_tiles;
         t.type = GT;
         int32_t m, n;
-        gm_grouped(g, st.m_tiles, (w1 - w0 + GM_TILE - 1) / GM_TILE, m, n);
+        // last tokens first: the weight's end is what the loss left in L2, and its
+        // start is what dh's first tiles then find there
+        const int32_t n_tiles = (w1 - w0 + GM_TILE - 1) / GM_TILE;
+        gm_grouped(g, st.m_tiles, n_tiles, m, n);
         t.m0 = m * TM;
-        t.n0 = n * GM_TILE;
+        t.n0 = (n_tiles - 1 - n) * GM_TILE;
         t.k0 = 0;
         t.nk = (d + 63) / 64;
         t.idesc = gm_idesc(false, PAIR);
