@@ -202,6 +202,10 @@ struct CeLoss {
     float2* partial;  // [cap, 2 * n_tiles] (max, scaled sum) of 128 tokens each
     float* xt;        // [cap] the target's logit
 
+    __device__ __forceinline__ void prefetch() const {
+        gm_prefetch(&map_h);
+        gm_prefetch(&map_w);
+    }
     __device__ __forceinline__ State begin() const {
         const int32_t n = *rows.n;
         return {n, (n + TM - 1) / TM};
@@ -308,6 +312,15 @@ struct CeGrad {
     int64_t ldw;
     int32_t dw_staged;               // columns of dW that go out through shared memory and TMA
 
+    __device__ __forceinline__ void prefetch() const {
+        gm_prefetch(&map_h_k);
+        gm_prefetch(&map_w_k);
+        gm_prefetch(&map_g_k);
+        gm_prefetch(&map_w_mn);
+        gm_prefetch(&map_g_mn);
+        gm_prefetch(&map_h_mn);
+        gm_prefetch(&map_g_out);
+    }
     __device__ __forceinline__ State begin() const {
         State st;
         st.n = *rows.n;

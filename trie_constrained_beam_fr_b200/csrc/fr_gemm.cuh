@@ -22,6 +22,7 @@
 //     static constexpr bool STAGED;        // the epilogue stores through shared memory
 //     static constexpr int STAGES;         // ring depth
 //     static constexpr bool DYNAMIC;       // tiles of unequal length: the pairs take the next one from a counter
+//     __device__ void prefetch() const;              // its tensor maps
 //     struct Tile { int nk; uint32_t idesc; ... };   // K stages; instruction descriptor
 //     struct State { ... };                          // what begin() read after the previous kernel
 //     __device__ State begin() const;
@@ -231,6 +232,11 @@ __device__ __forceinline__ uint32_t gm_in_cta(const void* p, uint32_t rank) {
 
 constexpr int GM_SLOTS = 4;  // tiles published ahead of the last reader
 
+// Fetches a tensor map (a kernel argument) ahead of the first copy that goes by it.
+__device__ __forceinline__ void gm_prefetch(const CUtensorMap* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 // Gives an accumulator back to the products: an epilogue calls it (the whole warp)
 // after its last read of it, before it converts and stores what it read.
 template <bool PAIR>
@@ -304,6 +310,7 @@ __device__ __forceinline__ void gm_run(const P& p, const GmCtl& ctl) {
     const uint32_t rank = PAIR ? gm_cta_rank() : 0;
     const uint32_t pair = PAIR ? blockIdx.x >> 1 : blockIdx.x, pairs = PAIR ? gridDim.x >> 1 : gridDim.x;  // (or single CTAs)
 
+    if (threadIdx.x == 32) p.prefetch();
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             tc_mbar_init(&sm->full[s], 1);
@@ -517,13 +524,18 @@ __device__ __forceinline__ float gm_max_nan(float a, float b) {
 }
 
 // Folds 32 values into a running (max m, sum s of e^(x - m)); a NaN stays in
-// both.
+// both.  Maximum and sum go through four chains: with two epilogue warps per
+// scheduler one chain's latency shows where a tile's products are short.
 __device__ __forceinline__ void gm_lse_fold(const float (&v)[32], float& m, float& s) {
     constexpr float L2E = 1.4426950408889634f;
-    float cm = v[0];
+    float c[4];
 #pragma unroll
-    for (int i = 1; i < 32; ++i) cm = gm_max_nan(cm, v[i]);
-    cm = gm_max_nan(cm, m);
+    for (int k = 0; k < 4; ++k) {
+        c[k] = gm_max_nan(v[k], v[k + 4]);
+#pragma unroll
+        for (int i = 8; i < 32; i += 4) c[k] = gm_max_nan(c[k], v[i + k]);
+    }
+    const float cm = gm_max_nan(gm_max_nan(gm_max_nan(c[0], c[1]), gm_max_nan(c[2], c[3])), m);
     if (cm != m) {
         s = (m == -INFINITY) ? 0.f : s * tc_ex2((m - cm) * L2E);
         m = cm;
@@ -531,7 +543,12 @@ __device__ __forceinline__ void gm_lse_fold(const float (&v)[32], float& m, floa
     if (m != -INFINITY) {
         const float nm = -m * L2E;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) s += tc_ex2(fmaf(v[i], L2E, nm));
+        for (int k = 0; k < 4; ++k) {
+            c[k] = tc_ex2(fmaf(v[k], L2E, nm));
+#pragma unroll
+            for (int i = 4; i < 32; i += 4) c[k] += tc_ex2(fmaf(v[i + k], L2E, nm));
+        }
+        s += (c[0] + c[1]) + (c[2] + c[3]);
     }
 }
 
@@ -580,17 +597,20 @@ __device__ __forceinline__ void gm_put(const GmStage& sg, int lane, const float 
                                         __float_as_uint(v[4 * j + 3])));
 }
 
-// Writes the buffer's first `rows` rows and `cols` columns of T to dst with
-// plain stores, a row at a time: for rows that TMA cannot address (15 us of 29
-// on 333 x 1,003 fp32 values were a lane's stores to its own row).
+// Writes columns [from, to) of the buffer's first `rows` rows of T to dst with
+// plain stores, a row at a time: for rows that TMA cannot address (15 us of 29 on
+// 333 x 1,003 fp32 values were a lane's stores to its own row).
 template <class T>
-__device__ __forceinline__ void gm_write_plain(const GmStage& sg, int lane, T* dst, int64_t ld, int rows, int cols) {
+__device__ __forceinline__ void gm_write_plain(const GmStage& sg, int lane, T* dst, int64_t ld, int rows, int to,
+                                               int from = 0) {
     __syncwarp();
+#pragma unroll 4
     for (int r = 0; r < rows; ++r) {
 #pragma unroll
         for (int c = lane; c < 128 / (int)sizeof(T); c += 32) {
             const int at = c * (int)sizeof(T);
-            if (c < cols) dst[r * ld + c] = *reinterpret_cast<const T*>(sg.buf + r * 128 + (((at >> 4) ^ (r & 7)) << 4) + (at & 15));
+            if (c >= from && c < to)
+                dst[r * ld + c] = *reinterpret_cast<const T*>(sg.buf + r * 128 + (((at >> 4) ^ (r & 7)) << 4) + (at & 15));
         }
     }
 }

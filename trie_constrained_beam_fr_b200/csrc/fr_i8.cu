@@ -142,8 +142,8 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR)
 // the tokens lie in shared memory (zeros behind d), __dp4a multiplies and one
 // warp reduction per value adds the lanes.  A warp takes 4 channels at a time,
 // so the channels spread evenly over the SMs.  151,936 channels x 2,048 values:
-// 52 us for 1 to 4 tokens (6.0 TB/s) where the tiles take 68 to 86; 8 tokens
-// (bound by __dp4a) took 85 us against 80 on tiles.
+// 49 to 58 us for 1 to 4 tokens (6.3 to 5.4 TB/s) where the tiles take 60 to 62; 8
+// tokens (bound by __dp4a) took 85 us.
 constexpr int FEW_ROWS = 4;
 constexpr int FEW_THREADS = 256;
 constexpr int FEW_CH = 4;
@@ -206,7 +206,9 @@ __global__ void __launch_bounds__(FEW_THREADS) k_i8_few(const int8_t* __restrict
                 }
             }
         };
-        // whole pieces, FEW_STEPS x 512 values with all their loads in flight
+        // FEW_STEPS x 512 values at a time, all their loads in flight; then what is
+        // left in one go.  A row's last piece may reach into its padding (the tokens
+        // hold zeros there), but not behind the last row.
         int32_t k = lane << 4;
         for (; k - (lane << 4) + FEW_STEPS * 512 <= d; k += FEW_STEPS * 512) {
             int4 w[FEW_STEPS][FEW_CH];
@@ -217,21 +219,31 @@ __global__ void __launch_bounds__(FEW_THREADS) k_i8_few(const int8_t* __restrict
 #pragma unroll
             for (int u = 0; u < FEW_STEPS; ++u) add(w[u], k + u * 512);
         }
-        for (; k < pitch; k += 512) {
+        const bool last_row = n0 + FEW_CH >= N && d < pitch;
+        if (k - (lane << 4) < d) {
+            int4 w[FEW_STEPS][FEW_CH];
+#pragma unroll
+            for (int u = 0; u < FEW_STEPS; ++u)
+#pragma unroll
+                for (int c = 0; c < FEW_CH; ++c) {
+                    w[u][c] = make_int4(0, 0, 0, 0);
+                    if (k + u * 512 < (last_row ? d & ~15 : pitch)) w[u][c] = few_load(src[c] + k + u * 512);
+                }
+#pragma unroll
+            for (int u = 0; u < FEW_STEPS; ++u)
+                if (k + u * 512 < pitch) add(w[u], k + u * 512);
+        }
+        if (last_row && lane == 0) {
             int4 w[FEW_CH];
 #pragma unroll
             for (int c = 0; c < FEW_CH; ++c) {
-                if (k + 16 <= d) {
-                    w[c] = few_load(src[c] + k);
-                } else {  // a row's last piece: nothing is read behind d
-                    w[c] = make_int4(0, 0, 0, 0);
-                    int8_t* b = reinterpret_cast<int8_t*>(&w[c]);
+                w[c] = make_int4(0, 0, 0, 0);
+                int8_t* b = reinterpret_cast<int8_t*>(&w[c]);
 #pragma unroll
-                    for (int j = 0; j < 15; ++j)
-                        if (k + j < d) b[j] = src[c][k + j];
-                }
+                for (int j = 0; j < 15; ++j)
+                    if ((d & ~15) + j < d) b[j] = src[c][(d & ~15) + j];
             }
-            add(w, k);
+            add(w, d & ~15);
         }
         int32_t mine = 0;  // lane r * FEW_CH + c keeps token r's channel c
 #pragma unroll
@@ -264,11 +276,16 @@ struct I8Base {
     };
     struct State {};
     CUtensorMap map_x, map_w;
+    __device__ __forceinline__ void prefetch() const {
+        gm_prefetch(&map_x);
+        gm_prefetch(&map_w);
+    }
     int32_t rows, N, k_blocks, m_tiles, n_tiles;
     int32_t bn;  // columns of a tile: 256, or fewer where that leaves SMs without one
     const float* xs;
     const float* ws;
     int32_t ws_vec;  // ws starts on 16 bytes
+    int32_t small;   // |sums| <= 2^22 (d <= 256)
 
     __device__ __forceinline__ State begin() const { return {}; }
     __device__ __forceinline__ bool tile(const State&, uint32_t g, Tile& t) const {
@@ -307,8 +324,17 @@ struct I8Base {
         else
             tc_tmem_ld32(taddr, v);
         if (last) release();
+        if (small) {
+            // sums up to 2^22 become fp32 by 1.5 * 2^23 and its subtraction (exact): the
+            // conversion instruction runs at the exponential's quarter rate, which
+            // shows where few K stages hide it
 #pragma unroll
-        for (int i = 0; i < CW; ++i) v[i] = (float)__float_as_int(v[i]) * xscale * (&w[i / 4].x)[i % 4];
+            for (int i = 0; i < CW; ++i)
+                v[i] = (__int_as_float(__float_as_int(v[i]) + 0x4B400000) - 12582912.f) * xscale * (&w[i / 4].x)[i % 4];
+        } else {
+#pragma unroll
+            for (int i = 0; i < CW; ++i) v[i] = (float)__float_as_int(v[i]) * xscale * (&w[i / 4].x)[i % 4];
+        }
     }
 };
 
@@ -359,16 +385,16 @@ struct I8Lse : I8Base<PAIR_> {
     using Base::rows;
     using Base::xs;
     using Base::scaled;
-    static constexpr bool STAGED = false;
-    static constexpr int STAGES = PAIR_ ? 7 : 4;
+    static constexpr bool STAGED = true;
+    static constexpr int STAGES = PAIR_ ? 6 : 4;
     float2* partial;  // [rows, n_parts] (max, scaled sum) of 128 columns each
     int32_t n_parts;
     float* slice;     // [rows, sid_span]
     int32_t sid_base, sid_span;
-    __device__ __forceinline__ void epilogue(const State&, const Tile& t, uint32_t taddr, int r, int half, const GmStage&,
+    __device__ __forceinline__ void epilogue(const State&, const Tile& t, uint32_t taddr, int r, int half, const GmStage& sg,
                                              GmRelease<PAIR_>& release) const {
         const int c0 = half * GM_EPI_COLS;
-        const int row = t.m0 + r;
+        const int row = t.m0 + r, lane = threadIdx.x & 31, row0 = row - lane;
         const float xscale = row < rows ? xs[row] : 0.f;
         float m = -INFINITY, s = 0.f;
 #pragma unroll 1
@@ -376,12 +402,13 @@ struct I8Lse : I8Base<PAIR_> {
             const int n = t.n0 + c;
             float v[32];
             scaled(taddr + (uint32_t)c, n, xscale, v, c + 32 == c0 + GM_EPI_COLS, release);
+            // the slice's columns of this chunk, a row at a time (a lane's stores to
+            // its own row took 267 us instead of 117 on 5,555 rows x 4,757 slice columns)
             const int lo = max(n, sid_base), hi = min(n + 32, sid_base + sid_span);
-            if (row < rows && lo < hi) {
-                float* dst = slice + (int64_t)row * sid_span;
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    if (n + i >= lo && n + i < hi) dst[n + i - sid_base] = v[i];
+            if (lo < hi && row0 < rows) {
+                gm_put(sg, lane, v);
+                gm_write_plain(sg, lane, slice + (int64_t)row0 * sid_span - sid_base + n, sid_span, min(32, rows - row0), hi - n,
+                               lo - n);
             }
             if (n + 32 > N) {
 #pragma unroll
@@ -458,6 +485,7 @@ fr_status i8_base(fr_i8* h, const int8_t* xq, int64_t ldx, const float* xs, int3
     b->n_tiles = (h->N + b->bn - 1) / b->bn;
     b->xs = xs;
     b->ws = h->ws;
+    b->small = h->d <= 256;  // 128 * 128 * 256 = 2^22
     b->ws_vec = (reinterpret_cast<uintptr_t>(h->ws) & 15u) == 0;
     return FR_OK;
 }
