@@ -308,7 +308,8 @@ void fr_beam_destroy(fr_beam* beam);
  * sticky, first error first, read with a synchronisation of the last run's
  * stream (not while that stream is being captured). */
 
-/* Token embedding.  V x d table, up to max_tokens tokens per call (< 2^30).
+/* Token embedding.  V x d table (V <= 2^30, d <= 2^24), up to max_tokens tokens
+ * per call (< 2^30).
  * Tokens are int32 in [0, V) or -1 (a dead beam or padding); any other value
  * is treated as -1 and recorded as FR_ERR_CODE_RANGE.
  *
@@ -387,8 +388,8 @@ void fr_ce_destroy(fr_ce* ce);
  *   nearest even (IEEE fp32 quotients, clamped to [-127, 127]),
  * for tokens before a product, or once for a weight's output channels.  A row
  * of zeros has scale 0 and zeros; a row with a NaN or an infinity keeps it as
- * its scale with zeros, so its products are NaN.  q: int8 [rows, ldq], columns
- * d.. left as they are.  It needs no handle.
+ * its scale with zeros, so its products are NaN.  d <= 2^30.  q: int8 [rows,
+ * ldq], columns d.. left as they are.  It needs no handle.
  *
  * fr_i8_init keeps the weight: int8 [N, ldw] and fp32 channel scales [N]
  * (caller-owned, valid and unchanged for the handle's lifetime), d <= 131,071

@@ -142,7 +142,7 @@ def test_the_largest_sums(handle, value):
 
 
 @pytest.mark.parametrize("rows,N,d,base,span", [(1, 64, 32, 0, 64), (3, 300, 64, 100, 37), (40, 1000, 520, 990, 10), (130, 700, 256, 200, 0),
-                                                (300, 5000, 96, 0, 768)])
+                                                (300, 5000, 96, 0, 768), (300, 1500, 200, 77, 1301), (33, 2000, 257, 129, 640)])
 def test_lse(handle, rows, N, d, base, span):
     g = torch.Generator().manual_seed(rows + N)
     xq, wq = _ints(g, rows, d), _ints(g, N, d)
@@ -158,6 +158,40 @@ def test_lse(handle, rows, N, d, base, span):
     bound = 3.1 * 2.0 ** -24 * big + (256 + N / 8192 + 8) * 2.0 ** -24 + 2.0 ** -22 + 2.0 ** -23 * (want.abs() + 3 * big)
     assert torch.all((lse.double().cpu() - want).abs() <= bound)
     assert torch.all((sl.double().cpu() - y[:, base:base + span]).abs() <= 3.1 * 2.0 ** -24 * y[:, base:base + span].abs())
+
+
+@pytest.mark.parametrize("rows", [3, 40, 140])
+@pytest.mark.parametrize("d", [255, 256, 257])
+def test_sums_at_the_end_of_the_short_rows(handle, rows, d):
+    """Sums of short rows (up to 2^22) and of longer ones are converted in two
+    ways: exact at the border, with values at both ends of the range."""
+    xq, wq = _padded(rows, d, torch.int8, 16), _padded(70, d, torch.int8, 16)
+    xq.fill_(-128), wq.fill_(-128)
+    xq[1], wq[1::2] = 127, 127
+    xq[2, ::2] = 0
+    h = handle(wq, torch.ones(70, device="cuda"), rows, 3, 64)
+    xs, out = torch.ones(rows, device="cuda"), torch.empty(rows, 70, device="cuda")
+    fr.fr_i8_matmul(h, xq, xs, out)
+    want = _product(xq, xs, wq, torch.ones(70))
+    assert torch.equal(out.double().cpu(), want)
+    lse, sl = torch.empty(rows, device="cuda"), torch.empty(rows, 64, device="cuda")
+    fr.fr_i8_lse(h, xq, xs, lse, sl)
+    assert torch.equal(sl.double().cpu(), want[:, 3:67])
+
+
+@pytest.mark.parametrize("rows", [1, 3])
+@pytest.mark.parametrize("N,d", [(5, 16), (5, 17), (8, 527), (9, 2048), (9, 2049), (10, 2063), (31, 2064), (6, 5000), (6, 6143)])
+def test_the_few_rows_last_pieces(handle, rows, N, d):
+    """Rows that end anywhere in the pieces, and a weight that ends with its last row."""
+    g = torch.Generator().manual_seed(N * d)
+    xq, pitch = _ints(g, rows, d), -(-d // 16) * 16
+    flat = torch.randint(-127, 128, ((N - 1) * pitch + d,), generator=g, dtype=torch.int32).to(torch.int8).cuda()
+    wq = flat.as_strided((N, d), (pitch, 1))
+    h = handle(wq, torch.ones(N, device="cuda"), rows)
+    xs, out = torch.ones(rows, device="cuda"), torch.empty(rows, N, device="cuda")
+    fr.fr_i8_matmul(h, xq, xs, out)
+    want = _product(xq, xs, wq, torch.ones(N))
+    assert torch.all((out.double().cpu() - want).abs() <= 2.0 ** -24 * want.abs())
 
 
 def test_a_row_that_is_not_finite_is_recorded(handle):

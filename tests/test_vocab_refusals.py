@@ -39,7 +39,8 @@ def test_null_handles():
     L.fr_i8_destroy(None)
 
 
-@pytest.mark.parametrize("V,d,n", [(0, 8, 8), (8, 0, 8), (8, 8, 0), (-1, 8, 8), (8, 8, 1 << 30)])
+@pytest.mark.parametrize("V,d,n", [(0, 8, 8), (8, 0, 8), (8, 8, 0), (-1, 8, 8), (8, 8, 1 << 30), ((1 << 30) + 1, 8, 8),
+                                    (8, (1 << 24) + 1, 8)])
 def test_embed_init_sizes(V, d, n):
     out = P(7)
     assert fr.libfr().fr_embed_init(V, d, n, ctypes.byref(out)) == BAD
@@ -78,7 +79,8 @@ def test_i8_quantize_arguments():
     for x, ldx, dtype, rows, d, q, ldq, s in (
             (None, 8, 0, 1, 8, a, 8, a), (a, 8, 0, 1, 8, None, 8, a), (a, 8, 0, 1, 8, a, 8, None), (a, 7, 0, 1, 8, a, 8, a),
             (a, 8, 0, 1, 8, a, 7, a), (a, 8, 2, 1, 8, a, 8, a), (a, 8, 0, -1, 8, a, 8, a), (a, 8, 0, 1, 0, a, 8, a),
-            (P(258), 8, 0, 1, 8, a, 8, a), (P(257), 8, 1, 1, 8, a, 8, a), (a, 8, 0, 1, 8, a, 8, P(257))):
+            (P(258), 8, 0, 1, 8, a, 8, a), (P(257), 8, 1, 1, 8, a, 8, a), (a, 8, 0, 1, 8, a, 8, P(257)),
+            (a, 1 << 31, 0, 1, (1 << 30) + 1, a, 1 << 31, a)):
         assert L.fr_i8_quantize(x, ldx, dtype, rows, d, q, ldq, s, None) == BAD
     assert L.fr_i8_quantize(a, 8, 0, 0, 8, a, 8, a, None) == fr.FR_OK  # no rows: nothing to do
 

@@ -70,23 +70,25 @@ struct CeRows {
 
 __device__ __forceinline__ int32_t ce_m_tiles(int32_t n) { return max((n + GM_TILE - 1) / GM_TILE, 1); }
 
-// A CTA packs CE_GATHER_ROWS consecutive rows.  Each counts the counted rows
-// before its own and in all by reading every target, so no CTA waits for
-// another and the rows of padding are shared out.
+// A CTA packs `per` consecutive rows, CE_GATHER_ROWS at a time.  Each counts the
+// counted rows before its own and in all by reading every target, so no CTA waits
+// for another and the rows of padding are shared out; four CTAs per SM at most
+// keep those reads to a few KB for each row.
 constexpr int CE_GATHER_ROWS = 16;
 constexpr int CE_GATHER_THREADS = 256;
 constexpr int CE_GATHER_CTAS = 32;  // at least: they share the padding
 __global__ void __launch_bounds__(CE_GATHER_THREADS)
     k_ce_gather(const __nv_bfloat16* __restrict__ hidden, int64_t ldh, const int32_t* __restrict__ targets,
-                const float* __restrict__ lse, const float* __restrict__ grad_loss, int32_t rows, int32_t V, int32_t d,
-                CeRows out, float* __restrict__ loss_out, float* __restrict__ lse_out,
+                const float* __restrict__ lse, const float* __restrict__ grad_loss, int32_t rows, int32_t per, int32_t V,
+                int32_t d, CeRows out, float* __restrict__ loss_out, float* __restrict__ lse_out,
                 __nv_bfloat16* __restrict__ grad_hidden, int64_t ldgh, int32_t* __restrict__ counters, int32_t n_counters,
                 int32_t* __restrict__ err) {
     __shared__ int32_t before_s, total_s, pos_s[CE_GATHER_ROWS];
     __shared__ uint32_t gmax_s;
     griddep_wait();
     griddep_launch_dependents();
-    const int32_t r0 = blockIdx.x * CE_GATHER_ROWS, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int32_t first = blockIdx.x * per, last = min(first + per, rows);
+    const int32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) before_s = 0, total_s = 0, gmax_s = 0u;
     __syncthreads();
     int32_t before = 0, total = 0;
@@ -94,7 +96,7 @@ __global__ void __launch_bounds__(CE_GATHER_THREADS)
     for (int32_t i = tid; i < rows; i += CE_GATHER_THREADS) {
         const int32_t live = (uint32_t)targets[i] < (uint32_t)V;
         total += live;
-        before += i < r0 ? live : 0;
+        before += i < first ? live : 0;
     }
     before = __reduce_add_sync(0xffffffffu, before);
     total = __reduce_add_sync(0xffffffffu, total);
@@ -103,14 +105,18 @@ __global__ void __launch_bounds__(CE_GATHER_THREADS)
         atomicAdd(&total_s, total);
     }
     __syncthreads();
-    if (warp == 0) {
-        const int32_t r = r0 + lane;
-        const int32_t t = lane < CE_GATHER_ROWS && r < rows ? targets[r] : -1;
-        const bool live = (uint32_t)t < (uint32_t)V;
-        const uint32_t m = __ballot_sync(0xffffffffu, live);
-        const int32_t pos = before_s + __popc(m & ((1u << lane) - 1u));
-        if (lane < CE_GATHER_ROWS) {
-            pos_s[lane] = live ? pos : -1;
+    const int32_t vecs = d >> 3;  // rows start on 16 bytes (checked by the caller)
+    for (int32_t r0 = first; r0 < last; r0 += CE_GATHER_ROWS) {
+        if (warp == 0) {
+            const int32_t r = r0 + lane;
+            const bool mine = lane < CE_GATHER_ROWS && r < last;
+            const int32_t t = mine ? targets[r] : -1;
+            const bool live = (uint32_t)t < (uint32_t)V;
+            const uint32_t m = __ballot_sync(0xffffffffu, live);
+            const int32_t pos = before_s + __popc(m & ((1u << lane) - 1u));
+            __syncwarp();
+            if (lane == 0) before_s += __popc(m);
+            if (lane < CE_GATHER_ROWS) pos_s[lane] = live ? pos : -1;
             if (live) {
                 out.tgt[pos] = t;
                 out.idx[pos] = r;
@@ -118,7 +124,7 @@ __global__ void __launch_bounds__(CE_GATHER_THREADS)
                     out.lse[pos] = lse[r];
                     out.g[pos] = grad_loss[r];
                 }
-            } else if (r < rows) {
+            } else if (mine) {
                 const bool bad = t != -1;
                 if (bad) set_error(err, FR_ERR_CODE_RANGE);
                 if (loss_out) {
@@ -127,20 +133,20 @@ __global__ void __launch_bounds__(CE_GATHER_THREADS)
                 }
             }
         }
-    }
-    __syncthreads();
-    const int32_t vecs = d >> 3;  // rows start on 16 bytes (checked by the caller)
-    for (int k = warp; k < CE_GATHER_ROWS && r0 + k < rows; k += CE_GATHER_THREADS / 32) {
-        const int32_t r = r0 + k, pos = pos_s[k];
-        if (pos >= 0) {
-            const uint4* src = reinterpret_cast<const uint4*>(hidden + r * ldh);
-            uint4* dst = reinterpret_cast<uint4*>(out.h + pos * out.pitch);
+        __syncthreads();
+        for (int k = warp; k < CE_GATHER_ROWS && r0 + k < last; k += CE_GATHER_THREADS / 32) {
+            const int32_t r = r0 + k, pos = pos_s[k];
+            if (pos >= 0) {
+                const uint4* src = reinterpret_cast<const uint4*>(hidden + r * ldh);
+                uint4* dst = reinterpret_cast<uint4*>(out.h + pos * out.pitch);
 #pragma unroll 8
-            for (int32_t i = lane; i < vecs; i += 32) dst[i] = src[i];
-            for (int32_t j = (vecs << 3) + lane; j < d; j += 32) out.h[pos * out.pitch + j] = hidden[r * ldh + j];
-        } else if (grad_hidden) {
-            for (int32_t j = lane; j < d; j += 32) grad_hidden[r * ldgh + j] = __float2bfloat16_rn(0.f);
+                for (int32_t i = lane; i < vecs; i += 32) dst[i] = src[i];
+                for (int32_t j = (vecs << 3) + lane; j < d; j += 32) out.h[pos * out.pitch + j] = hidden[r * ldh + j];
+            } else if (grad_hidden) {
+                for (int32_t j = lane; j < d; j += 32) grad_hidden[r * ldgh + j] = __float2bfloat16_rn(0.f);
+            }
         }
+        __syncthreads();
     }
     // zero rows up to the next whole tile (the pitch is a multiple of 8 elements)
     const int32_t n = total_s, end = ce_m_tiles(n) * GM_TILE;
@@ -550,6 +556,11 @@ bool ce_on_device(const fr_ce* h) {
     return cudaGetDevice(&dev) == cudaSuccess && dev == h->device;
 }
 
+// Rows per CTA of k_ce_gather.
+int32_t ce_gather_rows(const fr_ce* h, int32_t rows) {
+    return (int32_t)fr::ce_round(std::max((rows + 4 * h->sms - 1) / (4 * h->sms), 1), fr::CE_GATHER_ROWS);
+}
+
 template <bool PAIR>
 fr_status ce_run_loss(fr_ce* h, const void* hidden_dev, int64_t ldh, const void* weight_dev, int64_t ldw,
                       const int32_t* targets_dev, int32_t rows, float* loss_dev, float* lse_dev, cudaStream_t s) {
@@ -564,10 +575,10 @@ fr_status ce_run_loss(fr_ce* h, const void* hidden_dev, int64_t ldh, const void*
     p.n_tiles = h->n_tiles;
     p.partial = h->partial;
     p.xt = h->xt;
-    const int32_t gather = std::max((rows + fr::CE_GATHER_ROWS - 1) / fr::CE_GATHER_ROWS, fr::CE_GATHER_CTAS);
-    FR_CUDA_TRY(fr::launch_pdl(fr::k_ce_gather, gather, fr::CE_GATHER_THREADS, 0, s, (const __nv_bfloat16*)hidden_dev, ldh,
-                               targets_dev, (const float*)nullptr, (const float*)nullptr, rows, h->V, h->d, h->rows,
-                               loss_dev, lse_dev, (__nv_bfloat16*)nullptr, (int64_t)0, (int32_t*)nullptr, 0, h->err));
+    const int32_t per = ce_gather_rows(h, rows);
+    FR_CUDA_TRY(fr::launch_pdl(fr::k_ce_gather, std::max((rows + per - 1) / per, fr::CE_GATHER_CTAS), fr::CE_GATHER_THREADS, 0, s,
+                               (const __nv_bfloat16*)hidden_dev, ldh, targets_dev, (const float*)nullptr,
+                               (const float*)nullptr, rows, per, h->V, h->d, h->rows, loss_dev, lse_dev, (__nv_bfloat16*)nullptr, (int64_t)0, (int32_t*)nullptr, 0, h->err));
     fr::GmCtl ctl{h->err, h->wait_ns, h->starve};
     FR_CUDA_TRY(fr::gm_launch(fr::k_ce_loss<fr::CeLoss<PAIR>>, fr::ce_round(rows, TM) / TM * h->n_tiles, h->sms, s, p, ctl));
     FR_CUDA_TRY(fr::launch_pdl(fr::k_ce_combine, ((int64_t)rows + 7) / 8, 256, 0, s, (const float2*)h->partial, 2 * h->n_tiles,
@@ -614,10 +625,10 @@ fr_status ce_run_grad(fr_ce* h, const void* hidden_dev, int64_t ldh, const void*
     if (p.dw && (reinterpret_cast<uintptr_t>(grad_weight_dev) & 15u) == 0 && (ldgw & 7) == 0)
         p.dw_staged = fr::gm_staged_columns(h->d, 2);
     if (p.dw_staged && !fr::gm_encode(&p.map_dw, 2, grad_weight_dev, h->V, h->d, ldgw * 2, 32)) return FR_ERR_CUDA;
-    const int32_t gather = std::max((rows + fr::CE_GATHER_ROWS - 1) / fr::CE_GATHER_ROWS, fr::CE_GATHER_CTAS);
-    FR_CUDA_TRY(fr::launch_pdl(fr::k_ce_gather, gather, fr::CE_GATHER_THREADS, 0, s, (const __nv_bfloat16*)hidden_dev, ldh,
-                               targets_dev, lse_dev, grad_loss_dev, rows, h->V, h->d, h->rows, (float*)nullptr,
-                               (float*)nullptr, gh, ldgh, h->counters, pieces + 1, h->err));
+    const int32_t per = ce_gather_rows(h, rows);
+    FR_CUDA_TRY(fr::launch_pdl(fr::k_ce_gather, std::max((rows + per - 1) / per, fr::CE_GATHER_CTAS), fr::CE_GATHER_THREADS, 0, s,
+                               (const __nv_bfloat16*)hidden_dev, ldh, targets_dev, lse_dev, grad_loss_dev, rows, per, h->V,
+                               h->d, h->rows, (float*)nullptr, (float*)nullptr, gh, ldgh, h->counters, pieces + 1, h->err));
     fr::GmCtl ctl{h->err, h->wait_ns, h->starve};
     for (int32_t k = 0; k <= pieces; ++k) {
         p.v0 = p.v1 = p.w0 = p.w1 = 0;

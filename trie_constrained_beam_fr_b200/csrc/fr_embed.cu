@@ -595,7 +595,7 @@ cudaError_t em_grad_any(fr_embed* h, const void* grad, int64_t ldg, const int32_
 extern "C" fr_status fr_embed_init(int32_t V, int32_t d, int32_t max_tokens, fr_embed** out) {
     if (!out) return FR_ERR_INVALID_ARG;
     *out = nullptr;
-    if (V < 1 || d < 1 || max_tokens < 1 || max_tokens >= (1 << 30)) return FR_ERR_INVALID_ARG;
+    if (V < 1 || V > (1 << 30) || d < 1 || d > (1 << 24) || max_tokens < 1 || max_tokens >= (1 << 30)) return FR_ERR_INVALID_ARG;
     fr_embed* h = new (std::nothrow) fr_embed();
     if (!h) return FR_ERR_OOM;
     h->V = V;

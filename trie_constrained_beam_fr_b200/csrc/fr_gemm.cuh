@@ -6,8 +6,10 @@
 // bytes of K wide) and holds 128 rows of the accumulator in its tensor memory.
 // The pair reads each operand value once where two single CTAs with 128 x 256
 // tiles would read B twice: 32 KB instead of 48 KB per stage and CTA, which is
-// what bounds the 8-bit products (L2 to shared memory).
-// In each CTA warp 0 lane 0 copies its half of the stage into a ring with TMA
+// what bounds the 8-bit products (L2 to shared memory).  Calls of at most 128 rows
+// use single CTAs with tiles of 128 x 256 instead: half of a pair's rows would be
+// empty.
+// In each CTA warp 0 lane 0 copies its part of the stage into a ring with TMA
 // (arrivals on the first CTA's barrier); in the first CTA warp 1 lane 0 issues
 // the stage's four tcgen05.mma into one of two tensor-memory accumulators;
 // warps 4..11 (a tensor-memory lane quarter and half of the columns each, one

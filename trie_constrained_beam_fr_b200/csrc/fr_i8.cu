@@ -578,7 +578,7 @@ bool i8_bad_x(const fr_i8* h, const int8_t* xq, int64_t ldx, const float* xs, in
 
 extern "C" fr_status fr_i8_quantize(const void* x_dev, int64_t ldx, fr_dtype dtype, int32_t rows, int32_t d,
                                     int8_t* q_dev, int64_t ldq, float* scale_dev, fr_stream stream) {
-    if (!x_dev || !q_dev || !scale_dev || rows < 0 || d < 1 || ldx < d || ldq < d ||
+    if (!x_dev || !q_dev || !scale_dev || rows < 0 || d < 1 || d > (1 << 30) || ldx < d || ldq < d ||
         (dtype != FR_F32 && dtype != FR_BF16) ||
         (reinterpret_cast<uintptr_t>(x_dev) & (dtype == FR_F32 ? 3u : 1u)) ||
         (reinterpret_cast<uintptr_t>(scale_dev) & 3u))

@@ -666,7 +666,7 @@ def fr_i8_lse(i8, xq: torch.Tensor, xscale: torch.Tensor, lse: torch.Tensor, sli
     if slice_ is None:
         if i8.sid_span:
             raise ValueError("the handle has a SID range: slice is needed")
-    elif _matrix(slice_, "slice", (torch.float32,), rows, i8.sid_span) != i8.sid_span and rows > 1:
+    elif _matrix(slice_, "slice", (torch.float32,), rows, i8.sid_span) != i8.sid_span and rows > 1 and i8.sid_span > 0:
         raise ValueError("slice must be contiguous")
     _check(libfr().fr_i8_lse(i8, _ptr(xq), ldx, _ptr(xscale), rows, _ptr(lse), _ptr(slice_), _stream(stream)), "fr_i8_lse")
 
