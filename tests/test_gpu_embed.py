@@ -132,6 +132,27 @@ def test_grad(handle, kind, n, V, d, tg, tt, add, pad, offset):
     assert torch.equal(table, first)
 
 
+@pytest.mark.parametrize("runs", [
+    (1024, 1024, 1, 1023, 1025, 2048), (1000, 24, 1024, 1025, 31, 33, 960, 3000), (32, 992, 32, 32, 1000, 1), (1040, 1000, 40, 2000, 16, 40, 8),
+    (33000, 500, 33300, 7),
+])
+@pytest.mark.parametrize("d", [8, 70, 520])
+def test_grad_of_runs_at_the_joins_borders(handle, runs, d):
+    """Tokens repeated so often that their sums are put together from many
+    pieces, beginning and ending on, before and behind the pieces' borders."""
+    g = torch.Generator().manual_seed(sum(runs) + d)
+    n, V = sum(runs), len(runs) + 2
+    tok = torch.repeat_interleave(torch.arange(len(runs)), torch.tensor(runs))[torch.randperm(n, generator=g)].int().cuda()
+    grad, table = torch.randn(n, d, generator=g).to(BF16).cuda(), torch.full((V, d), 3.0, device="cuda")
+    h = handle(V, d, n)
+    fr.fr_embed_grad(h, grad, tok, table)
+    want, bound = _grad_reference(grad, tok, V, 1.0, None)
+    assert torch.all((table.double().cpu() - want).abs() <= bound + _half_step(F32) * (want.abs() + bound))
+    first = table.clone()
+    fr.fr_embed_grad(h, grad, tok, table)
+    assert torch.equal(table, first)
+
+
 def test_grad_is_the_lookups_gradient(handle):
     """sum(grad * lookup(T + e E)) differs from sum(grad * lookup(T)) by
     e * sum(dT * E): the lookup is linear, so the difference is exact up to

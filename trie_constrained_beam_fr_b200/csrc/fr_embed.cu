@@ -14,8 +14,9 @@
 //   k_em_sum      the sorted positions in chunks of EM_CHUNK: a CTA adds a
 //                 chunk's rows, a column group per thread, and writes the
 //                 finished tokens; a token that reaches over a chunk's edge
-//                 leaves fp32 partials, which the last of its chunks adds in
-//                 order.  More CTAs zero the rows that no token fell on.
+//                 leaves fp32 partials, which the last chunk to arrive adds in
+//                 order, in two levels.  More CTAs zero the rows that no token
+//                 fell on.
 //
 // The sort is stable and the partials are joined in order, so a sum's order
 // depends on the tokens alone: no floating-point atomics.
@@ -40,6 +41,7 @@ constexpr int EM_TILE = 1024;       // tokens that a sorting CTA ranks at a time
 constexpr int EM_BITS = 9;          // most digit bits of a sort pass
 constexpr int EM_SORT_CTAS = 128;   // most CTAs of a sort pass
 constexpr int EM_CHUNK = 32;        // sorted positions per CTA of the sum
+constexpr int EM_JOIN = 32;         // chunks of a long run that are added together first
 template <int VEC>
 constexpr int EM_UNROLL = VEC == 8 ? 4 : 16;  // rows in flight per thread of the sum
 constexpr int EM_ZERO_ROWS = 128;   // table rows per CTA that zeros
@@ -315,10 +317,16 @@ __device__ __forceinline__ int32_t em_lower_bound(const uint32_t* __restrict__ k
 
 // Chunk c holds the sorted positions [c * EM_CHUNK, ...).  Its partials:
 // part[2c] the run that began in an earlier chunk, part[2c + 1] the run that
-// begins here and goes on.  The last of a run's chunks to arrive adds its
-// partials in chunk order, so the sum does not depend on which that is.  The
-// CTAs behind the chunks' zero the rows that no token fell on, beside the
-// sums' reads.  Grid: chunks x column blocks, then the zeroing CTAs.
+// begins here and goes on.  The chunks of a run are taken in groups of EM_JOIN
+// (by chunk number).  The last of a group to arrive adds its partials in chunk
+// order; the last group to arrive adds the groups' sums, so the order does not
+// depend on who is last, and a token that fills the batch (padding that was not
+// marked) does not leave one CTA to add all of it (65,536 equal tokens of 2,048
+// bf16 values: 225 us, 544 in one level).  The CTAs behind the chunks' zero the
+// rows that no token fell on, beside the sums' reads.  A CTA has as many threads
+// as the columns need: latency bounds short rows (524,288 tokens of 64 values:
+// 149 us, 665 with 256 threads and a search for each run's ends).  Grid: chunks
+// x column blocks, then the zeroing CTAs.
 template <class TG, class TT, int VEC>
 __global__ void __launch_bounds__(EM_THREADS)
     k_em_sum(const TG* __restrict__ grad, int64_t ldg, int32_t d, const uint32_t* __restrict__ keys,
@@ -332,18 +340,34 @@ __global__ void __launch_bounds__(EM_THREADS)
     griddep_launch_dependents();
     if (blockIdx.x >= (uint32_t)chunks * blocks) {
         const int32_t v0 = (blockIdx.x - chunks * blocks) * EM_ZERO_ROWS, v1 = min(v0 + EM_ZERO_ROWS, V);
-        for (int k = threadIdx.x; k < EM_ZERO_ROWS; k += EM_THREADS) touched[k] = 0;
+        for (int k = threadIdx.x; k < EM_ZERO_ROWS; k += blockDim.x) touched[k] = 0;
         __syncthreads();
-        const int32_t end = em_lower_bound(keys, n, (uint32_t)v1);
-        for (int32_t i = em_lower_bound(keys, n, (uint32_t)v0) + threadIdx.x; i < end; i += EM_THREADS) touched[keys[i] - v0] = 1;
+        const int32_t begin = em_lower_bound(keys, n, (uint32_t)v0), end = em_lower_bound(keys, n, (uint32_t)v1);
+        if (end - begin <= 16 * (int32_t)blockDim.x) {
+            for (int32_t i = begin + threadIdx.x; i < end; i += blockDim.x) touched[keys[i] - v0] = 1;
+        } else {
+            // many tokens on few rows: a search for each row (65,536 equal tokens of 256
+            // values: 50 us, 399 by reading all of them)
+            for (int32_t v = v0 + threadIdx.x; v < v1; v += blockDim.x) {
+                int32_t lo = begin, hi = end;
+                while (lo < hi) {
+                    const int32_t mid = lo + (hi - lo) / 2;
+                    if (keys[mid] < (uint32_t)v)
+                        lo = mid + 1;
+                    else
+                        hi = mid;
+                }
+                touched[v - v0] = lo < end && keys[lo] == (uint32_t)v;
+            }
+        }
         __syncthreads();
         em_zero_rows<TT, VEC>(table, ldt, d, v0, v1, touched);
         return;
     }
     const int32_t chunk = blockIdx.x / blocks, block = blockIdx.x - chunk * blocks;
     const int64_t i0 = (int64_t)chunk * EM_CHUNK;
-    const int32_t j = (block * EM_THREADS + threadIdx.x) * VEC;  // this thread's columns
-    for (int k = threadIdx.x; k < EM_CHUNK + 2; k += EM_THREADS) {
+    const int32_t j = (block * (int32_t)blockDim.x + threadIdx.x) * VEC;  // this thread's columns
+    for (int k = threadIdx.x; k < EM_CHUNK + 2; k += blockDim.x) {
         const int64_t i = i0 + k - 1;
         key_s[k] = i >= 0 && i < n ? keys[i] : 0xFFFFFFFFu;
         if (k >= 1 && k <= EM_CHUNK) ord_s[k - 1] = i < n ? order[i] : 0;
@@ -353,6 +377,11 @@ __global__ void __launch_bounds__(EM_THREADS)
     while (m > 0 && key_s[m] >= (uint32_t)V) --m;  // tokens that do not count are sorted last
     if (m == 0) return;
     const bool head = key_s[0] == key_s[1], tail = key_s[m + 1] == key_s[m];
+    // how far the first key's run reaches back and the last key's goes on: a warp's
+    // probes, or a search where those are not enough
+    const int64_t back = i0 - 1 - (threadIdx.x & 31), on = i0 + m + (threadIdx.x & 31);
+    const uint32_t not_back = __ballot_sync(0xffffffffu, !(head && back >= 0 && keys[back] == key_s[1]));
+    const uint32_t not_on = __ballot_sync(0xffffffffu, !(tail && on < n && keys[on] == key_s[m]));
     if (j < d) {
         float sum[VEC];
 #pragma unroll
@@ -387,28 +416,55 @@ __global__ void __launch_bounds__(EM_THREADS)
     // the runs that reach over this chunk's edges: the first key's and, unless
     // it is the same run, the last key's
     const bool one = head && tail && key_s[1] == key_s[m];
+    // whether this CTA is the last of 1 + others to come here
+    const auto last = [&](int32_t* counter, int64_t others) -> bool {
+        if (others == 0) return true;
+        __threadfence();
+        __syncthreads();
+        if (threadIdx.x == 0) last_s = atomicAdd(counter, 1) == (int32_t)others;
+        __syncthreads();
+        if (!last_s) return false;
+        __threadfence();
+        return true;
+    };
     for (int r = 0; r < 2; ++r) {
         if (!(r == 0 ? head : tail && !one)) continue;
         const uint32_t key = r == 0 ? key_s[1] : key_s[m];
-        const int64_t c = em_lower_bound(keys, n, key) / EM_CHUNK, e = (em_lower_bound(keys, n, key + 1) - 1) / EM_CHUNK;
-        __threadfence();
-        __syncthreads();
-        if (threadIdx.x == 0) last_s = atomicAdd(&arrived[c * blocks + block], 1) == (int32_t)(e - c);
-        __syncthreads();
-        if (!last_s) continue;
-        __threadfence();
+        int64_t c = chunk, e = chunk;  // the run's chunks
+        if (r == 0) c = (not_back ? i0 - (__ffs(not_back) - 1) : em_lower_bound(keys, n, key)) / EM_CHUNK;
+        if (r == 1 || one) e = ((not_on ? i0 + m + (__ffs(not_on) - 1) : em_lower_bound(keys, n, key + 1)) - 1) / EM_CHUNK;
+        const auto partial = [&](int64_t k) { return part + (2 * k + (k == c ? 1 : 0)) * pitch + j; };
+        // the run's chunks of this group.  A group's counter is its first chunk's: where
+        // another run begins there too, this one has no other chunk in the group.
+        const int64_t k0 = max(c, (int64_t)chunk / EM_JOIN * EM_JOIN), k1 = min(e, (int64_t)chunk / EM_JOIN * EM_JOIN + EM_JOIN - 1);
+        if (!last(arrived + k0 * blocks + block, k1 - k0)) continue;
+        float sum[VEC];
         if (j < d) {
-            float sum[VEC];
-            em_load_cg<VEC>(part + (2 * c + 1) * pitch + j, sum);
+            em_load_cg<VEC>(partial(k0), sum);
 #pragma unroll 8
-            for (int64_t k = c + 1; k <= e; ++k) {
+            for (int64_t k = k0 + 1; k <= k1; ++k) {
                 float v[VEC];
                 em_load_cg<VEC>(part + 2 * k * pitch + j, v);
 #pragma unroll
                 for (int q = 0; q < VEC; ++q) sum[q] += v[q];
             }
-            em_write<TT, VEC>(table + (int64_t)key * ldt + j, sum, scale, accumulate != 0);
         }
+        const int64_t g0 = c / EM_JOIN, g1 = e / EM_JOIN;
+        if (g0 != g1) {
+            if (j < d) em_store<VEC>(partial(k0), sum);
+            if (!last(arrived + ((int64_t)chunks + c) * blocks + block, g1 - g0)) continue;
+            if (j < d) {
+                em_load_cg<VEC>(partial(c), sum);
+#pragma unroll 8
+                for (int64_t g = g0 + 1; g <= g1; ++g) {
+                    float v[VEC];
+                    em_load_cg<VEC>(part + 2 * g * EM_JOIN * pitch + j, v);
+#pragma unroll
+                    for (int q = 0; q < VEC; ++q) sum[q] += v[q];
+                }
+            }
+        }
+        if (j < d) em_write<TT, VEC>(table + (int64_t)key * ldt + j, sum, scale, accumulate != 0);
     }
 }
 
@@ -499,7 +555,7 @@ struct fr_embed {
     int32_t* pos[2] = {};
     int32_t* counts = nullptr;
     float* part = nullptr;       // [2 * chunks, pitch]
-    int32_t* arrived = nullptr;  // [chunks, column blocks] chunks of a run that have arrived, at its first chunk
+    int32_t* arrived = nullptr;  // [2, chunks, column blocks] chunks of a group, groups of a run that have arrived
     int64_t pitch = 0;
     int32_t* err = nullptr;
     cudaStream_t last_stream = nullptr;
@@ -552,7 +608,7 @@ cudaError_t em_sort(fr_embed* h, const int32_t* tokens, int32_t n, const uint32_
         const uint32_t* kin = p ? h->keys[(p - 1) & 1] : nullptr;
         const int32_t* pin = p ? h->pos[(p - 1) & 1] : nullptr;
         cudaError_t e = fr::launch_pdl(fr::k_em_hist, ctas, fr::EM_THREADS, 0, s, tokens, kin, n, per, h->V, p * bits, bits,
-                                       h->counts, h->err, h->arrived, p ? 0 : em_ceil(n, fr::EM_CHUNK) * em_ceil(h->d, fr::EM_THREADS));
+                                       h->counts, h->err, h->arrived, p ? 0 : 2 * em_ceil(n, fr::EM_CHUNK) * em_ceil(h->d, fr::EM_THREADS));
         if (e != cudaSuccess) return e;
         e = fr::launch_pdl(fr::k_em_scatter, ctas, fr::EM_THREADS, 0, s, tokens, kin, pin, n, per, h->V, p * bits, bits,
                            (const int32_t*)h->counts, h->keys[p & 1], h->pos[p & 1], h->err);
@@ -577,8 +633,9 @@ cudaError_t em_grad(fr_embed* h, const void* grad, int64_t ldg, const int32_t* t
     const int32_t* order;
     cudaError_t e = em_sort(h, tokens, n, &keys, &order, s);
     if (e != cudaSuccess) return e;
-    const int64_t chunks = em_ceil(n, fr::EM_CHUNK), wide = em_ceil(h->d, fr::EM_THREADS * VEC);
-    return fr::launch_pdl(fr::k_em_sum<TG, TT, VEC>, chunks * wide + zeros, fr::EM_THREADS, 0, s, (const TG*)grad, ldg, h->d, keys,
+    const int32_t threads = (int32_t)std::min<int64_t>(em_ceil(em_ceil(h->d, VEC), 32) * 32, fr::EM_THREADS);
+    const int64_t chunks = em_ceil(n, fr::EM_CHUNK), wide = em_ceil(h->d, threads * VEC);
+    return fr::launch_pdl(fr::k_em_sum<TG, TT, VEC>, chunks * wide + zeros, threads, 0, s, (const TG*)grad, ldg, h->d, keys,
                           order, n, h->V, scale, (TT*)table, ldt, accumulate, h->part, h->pitch, h->arrived, (int32_t)chunks, (int32_t)wide);
 }
 
@@ -609,7 +666,7 @@ extern "C" fr_status fr_embed_init(int32_t V, int32_t d, int32_t max_tokens, fr_
     }
     const int64_t n = max_tokens;
     cudaError_t e = cudaMalloc(&h->keys[0], n * 16);
-    if (e == cudaSuccess) e = cudaMalloc(&h->counts, ((size_t)(fr::EM_SORT_CTAS << fr::EM_BITS) + em_ceil(n, fr::EM_CHUNK) * em_ceil(d, fr::EM_THREADS)) * sizeof(int32_t));
+    if (e == cudaSuccess) e = cudaMalloc(&h->counts, ((size_t)(fr::EM_SORT_CTAS << fr::EM_BITS) + 2 * em_ceil(n, fr::EM_CHUNK) * em_ceil(d, fr::EM_THREADS)) * sizeof(int32_t));
     if (e == cudaSuccess) e = cudaMalloc(&h->part, (size_t)em_ceil(n, fr::EM_CHUNK) * 2 * h->pitch * 4);
     if (e == cudaSuccess) e = cudaMalloc(&h->err, sizeof(int32_t));
     if (e == cudaSuccess) e = cudaMemset(h->err, 0, sizeof(int32_t));
