@@ -118,6 +118,10 @@ def _grad(ce, h, w, t, lse, gl, pad=0, offset=0):
     (64, 20000, 137, 0.1, 2.0, 0, 0),    # three pieces, an odd hidden size, few rows
     (700, 3000, 520, 0.1, 30.0, 0, 0),   # peaked rows: probabilities near 0 and 1
     (260, 16400, 264, 0.9, 2.0, 5, 0),   # most rows do not count; last piece of 16 tokens
+    (13, 41365, 39, 0.0, 2.0, 0, 0),     # few rows, many tokens: narrow tiles, dh in many splits
+    (100, 30000, 75, 0.4, 2.0, 2, 1),
+    (600, 700, 300, 0.2, 2.0, 1, 1),
+    (20000, 50, 16, 0.3, 2.0, 0, 0),     # many rows, few tokens
 ])
 def test_loss_and_gradients(handle, rows, V, d, ignored, gain, pad, offset):
     h, w, t, gl = _inputs(rows, V, d, rows + V + d, gain, ignored, extra=8 if pad else 0)

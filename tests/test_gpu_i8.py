@@ -142,7 +142,8 @@ def test_the_largest_sums(handle, value):
 
 
 @pytest.mark.parametrize("rows,N,d,base,span", [(1, 64, 32, 0, 64), (3, 300, 64, 100, 37), (40, 1000, 520, 990, 10), (130, 700, 256, 200, 0),
-                                                (300, 5000, 96, 0, 768), (300, 1500, 200, 77, 1301), (33, 2000, 257, 129, 640)])
+                                                (300, 5000, 96, 0, 768), (300, 1500, 200, 77, 1301), (33, 2000, 257, 129, 640),
+                                                (20, 40000, 64, 39000, 1000), (300, 16500, 40, 1, 90)])
 def test_lse(handle, rows, N, d, base, span):
     g = torch.Generator().manual_seed(rows + N)
     xq, wq = _ints(g, rows, d), _ints(g, N, d)

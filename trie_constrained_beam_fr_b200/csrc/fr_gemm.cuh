@@ -31,7 +31,7 @@
 //     __device__ bool tile(const State&, uint32_t g, Tile&) const;  // tile g (< 2^31) of the launch; false behind the last
 //     __device__ int32_t* counter() const;           // DYNAMIC: zero before the launch; tiles fit an int32
 //     __device__ void load(const Tile&, int kb, int rank, uint8_t* a, uint8_t* b, uint32_t bar) const;
-//     __device__ uint32_t stage_bytes() const;       // that load() copies per CTA
+//     __device__ uint32_t stage_bytes(const Tile&) const;       // that load() copies into the pair's CTAs (or the one)
 //     __device__ bool a_mn(const Tile&) const, b_mn(const Tile&) const;  // operand stored MN-major
 //     // the first or second half of one row's columns; gives the accumulator back
 //     // as soon as it has been read
@@ -413,7 +413,7 @@ __device__ __forceinline__ void gm_run(const P& p, const GmCtl& ctl) {
                         break;
                     }
                     // the first CTA's barrier counts both CTAs' bytes
-                    if (rank == 0) tc_arrive_expect_tx(&sm->full[s], (PAIR ? 2 : 1) * p.stage_bytes());
+                    if (rank == 0) tc_arrive_expect_tx(&sm->full[s], p.stage_bytes(t));
                     p.load(t, kb, (int)rank, ringA + s * GM_OP_BYTES, ringB + s * B_BYTES, PAIR ? gm_in_first(&sm->full[s]) : smem_u32(&sm->full[s]));
                 }
             }
@@ -617,6 +617,19 @@ __device__ __forceinline__ void gm_write_plain(const GmStage& sg, int lane, T* d
     }
 }
 
+// Tile width (columns): the rounds that `units` pairs or CTAs need times a tile's
+// cost, its columns and about 64 columns' worth of start and end.  Fewer columns
+// than 256 where that leaves units without a tile, or its last round short.
+inline int32_t gm_width(int64_t m_tiles, int64_t columns, int64_t units, int32_t step, int32_t least = 64) {
+    int32_t best = GM_TILE;
+    int64_t cost = INT64_MAX;
+    for (int32_t bn = GM_TILE; bn >= least; bn -= step) {
+        const int64_t tiles = m_tiles * ((columns + bn - 1) / bn), c = (tiles + units - 1) / units * (bn + 64);
+        if (c < cost) cost = c, best = bn;
+    }
+    return best;
+}
+
 // Sends 64 bf16 columns of the warp's 32 rows to (x, y) of `map`.
 __device__ __forceinline__ void gm_stage64(const GmStage& sg, const CUtensorMap* map, int lane, const float (&v)[64], int x, int y) {
     gm_put(sg, lane, v);
@@ -629,6 +642,12 @@ __device__ __forceinline__ void gm_stage32(const GmStage& sg, const CUtensorMap*
     gm_put(sg, lane, v);
     sg.send<ADD>(map, lane, x, y);
 }
+
+// Rows of a single CTA's A copies when there are `rows` of them.  The products'
+// other rows are whatever the stage held and reach nothing.  Copies of 128 rows would
+// have most of them filled in, which takes longer than copying (4 rows x 129,820
+// tokens x 1,212 values: 77 us for the loss, 63 without).
+inline int32_t gm_a_rows(int32_t rows) { return std::min((rows + 7) / 8 * 8, GM_HALF); }
 
 // 2-D row-major tensor map: `rows` x `cols` elements of `esize` bytes (1: 8-bit
 // integers, 2: bf16, 4: fp32), row pitch `pitch` bytes, box box_rows x 128

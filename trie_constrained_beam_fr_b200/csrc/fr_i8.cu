@@ -264,6 +264,8 @@ __global__ void __launch_bounds__(FEW_THREADS) k_i8_few(const int8_t* __restrict
     }
 }
 
+constexpr int64_t I8_PARTIALS_MORE = 1 << 16;  // for narrow tiles of small calls
+
 // Tile walk shared by the two products.
 template <bool PAIR_>
 struct I8Base {
@@ -271,7 +273,7 @@ struct I8Base {
     static constexpr int TM = PAIR ? GM_TILE : GM_HALF;  // rows of a tile
     __device__ __forceinline__ int32_t* counter() const { return nullptr; }
     struct Tile {
-        int nk, m0, n0;
+        int nk, m0, n, n0;
         uint32_t idesc;
     };
     struct State {};
@@ -281,7 +283,8 @@ struct I8Base {
         gm_prefetch(&map_w);
     }
     int32_t rows, N, k_blocks, m_tiles, n_tiles;
-    int32_t bn;  // columns of a tile: 256, or fewer where that leaves SMs without one
+    int32_t bn;  // columns of a tile
+    int32_t a_rows;  // rows of a copy of x
     const float* xs;
     const float* ws;
     int32_t ws_vec;  // ws starts on 16 bytes
@@ -293,12 +296,13 @@ struct I8Base {
         int32_t m, n;
         gm_grouped(g, m_tiles, n_tiles, m, n);
         t.m0 = m * TM;
+        t.n = n;
         t.n0 = n * bn;
         t.nk = k_blocks;
         t.idesc = gm_idesc(true, PAIR, false, false, bn);
         return true;
     }
-    __device__ __forceinline__ uint32_t stage_bytes() const { return GM_OP_BYTES + (PAIR ? bn / 2 : bn) * GM_KB_BYTES; }
+    __device__ __forceinline__ uint32_t stage_bytes(const Tile&) const { return ((PAIR ? 2 : 1) * a_rows + bn) * GM_KB_BYTES; }
     __device__ __forceinline__ bool a_mn(const Tile&) const { return false; }
     __device__ __forceinline__ bool b_mn(const Tile&) const { return false; }
     __device__ __forceinline__ void load(const Tile& t, int kb, int rank, uint8_t* a, uint8_t* b, uint32_t bar) const {
@@ -360,13 +364,14 @@ struct I8Out : I8Base<PAIR_> {
     __device__ __forceinline__ void epilogue(const State&, const Tile& t, uint32_t taddr, int r, int half, const GmStage& sg,
                                              GmRelease<PAIR_>& release) const {
         constexpr int CW = 128 / sizeof(T);  // columns per staged store
-        const int row = t.m0 + r, lane = threadIdx.x & 31, row0 = row - lane, cols = max(bn / 2, 64);
+        const int row = t.m0 + r, lane = threadIdx.x & 31, row0 = row - lane;
+        const int cols = (bn / 2 + CW - 1) / CW * CW, c1 = min((half + 1) * cols, bn);
+        if (row0 >= rows) return;
         const float xscale = row < rows ? xs[row] : 0.f;
 #pragma unroll 1
-        for (int c = half * cols; c < min((half + 1) * cols, bn) && t.n0 + c < N; c += CW) {
+        for (int c = half * cols; c < c1 && t.n0 + c < N; c += CW) {
             float v[CW];
-            scaled(taddr + (uint32_t)c, t.n0 + c, xscale, v, c + CW == min((half + 1) * cols, bn), release);
-            if (row0 >= rows) continue;
+            scaled(taddr + (uint32_t)c, t.n0 + c, xscale, v, c + CW == c1, release);
             gm_put(sg, lane, v);
             if (t.n0 + c < staged)
                 sg.send<false>(&map_out, lane, t.n0 + c, row0);
@@ -381,31 +386,33 @@ struct I8Lse : I8Base<PAIR_> {
     using Base = I8Base<PAIR_>;
     using typename Base::State;
     using typename Base::Tile;
+    using Base::bn;
     using Base::N;
     using Base::rows;
     using Base::xs;
     using Base::scaled;
     static constexpr bool STAGED = true;
     static constexpr int STAGES = PAIR_ ? 6 : 4;
-    float2* partial;  // [rows, n_parts] (max, scaled sum) of 128 columns each
+    float2* partial;  // [rows, n_parts] (max, scaled sum) of half a tile's columns each
     int32_t n_parts;
     float* slice;     // [rows, sid_span]
     int32_t sid_base, sid_span;
     __device__ __forceinline__ void epilogue(const State&, const Tile& t, uint32_t taddr, int r, int half, const GmStage& sg,
                                              GmRelease<PAIR_>& release) const {
-        const int c0 = half * GM_EPI_COLS;
+        const int cols = (bn / 2 + 31) & ~31, c1 = min((half + 1) * cols, bn);
         const int row = t.m0 + r, lane = threadIdx.x & 31, row0 = row - lane;
+        if (row0 >= rows) return;
         const float xscale = row < rows ? xs[row] : 0.f;
         float m = -INFINITY, s = 0.f;
 #pragma unroll 1
-        for (int c = c0; c < c0 + GM_EPI_COLS && t.n0 + c < N; c += 32) {
+        for (int c = half * cols; c < c1 && t.n0 + c < N; c += 32) {
             const int n = t.n0 + c;
             float v[32];
-            scaled(taddr + (uint32_t)c, n, xscale, v, c + 32 == c0 + GM_EPI_COLS, release);
+            scaled(taddr + (uint32_t)c, n, xscale, v, c + 32 == c1, release);
             // the slice's columns of this chunk, a row at a time (a lane's stores to
             // its own row took 267 us instead of 117 on 5,555 rows x 4,757 slice columns)
             const int lo = max(n, sid_base), hi = min(n + 32, sid_base + sid_span);
-            if (lo < hi && row0 < rows) {
+            if (lo < hi) {
                 gm_put(sg, lane, v);
                 gm_write_plain(sg, lane, slice + (int64_t)row0 * sid_span - sid_base + n, sid_span, min(32, rows - row0), hi - n,
                                lo - n);
@@ -417,7 +424,7 @@ struct I8Lse : I8Base<PAIR_> {
             }
             gm_lse_fold(v, m, s);
         }
-        if (row < rows) partial[(int64_t)row * n_parts + (t.n0 + c0) / GM_EPI_COLS] = make_float2(m, s);
+        if (row < rows) partial[(int64_t)row * n_parts + 2 * t.n + half] = make_float2(m, s);
     }
 };
 
@@ -446,9 +453,9 @@ struct fr_i8 {
     const int8_t* wq = nullptr;
     const float* ws = nullptr;
     int64_t ldw = 0;
-    int32_t N = 0, d = 0, max_rows = 0, sid_base = 0, sid_span = 0, n_tiles = 0, sms = 0, device = 0;
-    CUtensorMap map_w[3];  // boxes of 128, 64 and 32 rows: tiles of 256, 128 and 64 columns
-    float2* partial = nullptr;  // [max_rows, 2 * n_tiles]
+    int32_t N = 0, d = 0, max_rows = 0, sid_base = 0, sid_span = 0, sms = 0, device = 0;
+    float2* partial = nullptr;  // partials values: at least [max_rows, 2 * (tiles of 256 columns)]
+    int64_t partials = 0;
     int32_t* err = nullptr;
     cudaStream_t last_stream = nullptr;
     uint64_t wait_ns = FR_WAIT_LIMIT_NS;
@@ -463,31 +470,30 @@ bool i8_on_device(const fr_i8* h) {
 }
 
 template <bool PAIR>
-fr_status i8_base(fr_i8* h, const int8_t* xq, int64_t ldx, const float* xs, int32_t rows, bool any_width,
-                  fr::I8Base<PAIR>* b) {
-    if (!fr::gm_encode(&b->map_x, 1, xq, rows, h->d, ldx, fr::GM_HALF)) return FR_ERR_CUDA;
-    // Tile width: the rounds that the pairs (or CTAs) need times a tile's cost (its
-    // columns, and about 64 columns' worth of start and end).
+fr_status i8_base(fr_i8* h, const int8_t* xq, int64_t ldx, const float* xs, int32_t rows, int32_t bn, fr::I8Base<PAIR>* b) {
     constexpr int TM = fr::I8Base<PAIR>::TM;
-    const int64_t units = PAIR ? h->sms / 2 : h->sms, m_tiles = (rows + TM - 1) / TM;
-    int best = 0;
-    int64_t cost = INT64_MAX;
-    for (int k = 0; k < (any_width ? 3 : 1); ++k) {
-        const int64_t bn = fr::GM_TILE >> k, tiles = m_tiles * ((h->N + bn - 1) / bn), c = (tiles + units - 1) / units * (bn + 64);
-        if (c < cost) cost = c, best = k;
-    }
-    b->bn = fr::GM_TILE >> best;
-    b->map_w = h->map_w[best];
+    b->a_rows = PAIR ? fr::GM_HALF : fr::gm_a_rows(rows);
+    if (!fr::gm_encode(&b->map_x, 1, xq, rows, h->d, ldx, b->a_rows) ||
+        !fr::gm_encode(&b->map_w, 1, h->wq, h->N, h->d, h->ldw, bn / 2))
+        return FR_ERR_CUDA;
+    b->bn = bn;
     b->rows = rows;
     b->N = h->N;
     b->k_blocks = (h->d + fr::GM_KB_BYTES - 1) / fr::GM_KB_BYTES;
-    b->m_tiles = (int32_t)m_tiles;
-    b->n_tiles = (h->N + b->bn - 1) / b->bn;
+    b->m_tiles = (rows + TM - 1) / TM;
+    b->n_tiles = (h->N + bn - 1) / bn;
     b->xs = xs;
     b->ws = h->ws;
     b->small = h->d <= 256;  // 128 * 128 * 256 = 2^22
     b->ws_vec = (reinterpret_cast<uintptr_t>(h->ws) & 15u) == 0;
     return FR_OK;
+}
+
+// Tile width of a call.
+template <bool PAIR>
+int32_t i8_width(const fr_i8* h, int32_t rows, int32_t step) {
+    constexpr int TM = fr::I8Base<PAIR>::TM;
+    return fr::gm_width((rows + TM - 1) / TM, h->N, PAIR ? h->sms / 2 : h->sms, step);
 }
 
 template <class P>
@@ -501,7 +507,8 @@ template <class T, bool PAIR>
 fr_status i8_tiles(fr_i8* h, const int8_t* xq, int64_t ldx, const float* xs, int32_t rows, void* out, int64_t ldo,
                    cudaStream_t s) {
     fr::I8Out<T, PAIR> p{};
-    const fr_status st = i8_base<PAIR>(h, xq, ldx, xs, rows, true, &p);
+    // (whole staged stores)
+    const fr_status st = i8_base<PAIR>(h, xq, ldx, xs, rows, i8_width<PAIR>(h, rows, 128 / sizeof(T)), &p);
     if (st != FR_OK) return st;
     p.out = (T*)out;
     p.ldo = ldo;
@@ -531,16 +538,23 @@ fr_status i8_out(fr_i8* h, const int8_t* xq, int64_t ldx, const float* xs, int32
 }
 
 template <bool PAIR>
-fr_status i8_rows_lse(fr_i8* h, const int8_t* xq, int64_t ldx, const float* xs, int32_t rows, float* slice, cudaStream_t s) {
+fr_status i8_rows_lse(fr_i8* h, const int8_t* xq, int64_t ldx, const float* xs, int32_t rows, float* lse, float* slice,
+                      cudaStream_t s) {
     fr::I8Lse<PAIR> p{};
-    const fr_status st = i8_base<PAIR>(h, xq, ldx, xs, rows, false, &p);
+    int32_t bn = i8_width<PAIR>(h, rows, 32);
+    if ((int64_t)rows * 2 * ((h->N + bn - 1) / bn) > h->partials) bn = fr::GM_TILE;
+    const fr_status st = i8_base<PAIR>(h, xq, ldx, xs, rows, bn, &p);
     if (st != FR_OK) return st;
     p.partial = h->partial;
-    p.n_parts = 2 * h->n_tiles;
+    p.n_parts = 2 * p.n_tiles;
     p.slice = slice;
     p.sid_base = h->sid_base;
     p.sid_span = h->sid_span;
-    return i8_launch(h, p, s);
+    const fr_status run = i8_launch(h, p, s);
+    if (run != FR_OK) return run;
+    FR_CUDA_TRY(fr::launch_pdl(fr::k_i8_combine, ((int64_t)rows + 7) / 8, 256, 0, s, (const float2*)h->partial, rows, p.n_parts,
+                               lse, h->err));
+    return FR_OK;
 }
 
 template <class T>
@@ -613,19 +627,18 @@ extern "C" fr_status fr_i8_init(const int8_t* weight_dev, int64_t ldw, const flo
     h->max_rows = max_rows;
     h->sid_base = sid_base;
     h->sid_span = sid_span;
-    h->n_tiles = (N + fr::GM_TILE - 1) / fr::GM_TILE;
+    h->partials = (int64_t)max_rows * 2 * ((N + fr::GM_TILE - 1) / fr::GM_TILE) + fr::I8_PARTIALS_MORE;
+    CUtensorMap map;
     if (cudaGetDevice(&h->device) != cudaSuccess ||
         cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, h->device) != cudaSuccess ||
-        !fr::gm_encode(&h->map_w[0], 1, weight_dev, N, d, ldw, fr::GM_HALF) ||
-        !fr::gm_encode(&h->map_w[1], 1, weight_dev, N, d, ldw, fr::GM_HALF / 2) ||
-        !fr::gm_encode(&h->map_w[2], 1, weight_dev, N, d, ldw, fr::GM_HALF / 4) ||
+        !fr::gm_encode(&map, 1, weight_dev, N, d, ldw, fr::GM_HALF) ||
         i8_setup_few<float>() != cudaSuccess || i8_setup_few<__nv_bfloat16>() != cudaSuccess ||
         i8_setup_tiles<true>() != cudaSuccess || i8_setup_tiles<false>() != cudaSuccess) {
         (void)cudaGetLastError();
         delete h;
         return FR_ERR_CUDA;
     }
-    cudaError_t e = cudaMalloc(&h->partial, sizeof(float2) * (size_t)max_rows * 2 * h->n_tiles);
+    cudaError_t e = cudaMalloc(&h->partial, sizeof(float2) * (size_t)h->partials);
     if (e == cudaSuccess) e = cudaMalloc(&h->err, sizeof(int32_t));
     if (e == cudaSuccess) e = cudaMemset(h->err, 0, sizeof(int32_t));
     if (e != cudaSuccess) {
@@ -663,12 +676,8 @@ extern "C" fr_status fr_i8_lse(fr_i8* h, const int8_t* xq_dev, int64_t ldx, cons
     const cudaStream_t s = (cudaStream_t)stream;
     h->last_stream = s;
     if (rows == 0) return FR_OK;
-    const fr_status st = rows <= fr::GM_HALF ? i8_rows_lse<false>(h, xq_dev, ldx, xscale_dev, rows, slice_dev, s)
-                                             : i8_rows_lse<true>(h, xq_dev, ldx, xscale_dev, rows, slice_dev, s);
-    if (st != FR_OK) return st;
-    FR_CUDA_TRY(fr::launch_pdl(fr::k_i8_combine, ((int64_t)rows + 7) / 8, 256, 0, s, (const float2*)h->partial, rows,
-                               2 * h->n_tiles, lse_dev, h->err));
-    return FR_OK;
+    return rows <= fr::GM_HALF ? i8_rows_lse<false>(h, xq_dev, ldx, xscale_dev, rows, lse_dev, slice_dev, s)
+                               : i8_rows_lse<true>(h, xq_dev, ldx, xscale_dev, rows, lse_dev, slice_dev, s);
 }
 
 extern "C" fr_status fr_i8_status(fr_i8* h) {
