@@ -266,8 +266,9 @@ __global__ void __launch_bounds__(FEW_THREADS) k_i8_few(const int8_t* __restrict
 
 constexpr int64_t I8_PARTIALS_MORE = 1 << 16;  // for narrow tiles of small calls
 
-// Tile walk shared by the two products.
-template <bool PAIR_>
+// Tile walk shared by the two products.  BN: columns of a tile, known to the compiler
+// (256) or not (0).
+template <bool PAIR_, int BN>
 struct I8Base {
     static constexpr bool I8 = true, DYNAMIC = false, PAIR = PAIR_;
     static constexpr int TM = PAIR ? GM_TILE : GM_HALF;  // rows of a tile
@@ -283,8 +284,10 @@ struct I8Base {
         gm_prefetch(&map_w);
     }
     int32_t rows, N, k_blocks, m_tiles, n_tiles;
-    int32_t bn;  // columns of a tile
-    int32_t a_rows;  // rows of a copy of x
+    int32_t narrow_bn;      // columns of a tile where BN is 0
+    int32_t single_a_rows;  // rows of a single CTA's copy of x
+    __device__ __forceinline__ int bn() const { return BN ? BN : narrow_bn; }
+    __device__ __forceinline__ int a_rows() const { return PAIR ? GM_HALF : single_a_rows; }
     const float* xs;
     const float* ws;
     int32_t ws_vec;  // ws starts on 16 bytes
@@ -297,19 +300,19 @@ struct I8Base {
         gm_grouped(g, m_tiles, n_tiles, m, n);
         t.m0 = m * TM;
         t.n = n;
-        t.n0 = n * bn;
+        t.n0 = n * bn();
         t.nk = k_blocks;
-        t.idesc = gm_idesc(true, PAIR, false, false, bn);
+        t.idesc = gm_idesc(true, PAIR, false, false, bn());
         return true;
     }
-    __device__ __forceinline__ uint32_t stage_bytes(const Tile&) const { return ((PAIR ? 2 : 1) * a_rows + bn) * GM_KB_BYTES; }
+    __device__ __forceinline__ uint32_t stage_bytes(const Tile&) const { return ((PAIR ? 2 : 1) * a_rows() + bn()) * GM_KB_BYTES; }
     __device__ __forceinline__ bool a_mn(const Tile&) const { return false; }
     __device__ __forceinline__ bool b_mn(const Tile&) const { return false; }
     __device__ __forceinline__ void load(const Tile& t, int kb, int rank, uint8_t* a, uint8_t* b, uint32_t bar) const {
         gm_tma_load<PAIR>(&map_x, a, bar, kb * GM_KB_BYTES, t.m0 + rank * GM_HALF);
         // a box is half a tile's columns: the CTA's, or both
-        gm_tma_load<PAIR>(&map_w, b, bar, kb * GM_KB_BYTES, t.n0 + rank * (bn / 2));
-        if constexpr (!PAIR) gm_tma_load<PAIR>(&map_w, b + bn / 2 * GM_KB_BYTES, bar, kb * GM_KB_BYTES, t.n0 + bn / 2);
+        gm_tma_load<PAIR>(&map_w, b, bar, kb * GM_KB_BYTES, t.n0 + rank * (bn() / 2));
+        if constexpr (!PAIR) gm_tma_load<PAIR>(&map_w, b + bn() / 2 * GM_KB_BYTES, bar, kb * GM_KB_BYTES, t.n0 + bn() / 2);
     }
     // y of CW columns from n on: the row's scale first, then the channel's
     template <int CW>
@@ -342,9 +345,9 @@ struct I8Base {
     }
 };
 
-template <class T, bool PAIR_>
-struct I8Out : I8Base<PAIR_> {
-    using Base = I8Base<PAIR_>;
+template <class T, bool PAIR_, int BN>
+struct I8Out : I8Base<PAIR_, BN> {
+    using Base = I8Base<PAIR_, BN>;
     using typename Base::State;
     using typename Base::Tile;
     using Base::bn;
@@ -365,7 +368,7 @@ struct I8Out : I8Base<PAIR_> {
                                              GmRelease<PAIR_>& release) const {
         constexpr int CW = 128 / sizeof(T);  // columns per staged store
         const int row = t.m0 + r, lane = threadIdx.x & 31, row0 = row - lane;
-        const int cols = (bn / 2 + CW - 1) / CW * CW, c1 = min((half + 1) * cols, bn);
+        const int cols = (bn() / 2 + CW - 1) / CW * CW, c1 = min((half + 1) * cols, bn());
         if (row0 >= rows) return;
         const float xscale = row < rows ? xs[row] : 0.f;
 #pragma unroll 1
@@ -381,9 +384,9 @@ struct I8Out : I8Base<PAIR_> {
     }
 };
 
-template <bool PAIR_>
-struct I8Lse : I8Base<PAIR_> {
-    using Base = I8Base<PAIR_>;
+template <bool PAIR_, int BN>
+struct I8Lse : I8Base<PAIR_, BN> {
+    using Base = I8Base<PAIR_, BN>;
     using typename Base::State;
     using typename Base::Tile;
     using Base::bn;
@@ -399,7 +402,7 @@ struct I8Lse : I8Base<PAIR_> {
     int32_t sid_base, sid_span;
     __device__ __forceinline__ void epilogue(const State&, const Tile& t, uint32_t taddr, int r, int half, const GmStage& sg,
                                              GmRelease<PAIR_>& release) const {
-        const int cols = (bn / 2 + 31) & ~31, c1 = min((half + 1) * cols, bn);
+        const int cols = (bn() / 2 + 31) & ~31, c1 = min((half + 1) * cols, bn());
         const int row = t.m0 + r, lane = threadIdx.x & 31, row0 = row - lane;
         if (row0 >= rows) return;
         const float xscale = row < rows ? xs[row] : 0.f;
@@ -469,14 +472,14 @@ bool i8_on_device(const fr_i8* h) {
     return cudaGetDevice(&dev) == cudaSuccess && dev == h->device;
 }
 
-template <bool PAIR>
-fr_status i8_base(fr_i8* h, const int8_t* xq, int64_t ldx, const float* xs, int32_t rows, int32_t bn, fr::I8Base<PAIR>* b) {
-    constexpr int TM = fr::I8Base<PAIR>::TM;
-    b->a_rows = PAIR ? fr::GM_HALF : fr::gm_a_rows(rows);
-    if (!fr::gm_encode(&b->map_x, 1, xq, rows, h->d, ldx, b->a_rows) ||
+template <bool PAIR, int BN>
+fr_status i8_base(fr_i8* h, const int8_t* xq, int64_t ldx, const float* xs, int32_t rows, int32_t bn, fr::I8Base<PAIR, BN>* b) {
+    constexpr int TM = fr::I8Base<PAIR, BN>::TM;
+    b->single_a_rows = fr::gm_a_rows(rows);
+    if (!fr::gm_encode(&b->map_x, 1, xq, rows, h->d, ldx, PAIR ? fr::GM_HALF : b->single_a_rows) ||
         !fr::gm_encode(&b->map_w, 1, h->wq, h->N, h->d, h->ldw, bn / 2))
         return FR_ERR_CUDA;
-    b->bn = bn;
+    b->narrow_bn = bn;
     b->rows = rows;
     b->N = h->N;
     b->k_blocks = (h->d + fr::GM_KB_BYTES - 1) / fr::GM_KB_BYTES;
@@ -490,10 +493,9 @@ fr_status i8_base(fr_i8* h, const int8_t* xq, int64_t ldx, const float* xs, int3
 }
 
 // Tile width of a call.
-template <bool PAIR>
 int32_t i8_width(const fr_i8* h, int32_t rows, int32_t step) {
-    constexpr int TM = fr::I8Base<PAIR>::TM;
-    return fr::gm_width((rows + TM - 1) / TM, h->N, PAIR ? h->sms / 2 : h->sms, step);
+    if (rows <= fr::GM_HALF) return fr::gm_width(1, h->N, h->sms, step);
+    return fr::gm_width((rows + fr::GM_TILE - 1) / fr::GM_TILE, h->N, h->sms / 2, step);
 }
 
 template <class P>
@@ -503,12 +505,11 @@ fr_status i8_launch(fr_i8* h, const P& p, cudaStream_t s) {
     return FR_OK;
 }
 
-template <class T, bool PAIR>
-fr_status i8_tiles(fr_i8* h, const int8_t* xq, int64_t ldx, const float* xs, int32_t rows, void* out, int64_t ldo,
+template <class T, bool PAIR, int BN>
+fr_status i8_tiles(fr_i8* h, int32_t bn, const int8_t* xq, int64_t ldx, const float* xs, int32_t rows, void* out, int64_t ldo,
                    cudaStream_t s) {
-    fr::I8Out<T, PAIR> p{};
-    // (whole staged stores)
-    const fr_status st = i8_base<PAIR>(h, xq, ldx, xs, rows, i8_width<PAIR>(h, rows, 128 / sizeof(T)), &p);
+    fr::I8Out<T, PAIR, BN> p{};
+    const fr_status st = i8_base<PAIR, BN>(h, xq, ldx, xs, rows, bn, &p);
     if (st != FR_OK) return st;
     p.out = (T*)out;
     p.ldo = ldo;
@@ -533,17 +534,16 @@ fr_status i8_out(fr_i8* h, const int8_t* xq, int64_t ldx, const float* xs, int32
             return FR_OK;
         }
     }
-    return rows <= fr::GM_HALF ? i8_tiles<T, false>(h, xq, ldx, xs, rows, out, ldo, s)
-                               : i8_tiles<T, true>(h, xq, ldx, xs, rows, out, ldo, s);
+    const int32_t bn = i8_width(h, rows, 128 / sizeof(T));  // (whole staged stores)
+    const auto run = rows <= fr::GM_HALF ? i8_tiles<T, false, 0> : bn == fr::GM_TILE ? i8_tiles<T, true, fr::GM_TILE> : i8_tiles<T, true, 0>;
+    return run(h, bn, xq, ldx, xs, rows, out, ldo, s);
 }
 
-template <bool PAIR>
-fr_status i8_rows_lse(fr_i8* h, const int8_t* xq, int64_t ldx, const float* xs, int32_t rows, float* lse, float* slice,
+template <bool PAIR, int BN>
+fr_status i8_rows_lse(fr_i8* h, int32_t bn, const int8_t* xq, int64_t ldx, const float* xs, int32_t rows, float* lse, float* slice,
                       cudaStream_t s) {
-    fr::I8Lse<PAIR> p{};
-    int32_t bn = i8_width<PAIR>(h, rows, 32);
-    if ((int64_t)rows * 2 * ((h->N + bn - 1) / bn) > h->partials) bn = fr::GM_TILE;
-    const fr_status st = i8_base<PAIR>(h, xq, ldx, xs, rows, bn, &p);
+    fr::I8Lse<PAIR, BN> p{};
+    const fr_status st = i8_base<PAIR, BN>(h, xq, ldx, xs, rows, bn, &p);
     if (st != FR_OK) return st;
     p.partial = h->partial;
     p.n_parts = 2 * p.n_tiles;
@@ -566,11 +566,11 @@ cudaError_t i8_setup_few() {
     return cudaSuccess;
 }
 
-template <bool PAIR>
+template <bool PAIR, int BN>
 cudaError_t i8_setup_tiles() {
-    cudaError_t e = fr::gm_setup(fr::k_i8<fr::I8Out<float, PAIR>>);
-    if (e == cudaSuccess) e = fr::gm_setup(fr::k_i8<fr::I8Out<__nv_bfloat16, PAIR>>);
-    if (e == cudaSuccess) e = fr::gm_setup(fr::k_i8<fr::I8Lse<PAIR>>);
+    cudaError_t e = fr::gm_setup(fr::k_i8<fr::I8Out<float, PAIR, BN>>);
+    if (e == cudaSuccess) e = fr::gm_setup(fr::k_i8<fr::I8Out<__nv_bfloat16, PAIR, BN>>);
+    if (e == cudaSuccess) e = fr::gm_setup(fr::k_i8<fr::I8Lse<PAIR, BN>>);
     return e;
 }
 
@@ -633,7 +633,8 @@ extern "C" fr_status fr_i8_init(const int8_t* weight_dev, int64_t ldw, const flo
         cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, h->device) != cudaSuccess ||
         !fr::gm_encode(&map, 1, weight_dev, N, d, ldw, fr::GM_HALF) ||
         i8_setup_few<float>() != cudaSuccess || i8_setup_few<__nv_bfloat16>() != cudaSuccess ||
-        i8_setup_tiles<true>() != cudaSuccess || i8_setup_tiles<false>() != cudaSuccess) {
+        i8_setup_tiles<true, fr::GM_TILE>() != cudaSuccess || i8_setup_tiles<true, 0>() != cudaSuccess ||
+        i8_setup_tiles<false, 0>() != cudaSuccess) {
         (void)cudaGetLastError();
         delete h;
         return FR_ERR_CUDA;
@@ -676,8 +677,10 @@ extern "C" fr_status fr_i8_lse(fr_i8* h, const int8_t* xq_dev, int64_t ldx, cons
     const cudaStream_t s = (cudaStream_t)stream;
     h->last_stream = s;
     if (rows == 0) return FR_OK;
-    return rows <= fr::GM_HALF ? i8_rows_lse<false>(h, xq_dev, ldx, xscale_dev, rows, lse_dev, slice_dev, s)
-                               : i8_rows_lse<true>(h, xq_dev, ldx, xscale_dev, rows, lse_dev, slice_dev, s);
+    int32_t bn = i8_width(h, rows, 32);
+    if ((int64_t)rows * 2 * ((h->N + bn - 1) / bn) > h->partials) bn = fr::GM_TILE;
+    const auto run = rows <= fr::GM_HALF ? i8_rows_lse<false, 0> : bn == fr::GM_TILE ? i8_rows_lse<true, fr::GM_TILE> : i8_rows_lse<true, 0>;
+    return run(h, bn, xq_dev, ldx, xscale_dev, rows, lse_dev, slice_dev, s);
 }
 
 extern "C" fr_status fr_i8_status(fr_i8* h) {
