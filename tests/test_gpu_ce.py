@@ -122,6 +122,7 @@ def _grad(ce, h, w, t, lse, gl, pad=0, offset=0):
     (100, 30000, 75, 0.4, 2.0, 2, 1),
     (600, 700, 300, 0.2, 2.0, 1, 1),
     (20000, 50, 16, 0.3, 2.0, 0, 0),     # many rows, few tokens
+    (7, 900, 150, 0.0, 2.0, 4, 2),       # dW's rows start on 4 bytes
 ])
 def test_loss_and_gradients(handle, rows, V, d, ignored, gain, pad, offset):
     h, w, t, gl = _inputs(rows, V, d, rows + V + d, gain, ignored, extra=8 if pad else 0)

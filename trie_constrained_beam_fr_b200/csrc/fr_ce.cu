@@ -75,7 +75,7 @@ __device__ __forceinline__ int32_t ce_k_rows(int32_t n) { return max((n + 63) / 
 // A CTA packs `per` consecutive rows, CE_GATHER_ROWS at a time.  Each counts the
 // counted rows before its own and in all by reading every target, so no CTA waits
 // for another; four CTAs per SM at most keep those reads to a few KB for each row.
-constexpr int CE_GATHER_ROWS = 16;
+constexpr int CE_GATHER_ROWS = 8;  // a warp each
 constexpr int CE_GATHER_THREADS = 256;
 constexpr int CE_GATHER_CTAS = 16;  // of the gradient, at least: they share the zero rows
 __global__ void __launch_bounds__(CE_GATHER_THREADS)
@@ -140,8 +140,15 @@ __global__ void __launch_bounds__(CE_GATHER_THREADS)
             if (pos >= 0) {
                 const uint4* src = reinterpret_cast<const uint4*>(hidden + r * ldh);
                 uint4* dst = reinterpret_cast<uint4*>(out.h + pos * out.pitch);
-#pragma unroll 8
-                for (int32_t i = lane; i < vecs; i += 32) dst[i] = src[i];
+                for (int32_t i = lane; i < vecs; i += 256) {
+                    uint4 v[8];
+#pragma unroll
+                    for (int u = 0; u < 8; ++u)
+                        if (i + 32 * u < vecs) v[u] = src[i + 32 * u];
+#pragma unroll
+                    for (int u = 0; u < 8; ++u)
+                        if (i + 32 * u < vecs) dst[i + 32 * u] = v[u];
+                }
                 for (int32_t j = (vecs << 3) + lane; j < d; j += 32) out.h[pos * out.pitch + j] = hidden[r * ldh + j];
             } else if (grad_hidden) {
                 for (int32_t j = lane; j < d; j += 32) grad_hidden[r * ldgh + j] = __float2bfloat16_rn(0.f);

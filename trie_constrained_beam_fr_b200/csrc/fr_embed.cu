@@ -47,6 +47,8 @@ constexpr int EM_UNROLL = VEC == 8 ? 4 : 16;  // rows in flight per thread of th
 constexpr int EM_ZERO_ROWS = 128;   // table rows per CTA that zeros
 constexpr int EM_SMALL = 1024;      // most tokens of the gradient in one kernel
 constexpr int EM_SMALL_THREADS = 128;
+template <int VEC>
+constexpr int EM_SMALL_GROUPS = VEC == 8 ? 1 : 4;  // groups of 32 * VEC columns per CTA of that form
 
 // VEC consecutive elements (1, or 8 that start on 16 bytes) as fp32, and back.
 template <int VEC>
@@ -470,20 +472,21 @@ __global__ void __launch_bounds__(EM_THREADS)
 
 // The whole gradient of at most EM_SMALL tokens in one kernel, without a sort:
 // CTA (i, column block) compares token i with all tokens; the first occurrence
-// of a token adds its rows in order, four warps a quarter of the list each (32
-// * VEC columns), joined in warp order.  The CTAs behind those zero the rows
-// that no token fell on.  Bound by latency: reading 1,024 tokens per CTA costs
-// less than the sort's six launches.
+// of a token adds its rows in order, four warps a quarter of the list each (256
+// columns, 128 of rows that start anywhere), joined in warp order.  The CTAs behind
+// those zero the rows that no token fell on.  Bound by latency: reading 1,024 tokens
+// per CTA costs less than the sort's six launches.
 template <class TG, class TT, int VEC>
 __global__ void __launch_bounds__(EM_SMALL_THREADS)
     k_em_small(const TG* __restrict__ grad, int64_t ldg, int32_t d, const int32_t* __restrict__ tokens, int32_t n, int32_t V,
                float scale, TT* __restrict__ table, int64_t ldt, int32_t accumulate, int32_t blocks,
                int32_t* __restrict__ err) {
     constexpr int WARPS = EM_SMALL_THREADS / 32, ROUNDS = EM_SMALL / EM_SMALL_THREADS;
+    constexpr int G = EM_SMALL_GROUPS<VEC>;  // groups of 32 * VEC columns
     __shared__ uint8_t touched[EM_ZERO_ROWS];
     __shared__ uint16_t list[EM_SMALL];
     __shared__ int32_t cnt[ROUNDS][WARPS];
-    __shared__ float sums[WARPS][32 * VEC];
+    __shared__ float sums[WARPS][32 * VEC * G];
     griddep_wait();
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -499,7 +502,7 @@ __global__ void __launch_bounds__(EM_SMALL_THREADS)
         em_zero_rows<TT, VEC>(table, ldt, d, v0, v1, touched);
         return;
     }
-    const int i = blockIdx.x / blocks, j = (blockIdx.x % blocks) * 32 * VEC + lane * VEC;
+    const int i = blockIdx.x / blocks, j = (blockIdx.x % blocks) * 32 * VEC * G + lane * VEC;
     const uint32_t t = em_key(tokens[i], V, err);
     if (t >= (uint32_t)V) return;
     uint32_t hit[ROUNDS];
@@ -521,28 +524,41 @@ __global__ void __launch_bounds__(EM_SMALL_THREADS)
             m += cnt[r][w];
         }
     __syncthreads();
-    float sum[VEC];
+    float sum[G][VEC];
 #pragma unroll
-    for (int q = 0; q < VEC; ++q) sum[q] = 0.f;
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int q = 0; q < VEC; ++q) sum[g][q] = 0.f;
     const int k0 = m * warp / WARPS, k1 = m * (warp + 1) / WARPS;
-    if (j < d) {
 #pragma unroll 4
-        for (int k = k0; k < k1; ++k) {
-            float v[VEC];
-            em_load<VEC>(grad + (int64_t)list[k] * ldg + j, v);
+    for (int k = k0; k < k1; ++k) {
+        const TG* src = grad + (int64_t)list[k] * ldg + j;
 #pragma unroll
-            for (int q = 0; q < VEC; ++q) sum[q] += v[q];
+        for (int g = 0; g < G; ++g) {
+            float v[VEC];
+            if (j + g * 32 * VEC < d) {
+                em_load<VEC>(src + g * 32 * VEC, v);
+#pragma unroll
+                for (int q = 0; q < VEC; ++q) sum[g][q] += v[q];
+            }
         }
     }
 #pragma unroll
-    for (int q = 0; q < VEC; ++q) sums[warp][q * 32 + lane] = sum[q];
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int q = 0; q < VEC; ++q) sums[warp][(g * VEC + q) * 32 + lane] = sum[g][q];
     __syncthreads();
-    if (warp == 0 && j < d) {
+    // a warp finishes every fourth group
 #pragma unroll
-        for (int w = 1; w < WARPS; ++w)
+    for (int g = 0; g < G; ++g) {
+        if (g % WARPS != warp || j + g * 32 * VEC >= d) continue;
 #pragma unroll
-            for (int q = 0; q < VEC; ++q) sum[q] += sums[w][q * 32 + lane];
-        em_write<TT, VEC>(table + (int64_t)t * ldt + j, sum, scale, accumulate != 0);
+        for (int q = 0; q < VEC; ++q) {
+            sum[g][q] = sums[0][(g * VEC + q) * 32 + lane];
+#pragma unroll
+            for (int w = 1; w < WARPS; ++w) sum[g][q] += sums[w][(g * VEC + q) * 32 + lane];
+        }
+        em_write<TT, VEC>(table + (int64_t)t * ldt + j + g * 32 * VEC, sum[g], scale, accumulate != 0);
     }
 }
 
@@ -622,7 +638,7 @@ cudaError_t em_sort(fr_embed* h, const int32_t* tokens, int32_t n, const uint32_
 template <class TG, class TT, int VEC>
 cudaError_t em_grad(fr_embed* h, const void* grad, int64_t ldg, const int32_t* tokens, int32_t n, float scale, void* table,
                     int64_t ldt, int32_t accumulate, cudaStream_t s) {
-    const int32_t blocks = (int32_t)em_ceil(h->d, 32 * VEC);
+    const int32_t blocks = (int32_t)em_ceil(h->d, 32 * VEC * fr::EM_SMALL_GROUPS<VEC>);
     const int64_t zeros = accumulate ? 0 : em_ceil(h->V, fr::EM_ZERO_ROWS);
     if (n <= fr::EM_SMALL && (int64_t)n * blocks < (1 << 30)) {
         if (n * (int64_t)blocks + zeros == 0) return cudaSuccess;
