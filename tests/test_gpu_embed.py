@@ -97,8 +97,11 @@ def _grad_reference(grad, tok, V, scale, before):
     (2049, 5000, 40, F32, BF16, False, 8, 8),
     (4100, 300000, 24, BF16, BF16, True, 5, 3),   # 19 bits of tokens: three sort passes
     (9000, 64, 136, BF16, BF16, False, 0, 0),     # runs over many chunks
-    (1024, 500, 264, F32, BF16, False, 0, 0),     # the most tokens of the one-kernel form
-    (1025, 500, 264, F32, BF16, False, 0, 0),     # the fewest of the sorted form
+    (1024, 500, 264, F32, BF16, False, 0, 0),
+    (1025, 500, 264, F32, BF16, False, 0, 0),
+    (2048, 500, 264, F32, BF16, False, 0, 0),     # the most tokens of the one-kernel form
+    (2049, 500, 264, F32, BF16, False, 0, 0),     # the fewest of the sorted form
+    (2047, 300, 401, F32, BF16, True, 1, 1),
     (300000, 700, 8, F32, F32, False, 0, 0),      # several tiles per sorting CTA
     (32769, 300001, 9, F32, F32, False, 0, 0),
     (20000, 511, 16, F32, F32, False, 0, 0),      # keys that fill their digits

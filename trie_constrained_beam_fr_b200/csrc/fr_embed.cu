@@ -8,7 +8,7 @@
 // reads n rows and writes V (or the touched ones).
 //
 //   k_em_lookup   a warp per row, 8 elements a lane at a time.
-//   k_em_small    the gradient of up to 1,024 tokens in one kernel.
+//   k_em_small    the gradient of few tokens in one kernel.
 //   k_em_hist / k_em_scatter   otherwise a stable radix sort of the tokens with
 //                 their positions, 9 bits a pass (two passes for V < 2^18).
 //   k_em_sum      the sorted positions in chunks of EM_CHUNK: a CTA adds a
@@ -45,7 +45,8 @@ constexpr int EM_JOIN = 32;         // chunks of a long run that are added toget
 template <int VEC>
 constexpr int EM_UNROLL = VEC == 8 ? 4 : 16;  // rows in flight per thread of the sum
 constexpr int EM_ZERO_ROWS = 128;   // table rows per CTA that zeros
-constexpr int EM_SMALL = 1024;      // most tokens of the gradient in one kernel
+constexpr int EM_SMALL = 2048;      // most tokens of the gradient in one kernel, and most
+constexpr int64_t EM_SMALL_READS = 1 << 24;  // tokens that its CTAs may read together
 constexpr int EM_SMALL_THREADS = 128;
 template <int VEC>
 constexpr int EM_SMALL_GROUPS = VEC == 8 ? 1 : 4;  // groups of 32 * VEC columns per CTA of that form
@@ -474,18 +475,23 @@ __global__ void __launch_bounds__(EM_THREADS)
 // CTA (i, column block) compares token i with all tokens; the first occurrence
 // of a token adds its rows in order, four warps a quarter of the list each (256
 // columns, 128 of rows that start anywhere), joined in warp order.  The CTAs behind
-// those zero the rows that no token fell on.  Bound by latency: reading 1,024 tokens
-// per CTA costs less than the sort's six launches.
+// those zero the rows that no token fell on.  Bound by latency: up to EM_SMALL_READS
+// that costs less than the sort's launches (2,000 tokens x 391 bf16 values 17.8 us
+// instead of 30.6, half as many reads 13 instead of 28; twice as many, 2,000 x 2,048:
+// 31.5 and 33.6), and up to EM_SMALL tokens if few of them are common (2,000 tokens of
+// which 14 differ: 25 and 28 us; all alike: 83 and 29).
 template <class TG, class TT, int VEC>
 __global__ void __launch_bounds__(EM_SMALL_THREADS)
     k_em_small(const TG* __restrict__ grad, int64_t ldg, int32_t d, const int32_t* __restrict__ tokens, int32_t n, int32_t V,
                float scale, TT* __restrict__ table, int64_t ldt, int32_t accumulate, int32_t blocks,
                int32_t* __restrict__ err) {
-    constexpr int WARPS = EM_SMALL_THREADS / 32, ROUNDS = EM_SMALL / EM_SMALL_THREADS;
+    constexpr int WARPS = EM_SMALL_THREADS / 32;
+    static_assert(EM_SMALL / 32 <= EM_SMALL_THREADS, "a thread per word of hits");
     constexpr int G = EM_SMALL_GROUPS<VEC>;  // groups of 32 * VEC columns
     __shared__ uint8_t touched[EM_ZERO_ROWS];
     __shared__ uint16_t list[EM_SMALL];
-    __shared__ int32_t cnt[ROUNDS][WARPS];
+    __shared__ uint32_t hits[EM_SMALL / 32];  // bit per token: it is this CTA's
+    __shared__ int32_t cnt[WARPS];
     __shared__ float sums[WARPS][32 * VEC * G];
     griddep_wait();
     griddep_launch_dependents();
@@ -505,24 +511,32 @@ __global__ void __launch_bounds__(EM_SMALL_THREADS)
     const int i = blockIdx.x / blocks, j = (blockIdx.x % blocks) * 32 * VEC * G + lane * VEC;
     const uint32_t t = em_key(tokens[i], V, err);
     if (t >= (uint32_t)V) return;
-    uint32_t hit[ROUNDS];
     bool earlier = false;
-#pragma unroll
-    for (int r = 0; r < ROUNDS; ++r) {
-        const int k = r * EM_SMALL_THREADS + threadIdx.x;
+#pragma unroll 8
+    for (int k = threadIdx.x; k < ((n + 31) & ~31); k += EM_SMALL_THREADS) {
         const bool same = k < n && (uint32_t)tokens[k] == t;
         earlier |= same && k < i;
-        hit[r] = __ballot_sync(0xffffffffu, same);
-        if (lane == 0) cnt[r][warp] = __popc(hit[r]);
+        const uint32_t hit = __ballot_sync(0xffffffffu, same);
+        if (lane == 0) hits[k >> 5] = hit;
     }
     if (__syncthreads_or(earlier)) return;
+    // thread w lists the tokens of word w
+    uint32_t hit = threadIdx.x < (n + 31) / 32 ? hits[threadIdx.x] : 0u;
+    int at = __popc(hit);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int below = __shfl_up_sync(0xffffffffu, at, o);
+        if (lane >= o) at += below;
+    }
+    if (lane == 31) cnt[warp] = at;
+    __syncthreads();
     int m = 0;
-    for (int r = 0; r < ROUNDS; ++r)
-        for (int w = 0; w < WARPS; ++w) {
-            if (w == warp && (hit[r] >> lane & 1u))
-                list[m + __popc(hit[r] & ((1u << lane) - 1u))] = (uint16_t)(r * EM_SMALL_THREADS + threadIdx.x);
-            m += cnt[r][w];
-        }
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+        if (w < warp) at += cnt[w];
+        m += cnt[w];
+    }
+    for (at -= __popc(hit); hit; hit &= hit - 1) list[at++] = (uint16_t)(threadIdx.x * 32 + __ffs(hit) - 1);
     __syncthreads();
     float sum[G][VEC];
 #pragma unroll
@@ -640,7 +654,7 @@ cudaError_t em_grad(fr_embed* h, const void* grad, int64_t ldg, const int32_t* t
                     int64_t ldt, int32_t accumulate, cudaStream_t s) {
     const int32_t blocks = (int32_t)em_ceil(h->d, 32 * VEC * fr::EM_SMALL_GROUPS<VEC>);
     const int64_t zeros = accumulate ? 0 : em_ceil(h->V, fr::EM_ZERO_ROWS);
-    if (n <= fr::EM_SMALL && (int64_t)n * blocks < (1 << 30)) {
+    if (n <= fr::EM_SMALL && (int64_t)n * n * blocks <= fr::EM_SMALL_READS) {
         if (n * (int64_t)blocks + zeros == 0) return cudaSuccess;
         return fr::launch_pdl(fr::k_em_small<TG, TT, VEC>, n * (int64_t)blocks + zeros, fr::EM_SMALL_THREADS, 0, s,
                               (const TG*)grad, ldg, h->d, tokens, n, h->V, scale, (TT*)table, ldt, accumulate, blocks, h->err);
