@@ -322,8 +322,7 @@ void fr_beam_destroy(fr_beam* beam);
  * fr_embed_grad:  the lookup's gradient,
  *   grad_table[v][j] = [accumulate] grad_table[v][j] + scale * sum_{i: tokens[i] = v} grad_out[i][j].
  * The sum is fp32 in an order that depends on the tokens alone (no
- * floating-point atomics; the tokens are sorted first, so repeated tokens are
- * neighbours); it is scaled, added and rounded once.
+ * floating-point atomics); it is scaled, added and rounded once.
  * accumulate = 0 writes every row of the table (zeros where no token fell);
  * accumulate = 1 adds to the rows that tokens fell on and leaves the others
  * untouched, e.g. to add to a tied lm_head's gradient.
