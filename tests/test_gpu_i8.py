@@ -105,8 +105,8 @@ def test_quantize_rows_that_are_not_finite():
     assert torch.all(q[:2] == 0) and torch.all(q[2] == 127)
 
 
-# up to 4 rows stream the weight; the others run on tiles of 256, 128 or 64 columns
-SHAPES = [(1, 1, 1), (1, 300, 64), (2, 77, 130), (3, 2001, 1000), (4, 41, 7), (4, 300, 9000), (4, 130, 20000), (5, 1000, 2048), (9, 130, 50),
+# one or two long rows stream the weight; the others run on tiles of 64 to 256 columns
+SHAPES = [(1, 1, 1), (1, 300, 9000), (2, 77, 1537), (1, 2001, 1600), (2, 130, 30000), (2, 130, 40000), (1, 300, 64), (2, 77, 130), (3, 2001, 1000), (4, 41, 7), (4, 300, 9000), (4, 130, 20000), (5, 1000, 2048), (9, 130, 50),
           (16, 513, 96), (20, 15001, 40), (33, 64, 16), (100, 1003, 521), (128, 256, 128),
           (129, 2500, 333), (300, 700, 4096)]
 
@@ -180,7 +180,7 @@ def test_sums_at_the_end_of_the_short_rows(handle, rows, d):
     assert torch.equal(sl.double().cpu(), want[:, 3:67])
 
 
-@pytest.mark.parametrize("rows", [1, 3])
+@pytest.mark.parametrize("rows", [1, 2, 3])
 @pytest.mark.parametrize("N,d", [(5, 16), (5, 17), (8, 527), (9, 2048), (9, 2049), (10, 2063), (31, 2064), (6, 5000), (6, 6143)])
 def test_the_few_rows_last_pieces(handle, rows, N, d):
     """Rows that end anywhere in the pieces, and a weight that ends with its last row."""

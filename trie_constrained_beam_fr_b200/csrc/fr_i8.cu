@@ -9,8 +9,8 @@
 // why the whole product runs on integers.
 //
 //   k_i8_quantize  a warp or a CTA per row: maximum, then values, held in registers.
-//   k_i8_few       up to 4 tokens: a stream over the weight (__dp4a).
-//   k_i8<I8Out>    tcgen05 kind::i8 tiles of 256 rows x 256 channels; the
+//   k_i8_few       one or two tokens of long rows: a stream over the weight (__dp4a).
+//   k_i8<I8Out>    tcgen05 kind::i8 tiles of up to 256 rows x 256 channels; the
 //                  epilogue scales and writes logits (bf16 or fp32).
 //   k_i8<I8Lse>    the same product whose epilogue reduces each row to
 //                  (max, scaled sum) partials and writes the SID slice, for
@@ -137,14 +137,17 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR)
     if (tid == 0) scale[r] = s;
 }
 
-// The product for up to 4 tokens: bound by the weight's bytes, which go straight
-// to registers (16 bytes a lane, 4 channels x 2,048 values per warp in flight);
-// the tokens lie in shared memory (zeros behind d), __dp4a multiplies and one
-// warp reduction per value adds the lanes.  A warp takes 4 channels at a time,
+// The product for one or two tokens of long rows: bound by the weight's bytes, which
+// go straight to registers (16 bytes a lane, 4 channels x 2,048 values per warp in
+// flight); the tokens lie in shared memory (zeros behind d), __dp4a multiplies and
+// one warp reduction per value adds the lanes.  A warp takes 4 channels at a time,
 // so the channels spread evenly over the SMs.  151,936 channels x 2,048 values:
-// 49 to 58 us for 1 to 4 tokens (6.3 to 5.4 TB/s) where the tiles take 60 to 62; 8
-// tokens (bound by __dp4a) took 85 us.
-constexpr int FEW_ROWS = 4;
+// 50 and 51 us for 1 and 2 tokens (6.2 TB/s) where the tiles take 60.  On the other
+// side, 4 tokens of 2,048 values: 60 and 62 (__dp4a begins to bind; of 1,536 values 50
+// and 45); one token of 1,536 values: 44 and 44, of 700: 39 and 29 (too few loads in
+// flight at a row's end).
+constexpr int FEW_ROWS = 2;
+constexpr int FEW_LEAST = 1537;  // least d
 constexpr int FEW_THREADS = 256;
 constexpr int FEW_CH = 4;
 constexpr int FEW_STEPS = 4;
@@ -160,8 +163,8 @@ __device__ __forceinline__ int4 few_load(const int8_t* p) {
 template <int R, class T>
 __global__ void __launch_bounds__(FEW_THREADS) k_i8_few(const int8_t* __restrict__ xq, int64_t ldx,
                                                         const float* __restrict__ xs, const int8_t* __restrict__ wq,
-                                                        int64_t ldw, const float* __restrict__ ws, int32_t rows, int32_t N,
-                                                        int32_t d, T* __restrict__ out, int64_t ldo) {
+                                                        int64_t ldw, const float* __restrict__ ws, int32_t N, int32_t d,
+                                                        T* __restrict__ out, int64_t ldo) {
     extern __shared__ __align__(16) int8_t few_x[];  // [R][pitch]
     const int32_t pieces = (d + 15) >> 4, pitch = pieces << 4;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -171,13 +174,11 @@ __global__ void __launch_bounds__(FEW_THREADS) k_i8_few(const int8_t* __restrict
         const int32_t r = i / pieces, k = (i - r * pieces) << 4;
         const int8_t* src = xq + r * ldx + k;
         int4 v = make_int4(0, 0, 0, 0);
-        if (r < rows) {
-            if (k + 16 <= d) {
-                v = *reinterpret_cast<const int4*>(src);
-            } else {
-                int8_t* b = reinterpret_cast<int8_t*>(&v);
-                for (int j = 0; j < d - k; ++j) b[j] = src[j];
-            }
+        if (k + 16 <= d) {
+            v = *reinterpret_cast<const int4*>(src);
+        } else {
+            int8_t* b = reinterpret_cast<int8_t*>(&v);
+            for (int j = 0; j < d - k; ++j) b[j] = src[j];
         }
         *reinterpret_cast<int4*>(few_x + r * pitch + k) = v;
     }
@@ -254,7 +255,7 @@ __global__ void __launch_bounds__(FEW_THREADS) k_i8_few(const int8_t* __restrict
                 if (lane == r * FEW_CH + c) mine = sum;
             }
         const int32_t r = lane / FEW_CH, n = n0 + lane % FEW_CH;
-        if (r < rows && r < R && n < N) {
+        if (r < R && n < N) {
             const float y = (float)mine * xs[r] * __ldg(ws + n);
             if constexpr (sizeof(T) == 4)
                 out[r * ldo + n] = y;
@@ -522,15 +523,14 @@ fr_status i8_tiles(fr_i8* h, int32_t bn, const int8_t* xq, int64_t ldx, const fl
 template <class T>
 fr_status i8_out(fr_i8* h, const int8_t* xq, int64_t ldx, const float* xs, int32_t rows, void* out, int64_t ldo,
                  cudaStream_t s) {
-    if (rows <= fr::FEW_ROWS) {
-        // 1, 2 or 4 tokens at a time, as long as they fit into shared memory
-        const int R = rows <= 1 ? 1 : rows <= 2 ? 2 : 4;
-        const size_t smem = (size_t)R * ((h->d + 15) / 16 * 16);
+    if (rows <= fr::FEW_ROWS && h->d >= fr::FEW_LEAST) {
+        // as long as the tokens fit into shared memory
+        const size_t smem = (size_t)rows * ((h->d + 15) / 16 * 16);
         if (smem <= (size_t)fr::FEW_SMEM) {
-            auto k = R == 1 ? fr::k_i8_few<1, T> : R == 2 ? fr::k_i8_few<2, T> : fr::k_i8_few<4, T>;
+            auto k = rows == 1 ? fr::k_i8_few<1, T> : fr::k_i8_few<2, T>;
             const int64_t groups = (h->N + fr::FEW_CH - 1) / fr::FEW_CH, warps = fr::FEW_THREADS / 32;
             FR_CUDA_TRY(fr::launch_pdl(k, std::min<int64_t>((groups + warps - 1) / warps, 3 * (int64_t)h->sms), fr::FEW_THREADS,
-                                       smem, s, xq, ldx, xs, h->wq, h->ldw, h->ws, rows, h->N, h->d, (T*)out, ldo));
+                                       smem, s, xq, ldx, xs, h->wq, h->ldw, h->ws, h->N, h->d, (T*)out, ldo));
             return FR_OK;
         }
     }
@@ -559,7 +559,7 @@ fr_status i8_rows_lse(fr_i8* h, int32_t bn, const int8_t* xq, int64_t ldx, const
 
 template <class T>
 cudaError_t i8_setup_few() {
-    for (auto k : {fr::k_i8_few<1, T>, fr::k_i8_few<2, T>, fr::k_i8_few<4, T>}) {
+    for (auto k : {fr::k_i8_few<1, T>, fr::k_i8_few<2, T>}) {
         const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, fr::FEW_SMEM);
         if (e != cudaSuccess) return e;
     }
