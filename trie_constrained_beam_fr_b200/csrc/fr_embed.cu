@@ -291,13 +291,14 @@ __device__ __forceinline__ void em_zero_rows(TT* table, int64_t ldt, int32_t d, 
     }
 }
 
-// One finished column group of a table row.
+// One finished column group of a table row; `old` is what it held, where the sum is
+// added to it (loaded beside the gradients: behind the sum its latency would show for
+// every token).
 template <class TT, int VEC>
-__device__ __forceinline__ void em_write(TT* dst, const float (&sum)[VEC], float scale, bool accumulate) {
+__device__ __forceinline__ void em_write(TT* dst, const float (&sum)[VEC], const float (&old)[VEC], float scale, bool accumulate) {
     float v[VEC];
-    if (accumulate) em_load<VEC>(dst, v);
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) v[k] = accumulate ? fmaf(scale, sum[k], v[k]) : scale * sum[k];
+    for (int k = 0; k < VEC; ++k) v[k] = accumulate ? fmaf(scale, sum[k], old[k]) : scale * sum[k];
     em_store<VEC>(dst, v);
 }
 
@@ -392,10 +393,14 @@ __global__ void __launch_bounds__(EM_THREADS)
         bool from_before = head;
         constexpr int U = EM_UNROLL<VEC>;
         for (int k0 = 0; k0 < m; k0 += U) {
-            float v[U][VEC];
+            float v[U][VEC], old[U][VEC];
 #pragma unroll
             for (int u = 0; u < U; ++u)
                 if (k0 + u < m) em_load<VEC>(grad + (int64_t)ord_s[k0 + u] * ldg + j, v[u]);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (accumulate && k0 + u < m && key_s[k0 + u + 2] != key_s[k0 + u + 1])
+                    em_load<VEC>(table + (int64_t)key_s[k0 + u + 1] * ldt + j, old[u]);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int k = k0 + u;
@@ -406,7 +411,7 @@ __global__ void __launch_bounds__(EM_THREADS)
                 const bool ends = key_s[k + 2] != key;
                 if (ends || k == m - 1) {
                     if (ends && !from_before)
-                        em_write<TT, VEC>(table + (int64_t)key * ldt + j, sum, scale, accumulate != 0);
+                        em_write<TT, VEC>(table + (int64_t)key * ldt + j, sum, old[u], scale, accumulate != 0);
                     else
                         em_store<VEC>(part + (2 * (int64_t)chunk + (from_before ? 0 : 1)) * pitch + j, sum);
                     from_before = false;
@@ -467,7 +472,11 @@ __global__ void __launch_bounds__(EM_THREADS)
                 }
             }
         }
-        if (j < d) em_write<TT, VEC>(table + (int64_t)key * ldt + j, sum, scale, accumulate != 0);
+        if (j < d) {
+            float old[VEC];
+            if (accumulate) em_load<VEC>(table + (int64_t)key * ldt + j, old);
+            em_write<TT, VEC>(table + (int64_t)key * ldt + j, sum, old, scale, accumulate != 0);
+        }
     }
 }
 
@@ -543,6 +552,12 @@ __global__ void __launch_bounds__(EM_SMALL_THREADS)
     for (int g = 0; g < G; ++g)
 #pragma unroll
         for (int q = 0; q < VEC; ++q) sum[g][q] = 0.f;
+    // a warp finishes every fourth group
+    float old[G][VEC];
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+        if (accumulate && g % WARPS == warp && j + g * 32 * VEC < d)
+            em_load<VEC>(table + (int64_t)t * ldt + j + g * 32 * VEC, old[g]);
     const int k0 = m * warp / WARPS, k1 = m * (warp + 1) / WARPS;
 #pragma unroll 4
     for (int k = k0; k < k1; ++k) {
@@ -562,7 +577,6 @@ __global__ void __launch_bounds__(EM_SMALL_THREADS)
 #pragma unroll
         for (int q = 0; q < VEC; ++q) sums[warp][(g * VEC + q) * 32 + lane] = sum[g][q];
     __syncthreads();
-    // a warp finishes every fourth group
 #pragma unroll
     for (int g = 0; g < G; ++g) {
         if (g % WARPS != warp || j + g * 32 * VEC >= d) continue;
@@ -572,7 +586,7 @@ __global__ void __launch_bounds__(EM_SMALL_THREADS)
 #pragma unroll
             for (int w = 1; w < WARPS; ++w) sum[g][q] += sums[w][(g * VEC + q) * 32 + lane];
         }
-        em_write<TT, VEC>(table + (int64_t)t * ldt + j + g * 32 * VEC, sum[g], scale, accumulate != 0);
+        em_write<TT, VEC>(table + (int64_t)t * ldt + j + g * 32 * VEC, sum[g], old[g], scale, accumulate != 0);
     }
 }
 
