@@ -140,9 +140,9 @@ def _check(status: int, what: str) -> None:
         raise FrError(status, what)
 
 
-def _stream(stream) -> Optional[int]:
+def _stream(stream, device: Optional[int] = None) -> Optional[int]:
     if stream is None:  # the current stream's handle, without building a Stream object (a microsecond and a half)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if device is None else device)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -455,13 +455,15 @@ def fr_lmhead_destroy(lmhead) -> None:
 # are checked here.
 
 
-def _on_current_device(*tensors: Optional[torch.Tensor]) -> None:
+def _on_current_device(*tensors: Optional[torch.Tensor]) -> int:
+    """Checks that every tensor is on the current device; returns it."""
     here = torch.cuda.current_device()
     for t in tensors:
         if t is not None and t.get_device() != here:
             if not t.is_cuda:
                 raise ValueError("expected a CUDA tensor")
             raise ValueError("every tensor must be on the current CUDA device (%d)" % here)
+    return here
 
 
 def _matrix(t: torch.Tensor, what: str, dtypes, rows: Optional[int], cols: int) -> int:
@@ -510,25 +512,25 @@ def fr_embed_lookup(embed, table: torch.Tensor, tokens: torch.Tensor, out: torch
     """out[i] = scale * table[tokens[i]] (zeros for token -1).  table [V, d]
     and out [n, d] float32 or bf16, tokens int32 [n]."""
     n = tokens.shape[0] if tokens.dim() == 1 else -1
-    _on_current_device(table, tokens, out)
+    here = _on_current_device(table, tokens, out)
     _vector(tokens, "tokens", torch.int32, n)
     ldt = _matrix(table, "table", _FLOATS, embed.V, embed.d)
     ldo = _matrix(out, "out", _FLOATS, n, embed.d)
     _check(libfr().fr_embed_lookup(embed, _ptr(table), ldt, _FLOATS[table.dtype], _ptr(tokens), n, float(scale),
-                                   _ptr(out), ldo, _FLOATS[out.dtype], _stream(stream)), "fr_embed_lookup")
+                                   _ptr(out), ldo, _FLOATS[out.dtype], _stream(stream, here)), "fr_embed_lookup")
 
 
 def fr_embed_grad(embed, grad_out: torch.Tensor, tokens: torch.Tensor, grad_table: torch.Tensor, scale: float = 1.0,
                   accumulate: bool = False, stream=None) -> None:
     """grad_table[v] (+)= scale * sum of grad_out's rows whose token is v."""
     n = tokens.shape[0] if tokens.dim() == 1 else -1
-    _on_current_device(grad_out, tokens, grad_table)
+    here = _on_current_device(grad_out, tokens, grad_table)
     _vector(tokens, "tokens", torch.int32, n)
     ldg = _matrix(grad_out, "grad_out", _FLOATS, n, embed.d)
     ldt = _matrix(grad_table, "grad_table", _FLOATS, embed.V, embed.d)
     _check(libfr().fr_embed_grad(embed, _ptr(grad_out), ldg, _FLOATS[grad_out.dtype], _ptr(tokens), n, float(scale),
                                  _ptr(grad_table), ldt, _FLOATS[grad_table.dtype], int(bool(accumulate)),
-                                 _stream(stream)), "fr_embed_grad")
+                                 _stream(stream, here)), "fr_embed_grad")
 
 
 def fr_embed_status(embed) -> int:
@@ -564,12 +566,12 @@ def fr_ce_loss(ce, hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Te
     """Each row's cross entropy of hidden @ weight.T against its target (0 for
     target -1) and its log-sum-exp.  hidden bf16 [rows, d], weight bf16 [V, d],
     targets int32 [rows], loss and lse float32 [rows]."""
-    _on_current_device(hidden, weight, targets, loss, lse)
+    here = _on_current_device(hidden, weight, targets, loss, lse)
     rows, ldh, ldw = _ce_inputs(ce, hidden, weight, targets)
     _vector(loss, "loss", torch.float32, rows)
     _vector(lse, "lse", torch.float32, rows)
     _check(libfr().fr_ce_loss(ce, _ptr(hidden), ldh, _ptr(weight), ldw, _ptr(targets), rows, _ptr(loss), _ptr(lse),
-                              _stream(stream)), "fr_ce_loss")
+                              _stream(stream, here)), "fr_ce_loss")
 
 
 def fr_ce_grad(ce, hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor,
@@ -578,14 +580,14 @@ def fr_ce_grad(ce, hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Te
     """The loss's gradients from fr_ce_loss's lse and the rows' incoming
     gradients (float32 [rows]): grad_hidden bf16 [rows, d], grad_weight bf16
     [V, d]; either may be None."""
-    _on_current_device(hidden, weight, targets, lse, grad_loss, grad_hidden, grad_weight)
+    here = _on_current_device(hidden, weight, targets, lse, grad_loss, grad_hidden, grad_weight)
     rows, ldh, ldw = _ce_inputs(ce, hidden, weight, targets)
     _vector(lse, "lse", torch.float32, rows)
     _vector(grad_loss, "grad_loss", torch.float32, rows)
     ldgh = 0 if grad_hidden is None else _matrix(grad_hidden, "grad_hidden", (torch.bfloat16,), rows, ce.d)
     ldgw = 0 if grad_weight is None else _matrix(grad_weight, "grad_weight", (torch.bfloat16,), ce.V, ce.d)
     _check(libfr().fr_ce_grad(ce, _ptr(hidden), ldh, _ptr(weight), ldw, _ptr(targets), _ptr(lse), _ptr(grad_loss), rows,
-                              _ptr(grad_hidden), ldgh, _ptr(grad_weight), ldgw, _stream(stream)), "fr_ce_grad")
+                              _ptr(grad_hidden), ldgh, _ptr(grad_weight), ldgw, _stream(stream, here)), "fr_ce_grad")
 
 
 def fr_ce_status(ce) -> int:
@@ -608,7 +610,7 @@ def fr_ce_destroy(ce) -> None:
 def fr_i8_quantize(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, stream=None) -> None:
     """Rows of x (float32 or bf16 [rows, d]) to int8 q [rows, d] with a scale
     for each row (float32 [rows])."""
-    _on_current_device(x, q, scale)
+    here = _on_current_device(x, q, scale)
     if x.dim() != 2:
         raise ValueError("x must be a [rows, d] tensor")
     rows, d = x.shape
@@ -616,7 +618,7 @@ def fr_i8_quantize(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, stream
     ldq = _matrix(q, "q", (torch.int8,), rows, d)
     _vector(scale, "scale", torch.float32, rows)
     _check(libfr().fr_i8_quantize(_ptr(x), ldx, _FLOATS[x.dtype], rows, d, _ptr(q), ldq, _ptr(scale),
-                                  _stream(stream)), "fr_i8_quantize")
+                                  _stream(stream, here)), "fr_i8_quantize")
 
 
 def fr_i8_init(weight: torch.Tensor, weight_scale: torch.Tensor, max_rows: int, sid_base: int = 0,
@@ -649,18 +651,18 @@ def _i8_inputs(i8, xq, xscale):
 def fr_i8_matmul(i8, xq: torch.Tensor, xscale: torch.Tensor, out: torch.Tensor, stream=None) -> None:
     """out[r, n] = (xq[r] . weight[n]) * xscale[r] * weight_scale[n]; xq int8
     [rows, d] (row pitch a multiple of 16), out float32 or bf16 [rows, N]."""
-    _on_current_device(xq, xscale, out)
+    here = _on_current_device(xq, xscale, out)
     rows, ldx = _i8_inputs(i8, xq, xscale)
     ldo = _matrix(out, "out", _FLOATS, rows, i8.N)
     _check(libfr().fr_i8_matmul(i8, _ptr(xq), ldx, _ptr(xscale), rows, _ptr(out), ldo, _FLOATS[out.dtype],
-                                _stream(stream)), "fr_i8_matmul")
+                                _stream(stream, here)), "fr_i8_matmul")
 
 
 def fr_i8_lse(i8, xq: torch.Tensor, xscale: torch.Tensor, lse: torch.Tensor, slice_: Optional[torch.Tensor],
               stream=None) -> None:
     """The same product as each row's log-sum-exp (float32 [rows]) and SID
     slice (float32 [rows, sid_span], contiguous), for fr_beam_step_lse."""
-    _on_current_device(xq, xscale, lse, slice_)
+    here = _on_current_device(xq, xscale, lse, slice_)
     rows, ldx = _i8_inputs(i8, xq, xscale)
     _vector(lse, "lse", torch.float32, rows)
     if slice_ is None:
@@ -668,7 +670,7 @@ def fr_i8_lse(i8, xq: torch.Tensor, xscale: torch.Tensor, lse: torch.Tensor, sli
             raise ValueError("the handle has a SID range: slice is needed")
     elif _matrix(slice_, "slice", (torch.float32,), rows, i8.sid_span) != i8.sid_span and rows > 1 and i8.sid_span > 0:
         raise ValueError("slice must be contiguous")
-    _check(libfr().fr_i8_lse(i8, _ptr(xq), ldx, _ptr(xscale), rows, _ptr(lse), _ptr(slice_), _stream(stream)), "fr_i8_lse")
+    _check(libfr().fr_i8_lse(i8, _ptr(xq), ldx, _ptr(xscale), rows, _ptr(lse), _ptr(slice_), _stream(stream, here)), "fr_i8_lse")
 
 
 def fr_i8_status(i8) -> int:
