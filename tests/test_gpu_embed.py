@@ -102,6 +102,7 @@ def _grad_reference(grad, tok, V, scale, before):
     (2048, 500, 264, F32, BF16, False, 0, 0),     # the most tokens of the one-kernel form
     (2049, 500, 264, F32, BF16, False, 0, 0),     # the fewest of the sorted form
     (2047, 300, 401, F32, BF16, True, 1, 1),
+    (600, 40, 12000, BF16, F32, True, 0, 0),      # few tokens, sorted: long rows
     (300000, 700, 8, F32, F32, False, 0, 0),      # several tiles per sorting CTA
     (32769, 300001, 9, F32, F32, False, 0, 0),
     (20000, 511, 16, F32, F32, False, 0, 0),      # keys that fill their digits
