@@ -39,9 +39,9 @@
 //                              GmRelease&) const;
 //   };
 //
-// Every wait on a barrier is bounded; on expiry the kernel records
-// FR_ERR_DEVICE, stops issuing, drains the copies and products already issued,
-// frees its tensor memory and returns.
+// Every wait on a barrier is bounded, and a whole warp's ends alike in all its lanes;
+// on expiry the kernel records FR_ERR_DEVICE, stops issuing, drains the copies and
+// products already issued, frees its tensor memory and returns.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -360,9 +360,9 @@ __device__ __forceinline__ void gm_run(const P& p, const GmCtl& ctl) {
         if (!P::DYNAMIC) return p.tile(st, pair + i * pairs, t);
         const int s = i % GM_SLOTS;
         // only the second CTA's readers need to synchronise with another CTA
-        if (!(rank == 0 ? tc_wait(&sm->tile_full[s], (i / GM_SLOTS) & 1, abort_flag, ctl.err, ctl.wait_ns)
-                        : gm_wait_pair(&sm->tile_full[s], (i / GM_SLOTS) & 1, abort_flag, ctl.err, ctl.wait_ns)))
-            return false;
+        const bool there = rank == 0 ? tc_wait(&sm->tile_full[s], (i / GM_SLOTS) & 1, abort_flag, ctl.err, ctl.wait_ns)
+                                     : gm_wait_pair(&sm->tile_full[s], (i / GM_SLOTS) & 1, abort_flag, ctl.err, ctl.wait_ns);
+        if (!(whole ? __all_sync(0xffffffffu, there) : there)) return false;
         const int32_t g = *(volatile int32_t*)&sm->tile_id[s];
         if (whole) __syncwarp();
         if (!whole || lane == 0) {
@@ -475,7 +475,7 @@ __device__ __forceinline__ void gm_run(const P& p, const GmCtl& ctl) {
         const uint32_t empty0 = PAIR ? gm_in_first(&sm->tmem_empty[0]) : 0, empty1 = PAIR ? gm_in_first(&sm->tmem_empty[1]) : 0;
         for (int i = 0; next(i, true); ++i) {
             const int acc = i & 1;
-            if (!tc_wait(&sm->tmem_full[acc], (i >> 1) & 1, abort_flag, ctl.err, ctl.wait_ns)) break;
+            if (!tc_wait_warp(&sm->tmem_full[acc], (i >> 1) & 1, abort_flag, ctl.err, ctl.wait_ns)) break;
             tc_fence_after();
             GmRelease<PAIR> release{&sm->tmem_empty[acc], acc ? empty1 : empty0, lane, false};
             p.epilogue(st, t, tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * GM_TILE), (int)rank * GM_HALF + q * 32 + lane,

@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(LM_THREADS, 1)
         int local = 0;
         for (int tile = blockIdx.x; tile < total_tiles; tile += gridDim.x, ++local) {
             const int acc = local & 1;
-            if (!tc_wait(&sm->tmem_full[acc], (local >> 1) & 1, abort_flag, a.err, a.wait_ns)) break;
+            if (!tc_wait_warp(&sm->tmem_full[acc], (local >> 1) & 1, abort_flag, a.err, a.wait_ns)) break;
             tc_fence_after();
             const int mt = tile % a.m_tiles, nt = tile / a.m_tiles;
             const int row = mt * LM_BM + r_in, n0 = nt * LM_BN;

@@ -65,6 +65,14 @@ __device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, volatile
     }
 }
 
+// The wait of a whole warp.  Each lane polls the barrier and the flag for itself, so
+// while a wait expires their answers may differ; lanes that went on would stop at the
+// next warp-wide instruction and wait there, without limit, for those that gave up.
+__device__ __forceinline__ bool tc_wait_warp(uint64_t* bar, uint32_t parity, volatile int32_t* abort_flag,
+                                             int32_t* err, uint64_t limit_ns) {
+    return __all_sync(0xffffffffu, tc_wait(bar, parity, abort_flag, err, limit_ns));
+}
+
 // Bounded wait that ignores the abort flag (draining work already issued).
 __device__ __forceinline__ void tc_wait_drain(uint64_t* bar, uint32_t parity) {
     const uint64_t t0 = tc_now_ns();
