@@ -163,3 +163,52 @@ def test_two_handles_on_two_streams():
             assert all(torch.equal(x, y) for x, y in zip((s[4], s[7], s[8]), wnt))
     for s in sets:
         fr.fr_ce_destroy(s[0])
+
+
+def _queued():
+    """Work on the default stream that is still running when the caller goes on."""
+    torch.cuda.synchronize()
+    torch.cuda._sleep(400_000_000)  # about 0.2 s
+
+
+@pytest.mark.parametrize("which", ["embed", "ce", "i8", "lmhead"])
+def test_an_error_of_a_run_right_after_init(which):
+    """A handle made while the default stream is busy and used on another stream at
+    once: what that run records is there to read, and a run without an error
+    leaves nothing."""
+    rows, V, d = 4, 70, 32
+    g = torch.Generator().manual_seed(0)
+    bad_tok = torch.tensor([1, V, 2, 3], dtype=torch.int32, device="cuda")
+    good_tok = torch.tensor([1, 5, 2, 3], dtype=torch.int32, device="cuda")
+    good = torch.randn(rows, d, generator=g).to(BF16).cuda()
+    bad = good.clone()
+    bad[2, 3] = float("nan")
+    table = torch.randn(V, d, generator=g).to(BF16).cuda()
+    wq, ws = torch.ones(V, d, dtype=torch.int8, device="cuda"), torch.ones(V, device="cuda")
+    xq, good_s = torch.ones(rows, d, dtype=torch.int8, device="cuda"), torch.ones(rows, device="cuda")
+    bad_s = good_s.clone()
+    bad_s[1] = float("nan")
+    out, loss, lse = torch.empty(rows, d, device="cuda"), torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    side = torch.cuda.Stream()
+    make, run, status, destroy = {
+        "embed": (lambda: fr.fr_embed_init(V, d, rows), lambda h, wrong: fr.fr_embed_lookup(h, table, bad_tok if wrong else good_tok, out, stream=side),
+                  fr.fr_embed_status, fr.fr_embed_destroy),
+        "ce": (lambda: fr.fr_ce_init(V, d, rows), lambda h, wrong: fr.fr_ce_loss(h, good, table, bad_tok if wrong else good_tok, loss, lse, stream=side),
+               fr.fr_ce_status, fr.fr_ce_destroy),
+        "i8": (lambda: fr.fr_i8_init(wq, ws, rows), lambda h, wrong: fr.fr_i8_lse(h, xq, bad_s if wrong else good_s, lse, None, stream=side),
+               fr.fr_i8_status, fr.fr_i8_destroy),
+        "lmhead": (lambda: fr.fr_lmhead_init(table, rows, 0, 0), lambda h, wrong: fr.fr_lmhead_run(h, bad if wrong else good, lse, None, stream=side),
+                   fr.fr_lmhead_status, fr.fr_lmhead_destroy),
+    }[which]
+    want = fr.FR_ERR_CODE_RANGE if which in ("embed", "ce") else fr.FR_ERR_NAN_LOGIT
+    for wrong in (None, True, False):  # (first with nothing queued: a kernel's first launch loads it, which may wait)
+        if wrong is not None:
+            _queued()
+        h = make()
+        try:
+            run(h, wrong)
+            side.synchronize()
+            torch.cuda.synchronize()
+            assert status(h) == (want if wrong else fr.FR_OK), wrong
+        finally:
+            destroy(h)

@@ -798,8 +798,7 @@ extern "C" fr_status fr_ce_init(int32_t V, int32_t d, int32_t max_rows, fr_ce** 
     if (e == cudaSuccess) e = cudaMalloc(&h->partial, (size_t)h->partials * sizeof(float2));
     if (e == cudaSuccess) e = cudaMalloc(&h->g, (size_t)h->g_elems * (h->piece < V ? 2 : 1) * 2);
     if (e == cudaSuccess) e = cudaMalloc(&h->dh, dh_rows * pitch * 4);
-    if (e == cudaSuccess) e = cudaMalloc(&h->err, sizeof(int32_t));
-    if (e == cudaSuccess) e = cudaMemset(h->err, 0, sizeof(int32_t));
+    if (e == cudaSuccess) e = fr::new_status_word(&h->err);
     if (e != cudaSuccess) {
         (void)cudaGetLastError();
         ce_free(h);

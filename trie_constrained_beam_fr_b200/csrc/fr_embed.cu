@@ -714,8 +714,7 @@ extern "C" fr_status fr_embed_init(int32_t V, int32_t d, int32_t max_tokens, fr_
     cudaError_t e = cudaMalloc(&h->keys[0], n * 16);
     if (e == cudaSuccess) e = cudaMalloc(&h->counts, ((size_t)(fr::EM_SORT_CTAS << fr::EM_BITS) + 2 * em_ceil(n, fr::EM_CHUNK) * em_ceil(d, fr::EM_THREADS)) * sizeof(int32_t));
     if (e == cudaSuccess) e = cudaMalloc(&h->part, (size_t)em_ceil(n, fr::EM_CHUNK) * 2 * h->pitch * 4);
-    if (e == cudaSuccess) e = cudaMalloc(&h->err, sizeof(int32_t));
-    if (e == cudaSuccess) e = cudaMemset(h->err, 0, sizeof(int32_t));
+    if (e == cudaSuccess) e = fr::new_status_word(&h->err);
     if (e != cudaSuccess) {
         (void)cudaGetLastError();
         em_free(h);

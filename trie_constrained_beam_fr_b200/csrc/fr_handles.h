@@ -31,6 +31,16 @@ int64_t scan_temp_elems(int64_t n);
 cudaError_t scan_exclusive_i32(const int32_t* in, int32_t* out, int64_t n, int32_t* temp,
                                int32_t* total, cudaStream_t stream);
 
+// A handle's status word, cleared when this returns: the clearing runs on the legacy
+// default stream, behind what is queued there, and a non-blocking stream's first run
+// is not ordered behind it.
+inline cudaError_t new_status_word(int32_t** word) {
+    cudaError_t e = cudaMalloc(word, sizeof(int32_t));
+    if (e == cudaSuccess) e = cudaMemset(*word, 0, sizeof(int32_t));
+    if (e == cudaSuccess) e = cudaStreamSynchronize(cudaStreamLegacy);
+    return e;
+}
+
 }  // namespace fr
 
 #define FR_CUDA_TRY(expr)                                                   \

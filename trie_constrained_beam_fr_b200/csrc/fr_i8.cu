@@ -640,8 +640,7 @@ extern "C" fr_status fr_i8_init(const int8_t* weight_dev, int64_t ldw, const flo
         return FR_ERR_CUDA;
     }
     cudaError_t e = cudaMalloc(&h->partial, sizeof(float2) * (size_t)h->partials);
-    if (e == cudaSuccess) e = cudaMalloc(&h->err, sizeof(int32_t));
-    if (e == cudaSuccess) e = cudaMemset(h->err, 0, sizeof(int32_t));
+    if (e == cudaSuccess) e = fr::new_status_word(&h->err);
     if (e != cudaSuccess) {
         (void)cudaGetLastError();
         cudaFree(h->partial);
