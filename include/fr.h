@@ -322,7 +322,7 @@ void fr_beam_destroy(fr_beam* beam);
  *
  * fr_embed_grad:  the lookup's gradient,
  *   grad_table[v][j] = [accumulate] grad_table[v][j] + scale * sum_{i: tokens[i] = v} grad_out[i][j].
- * The sum is fp32 in an order that depends on the tokens alone (no
+ * The sum is fp32 in an order that depends on the tokens and d alone (no
  * floating-point atomics); it is scaled, added and rounded once.
  * accumulate = 0 writes every row of the table (zeros where no token fell);
  * accumulate = 1 adds to the rows that tokens fell on and leaves the others

@@ -261,3 +261,21 @@ def test_refusals(handle):
             bad()
     with pytest.raises(fr.FrError):
         fr.fr_embed_lookup(h, table, torch.zeros(5, dtype=torch.int32, device="cuda"), torch.ones(5, 16, device="cuda"))
+
+
+@pytest.mark.parametrize("n,d", [(1400, 2048), (1700, 1536), (2048, 1280), (1000, 2056)])
+def test_the_sums_order_does_not_depend_on_where_rows_start(handle, n, d):
+    """The same tokens and values in rows that start on 16 bytes and in rows that
+    start anywhere: the same sums, bit for bit."""
+    g = torch.Generator().manual_seed(n + d)
+    V = 40
+    tok = _tokens(g, n, V, "hot").cuda()
+    grad = _rand(g, n, d, F32)
+    h = handle(V, d, n)
+    got = []
+    for pad, offset in ((0, 0), (1, 0), (3, 1)):
+        src, table = _rand(g, n, d, F32, pad, offset), _rand(g, V, d, F32, pad, offset)
+        src.copy_(grad)
+        fr.fr_embed_grad(h, src, tok, table, scale=0.3)
+        got.append(table.clone())
+    assert torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])

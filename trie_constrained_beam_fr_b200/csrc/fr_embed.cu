@@ -19,7 +19,7 @@
 //                 fell on.
 //
 // The sort is stable and the partials are joined in order, so a sum's order
-// depends on the tokens alone: no floating-point atomics.
+// depends on the tokens and d alone: no floating-point atomics.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -670,7 +670,11 @@ cudaError_t em_grad(fr_embed* h, const void* grad, int64_t ldg, const int32_t* t
                     int64_t ldt, int32_t accumulate, cudaStream_t s) {
     const int32_t blocks = (int32_t)em_ceil(h->d, 32 * VEC * fr::EM_SMALL_GROUPS<VEC>);
     const int64_t zeros = accumulate ? 0 : em_ceil(h->V, fr::EM_ZERO_ROWS);
-    if (n <= fr::EM_SMALL && (int64_t)n * n * blocks <= fr::EM_SMALL_READS) {
+    // By n and d alone: the two forms add in different orders, and where rows start may
+    // not change a sum.  The price is paid by rows of a d that is a multiple of 8 which
+    // start off 16 bytes all the same: their CTAs have 128 columns, and twice as many read
+    // (1,400 tokens x 2,048 bf16 values from 2 bytes on: 50 us here, 26 sorted; added 40 and 27).
+    if (n <= fr::EM_SMALL && (int64_t)n * n * em_ceil(h->d, h->d % 8 ? 128 : 256) <= fr::EM_SMALL_READS) {
         if (n * (int64_t)blocks + zeros == 0) return cudaSuccess;
         return fr::launch_pdl(fr::k_em_small<TG, TT, VEC>, n * (int64_t)blocks + zeros, fr::EM_SMALL_THREADS, 0, s,
                               (const TG*)grad, ldg, h->d, tokens, n, h->V, scale, (TT*)table, ldt, accumulate, blocks, h->err);
