@@ -364,3 +364,26 @@ def test_refusals(handle):
         fr.fr_ce_loss(ce, odd, w, t, loss, lse)
     with pytest.raises(fr.FrError):  # base not on 16 bytes
         fr.fr_ce_loss(ce, torch.zeros(8 * 32 + 8, dtype=BF16, device="cuda")[1:257].view(8, 32), w, t, loss, lse)
+
+
+@pytest.mark.parametrize("big,small", [(1e30, 1e-10), (1e10, 1e-33), (3e38, 1e-12), (1.5, 1e-30), (2.0 ** 64, 2.0 ** -60)])
+def test_incoming_gradients_of_very_different_sizes(handle, big, small):
+    """A row's dh does not depend on the other rows' incoming gradients: rows
+    of small ones beside rows of large ones have the same relative bounds.  Only
+    entries of G that lie below 2^-126 at the scale they are kept at lose to subnormals."""
+    rows, V, d = 60, 130, 40
+    h, w, t, gl = _inputs(rows, V, d, 17, gain=1.0, ignored=0.1)
+    w *= 0.125  # results of the largest incoming gradients stay finite
+    gl = torch.where(torch.arange(rows, device="cuda") % 2 == 0, big, small) * torch.where(gl < 0, -0.5, 1.0)
+    gl = gl.float().contiguous()
+    ce = handle(V, d, rows)
+    loss, lse = _loss(ce, h, w, t)
+    dh, dw = _grad(ce, h, w, t, lse, gl)
+    ref = _reference(h, w, t, gl)
+    # subnormal steps: of G (2^-134, half of bf16's) in a sum over V and of the sums, at
+    # the scale that G is kept at (below 2, or the largest incoming gradient over 2^64)
+    slack = (V * 2.0 ** -134 * float(w.abs().max()) + (rows + V) * 2.0 ** -149) * max(2.0, big * 2.0 ** -64) + 2.0 ** -134
+    _close(dh, (ref["dh"][0], ref["dh"][1] + slack))
+    if big < 1e38:  # (dW sums many rows)
+        slack *= max(1.0, float(h.abs().max()) / float(w.abs().max()))
+        _close(dw, (ref["dw"][0], ref["dw"][1] + slack))

@@ -27,10 +27,11 @@
 //
 // G is rounded to bf16, the operand type of the products: half a step (2^-8)
 // of each entry, the same as one rounding of the inputs.  What is rounded is
-// G / max |g|; the maximum multiplies the fp32 sums.  So the entries at the
-// targets, which carry most of a gradient whose probabilities are spread, are
-// p - 1 without g's own rounding when all rows have the same g (a mean), and a
-// small or large g neither underflows nor overflows.
+// G / scale, where the scale is max |g| times a power of two (ce_scale); it
+// multiplies the fp32 sums.  So the entries at the targets, which carry most of
+// a gradient whose probabilities are spread, are p - 1 times a power of two,
+// without g's own rounding, when all rows have the same g (a mean), and a small
+// or large g neither underflows nor overflows.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -66,8 +67,19 @@ struct CeRows {
     float* g;          // [cap]
     int32_t* idx;      // [cap] original row
     int32_t* n;        // [1] counted rows
-    float* gmax;       // [1] largest finite |g| of a counted row, 1 if there is none or it is 0
+    float* gscale;     // [1] what g is divided by (ce_scale)
 };
+
+// What the incoming gradients are divided by before G is rounded, given the largest
+// finite |g| of a counted row: that value times a power of two (so an entry p - 1 of
+// equal g's still carries no rounding of g), below 2 unless it is above 2^65.  A
+// quotient by the value itself would push the small g's of a mixed batch below 2^-126
+// (beside 1e30, a g of 1e-10 lost all but a bit or two).  What is kept is at most 2^64, so no sum
+// of the products overflows before its result does.
+__device__ __forceinline__ float ce_scale(float largest) {
+    if (largest == 0.f) return 1.f;
+    return largest < 2.f ? largest : scalbnf(largest, -min(ilogbf(largest), 64));
+}
 
 // Rows that dW's K stages (64 rows each, at least one) run over.
 __device__ __forceinline__ int32_t ce_k_rows(int32_t n) { return max((n + 63) / 64, 1) * 64; }
@@ -178,7 +190,7 @@ __global__ void __launch_bounds__(CE_GATHER_THREADS)
         const uint32_t w = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
         if (lane == 0) atomicMax(&gmax_s, w);
         __syncthreads();
-        if (tid == 0) *out.gmax = gmax_s ? __uint_as_float(gmax_s) : 1.f;
+        if (tid == 0) *out.gscale = ce_scale(__uint_as_float(gmax_s));
     }
 }
 
@@ -319,7 +331,7 @@ struct CeGrad {
     struct State {
         int32_t n, m_tiles, dh_tiles, dw_tiles, g_tiles, dw_nk, dh_per;
         bool dw_first;
-        float gmax;
+        float scale;
     };
     CUtensorMap map_h_k, map_h_mn;   // packed rows: K-major (128 x 64) and MN-major (64 x 64) boxes
     CUtensorMap map_w_k, map_w_mn;   // weight: K-major (128 x 64) and MN-major (64 x 64) boxes
@@ -353,7 +365,7 @@ struct CeGrad {
     __device__ __forceinline__ State begin() const {
         State st;
         st.n = *rows.n;
-        st.gmax = *rows.gmax;
+        st.scale = *rows.gscale;
         st.m_tiles = max((st.n + TM - 1) / TM, 1);
         st.dh_tiles = dh && v1 > v0 && st.n ? st.m_tiles * d_tiles * splits : 0;
         st.dw_tiles = dw && v1 > v0 ? (v1 - v0 + TM - 1) / TM * d_tiles : 0;
@@ -441,7 +453,7 @@ struct CeGrad {
             if (row0 >= ce_k_rows(st.n)) return;  // rows that no product sums over
             const int cols = (bn() / 2 + 63) & ~63, c1 = min((half + 1) * cols, bn());
             const bool live = row < st.n;
-            const float g = live ? __fdiv_rn(rows.g[row], st.gmax) : 0.f, nl = live ? -rows.lse[row] * CE_L2E : 0.f;
+            const float g = live ? __fdiv_rn(rows.g[row], st.scale) : 0.f, nl = live ? -rows.lse[row] * CE_L2E : 0.f;
             const int32_t tgt = live ? rows.tgt[row] - w0 - t.n0 : -1;  // column in the tile
             const int width = w1 - w0 - t.n0;  // columns of this tile that are tokens
 #pragma unroll 1
@@ -481,7 +493,7 @@ struct CeGrad {
                 gm_ld64(taddr + (uint32_t)c, x);
                 if (c + 64 == c0 + GM_EPI_COLS) release();
 #pragma unroll
-                for (int i = 0; i < 64; ++i) x[i] *= st.gmax;
+                for (int i = 0; i < 64; ++i) x[i] *= st.scale;
                 if (v >= v1) continue;
                 if (t.n0 + c < dw_staged) {
                     gm_stage64(sg, &map_dw, lane, x, t.n0 + c, v);
@@ -507,12 +519,12 @@ __device__ __forceinline__ void ce_add(float4& x, const float4& y) {
     x.w += y.w;
 }
 
-// 4 columns of dh: times max |g|, rounded.
-__device__ __forceinline__ void ce_put(__nv_bfloat16* dst, int32_t j, int32_t d, float4 x, float gmax, bool vec) {
-    x.x *= gmax;
-    x.y *= gmax;
-    x.z *= gmax;
-    x.w *= gmax;
+// 4 columns of dh: times G's scale, rounded.
+__device__ __forceinline__ void ce_put(__nv_bfloat16* dst, int32_t j, int32_t d, float4 x, float scale, bool vec) {
+    x.x *= scale;
+    x.y *= scale;
+    x.z *= scale;
+    x.w *= scale;
     if (vec && j + 4 <= d) {
         const __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), b = __floats2bfloat162_rn(x.z, x.w);
         *reinterpret_cast<uint2*>(dst + j) =
@@ -534,14 +546,14 @@ __global__ void __launch_bounds__(CE_FINISH_THREADS)
     griddep_launch_dependents();
     const int64_t c = blockIdx.x;
     if (c >= *rows.n) return;
-    const float gmax = *rows.gmax;
+    const float scale = *rows.gscale;
     const float* src = dh + c * rows.pitch;
     __nv_bfloat16* dst = grad_hidden + rows.idx[c] * ldgh;
     for (int32_t j = threadIdx.x * 4; j < d; j += 4 * CE_FINISH_THREADS) {
         float4 x = *reinterpret_cast<const float4*>(src + j);
 #pragma unroll 8
         for (int k = 1; k < splits; ++k) ce_add(x, *reinterpret_cast<const float4*>(src + k * dh_split + j));
-        ce_put(dst, j, d, x, gmax, vec != 0);
+        ce_put(dst, j, d, x, scale, vec != 0);
     }
 }
 
@@ -570,7 +582,7 @@ __global__ void __launch_bounds__(CE_FINISH_THREADS)
     __syncthreads();
     if (group != 0 || j >= d) return;
     for (int k = 1; k < groups; ++k) ce_add(x, sums[k * width + q]);
-    ce_put(grad_hidden + rows.idx[c] * ldgh, j, d, x, *rows.gmax, vec != 0);
+    ce_put(grad_hidden + rows.idx[c] * ldgh, j, d, x, *rows.gscale, vec != 0);
 }
 
 int64_t ce_round(int64_t x, int64_t q) { return (x + q - 1) / q * q; }
@@ -809,7 +821,7 @@ extern "C" fr_status fr_ce_init(int32_t V, int32_t d, int32_t max_rows, fr_ce** 
     h->xt = h->rows.g + cap;
     h->rows.idx = reinterpret_cast<int32_t*>(h->xt + cap);
     h->rows.n = h->rows.idx + cap;
-    h->rows.gmax = reinterpret_cast<float*>(h->rows.n + 1);
+    h->rows.gscale = reinterpret_cast<float*>(h->rows.n + 1);
     h->counters = h->rows.n + 2;
     *out = h;
     return FR_OK;
