@@ -365,10 +365,15 @@ void fr_embed_destroy(fr_embed* embed);
  * h and W: base 16-byte aligned, pitches multiples of 8 elements (else
  * FR_ERR_INVALID_ARG).  The gradients' base and pitch only need the element's
  * alignment; 16-byte aligned ones are written faster.  Limits: d <= 2^20, V <=
- * 2^24, max_rows * V <= 2^44.  init allocates max_rows * (6 d + V / 16) bytes and
- * two pieces of G: 1 GB or 16 KB * max_rows, whichever is more, or less when V is
- * one piece (2 V * max_rows).  The kernels take one CTA per SM and all of its
- * tensor memory while they run, as fr_lmhead_run does. */
+ * 2^24, max_rows * V <= 2^44.  init allocates, with max_rows and V rounded up to
+ * multiples of 256 and d of 8 (also for a handle that only fr_ce_loss is called on):
+ *   max_rows * (2 d + V / 16 + 20) bytes and half a megabyte,
+ *   dh's fp32 sums, 4 d bytes for max_rows rows, or for 512 * SMs / ceil(d / 256)
+ *     where that is more (few rows are split: 78 MB on 148 SMs if d is a multiple of 256),
+ *   pieces of G: 2 V * max_rows bytes if that is one piece (at most 4,096 tokens, or
+ *     512 MB), else two pieces of 512 MB or 8 KB * max_rows each, whichever is more.
+ * The kernels take one CTA per SM and all of its tensor memory while they run, as
+ * fr_lmhead_run does. */
 typedef struct fr_ce fr_ce;
 fr_status fr_ce_init(int32_t V, int32_t d, int32_t max_rows, fr_ce** out);
 fr_status fr_ce_loss(fr_ce* ce, const void* hidden_dev, int64_t ldh, const void* weight_dev, int64_t ldw,

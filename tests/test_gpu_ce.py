@@ -387,3 +387,20 @@ def test_incoming_gradients_of_very_different_sizes(handle, big, small):
     if big < 1e38:  # (dW sums many rows)
         slack *= max(1.0, float(h.abs().max()) / float(w.abs().max()))
         _close(dw, (ref["dw"][0], ref["dw"][1] + slack))
+
+
+@pytest.mark.parametrize("V,d,rows", [(5120, 256, 1), (151936, 2048, 96), (300, 40, 150), (151936, 64, 2048), (9000, 96, 40000)])
+def test_a_handle_takes_the_memory_that_the_header_states(handle, V, d, rows):
+    """Of include/fr.h's account for fr_ce_init, and of no more: each of six
+    allocations is rounded up to the driver's 2 MB."""
+    handle(64, 64, 1)  # (what the first init loads)
+    torch.cuda.synchronize()
+    before = torch.cuda.mem_get_info()[0]
+    handle(V, d, rows)
+    taken = before - torch.cuda.mem_get_info()[0]
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    R, W, D = -(-rows // 256) * 256, -(-V // 256) * 256, -(-d // 8) * 8
+    piece = max(512 << 20, 8192 * R)
+    stated = R * (2 * D + W / 16 + 20) + (1 << 19) + 4 * D * max(R, 512 * sms // -(-d // 256))
+    stated += 2 * W * R if 2 * W * R <= piece else 2 * piece
+    assert 0 < taken <= stated + 6 * (2 << 20)
