@@ -404,3 +404,62 @@ def test_a_handle_takes_the_memory_that_the_header_states(handle, V, d, rows):
     stated = R * (2 * D + W / 16 + 20) + (1 << 19) + 4 * D * max(R, 512 * sms // -(-d // 256))
     stated += 2 * W * R if 2 * W * R <= piece else 2 * piece
     assert 0 < taken <= stated + 6 * (2 << 20)
+
+
+def _spread(t, borders):
+    """Targets of the counted rows dealt over the ranges between `borders`, first and last token of each among them."""
+    live = torch.nonzero(t >= 0)[:, 0]
+    at = []
+    for lo, hi in zip(borders, borders[1:]):
+        at += [lo, hi - 1, (lo + hi) // 2]
+    t[live] = torch.tensor(at, dtype=torch.int32, device="cuda").repeat(len(live) // len(at) + 1)[:len(live)]
+
+
+@pytest.mark.parametrize("rows,V,d,counted,pieces", [
+    (66000, 8500, 40, 0.01, (0, 4096, 8192, 8500)),           # three pieces of G, few of many rows count
+    (66000, 8200, 264, 0.005, (0, 4096, 8192, 8200)),         # a last piece of 8 tokens, two column tiles of dh
+    (200, 1048876, 8, 0.08, (0, 1048576, 1048876)),           # pairs: dh in splits, most of them empty in the last piece
+    (100, 1048876, 8, 0.15, (0, 1048576, 1048876)),           # the same on single CTAs
+])
+def test_gradients_over_several_pieces_of_the_vocabulary(handle, rows, V, d, counted, pieces):
+    """G is kept for 512 MB of a handle's rows by tokens at a time (4,096 tokens at
+    least).  The targets lie in every piece, so that a piece that was lost or added
+    twice would be off by a whole row of W or h.  An fp32 chain of dh has at most
+    16,384 terms (a split of a piece), and the splits and pieces are added to it."""
+    h, w, t, gl = _inputs(rows, V, d, rows + V, ignored=1 - counted, extra=8)
+    _spread(t, pieces)
+    ce = handle(V, d, rows)
+    loss, lse = _loss(ce, h, w, t)
+    dh, dw = _grad(ce, h, w, t, lse, gl, 3, 1)
+    assert fr.fr_ce_status(ce) == fr.FR_OK
+    live = t >= 0
+    assert torch.all(dh[~live] == 0)
+    ref = _reference(h[live], w, t[live], gl[live])
+    want, bound = ref["dh"]
+    if V > 16384:
+        hd, wd, at = h[live].double().cpu(), w.double().cpu(), t[live].long().cpu()[:, None]
+        G = torch.softmax(hd @ wd.T, 1)
+        G = (G - torch.zeros_like(G).scatter_(1, at, 1.0)) * gl[live].double().cpu()[:, None]
+        bound = bound - (V - 16384 - 512) * 2.0 ** -23 * (G.abs() @ wd.abs())
+    _close(dh[live], (want, bound))
+    _close(dw, ref["dw"])
+    _close(loss[live], ref["loss"])
+    a, b = _grad(ce, h, w, t, lse, gl, 3, 1)
+    assert torch.equal(a, dh) and torch.equal(b, dw)
+    a, b = torch.empty_like(dh), torch.empty_like(dw)
+    fr.fr_ce_grad(ce, h, w, t, lse, gl, a, None)
+    fr.fr_ce_grad(ce, h, w, t, lse, gl, None, b)
+    assert torch.equal(a, dh) and torch.equal(b, dw)
+
+
+@pytest.mark.parametrize("V", [700, 1300])
+def test_more_rows_than_a_group_of_tiles_holds(handle, V):
+    """Tile rows are walked 32 (8,192 rows) at a time: counted rows beyond, by several column tiles."""
+    rows, d = 9100, 24
+    h, w, t, gl = _inputs(rows, V, d, V, ignored=0.02)
+    ce = handle(V, d, rows)
+    loss, lse = _loss(ce, h, w, t)
+    dh, dw = _grad(ce, h, w, t, lse, gl)
+    ref = _reference(h, w, t, gl)
+    for got, name in ((loss, "loss"), (lse, "lse"), (dh, "dh"), (dw, "dw")):
+        _close(got, ref[name])
