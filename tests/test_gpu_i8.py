@@ -293,3 +293,44 @@ def test_refusals(handle):
         fr.fr_i8_matmul(h, _ints(g, 5, 32), torch.ones(5, device="cuda"), torch.ones(5, 40, device="cuda"))  # > max_rows
     with pytest.raises(fr.FrError):  # base not on 16 bytes
         fr.fr_i8_matmul(h, torch.zeros(4 * 32 + 1, dtype=torch.int8, device="cuda")[1:].view(4, 32), xs, out)
+
+
+# A tile of 256 columns is taken where that fills the pairs' rounds (74 pairs on 148
+# SMs), and more than 8,192 rows are walked in groups of 32 tile rows.
+WIDE = [(300, 9472, 64), (257, 9410, 300), (512, 9345, 128), (9000, 1000, 48), (8500, 2050, 272)]
+
+
+@pytest.mark.parametrize("tout", [F32, BF16])
+@pytest.mark.parametrize("rows,N,d", WIDE)
+def test_matmul_of_whole_tiles_and_groups(handle, tout, rows, N, d):
+    g = torch.Generator().manual_seed(rows + N + d)
+    xq, wq = _ints(g, rows, d), _ints(g, N, d, extra=16)
+    xs, ws = torch.rand(rows, generator=g).cuda(), torch.rand(N, generator=g).cuda()
+    h = handle(wq, ws, rows)
+    want = _product(xq, xs, wq, ws)
+    for pad in (0, 3, 8):  # rows that start on 16 bytes or not
+        out = torch.full((rows, N + pad), 5.0, dtype=tout, device="cuda")
+        fr.fr_i8_matmul(h, xq, xs, out[:, :N])
+        assert fr.fr_i8_status(h) == fr.FR_OK
+        err = (out[:, :N].double().cpu() - want).abs()
+        assert torch.all(err <= (3.1 * 2.0 ** -24 + torch.finfo(tout).eps / 2) * want.abs())
+        assert torch.all(out[:, N:] == 5.0)
+
+
+@pytest.mark.parametrize("rows,N,d,base,span", [(300, 9472, 64, 200, 700), (257, 9410, 300, 9310, 100), (512, 9345, 128, 0, 0),
+                                                (9000, 1000, 48, 250, 300), (8500, 2050, 272, 2049, 1)])
+def test_lse_of_whole_tiles_and_groups(handle, rows, N, d, base, span):
+    g = torch.Generator().manual_seed(rows + N)
+    xq, wq = _ints(g, rows, d), _ints(g, N, d)
+    xs = (torch.rand(rows, generator=g) / 73 + 1e-4).cuda()
+    ws = (torch.rand(N, generator=g) / 73 * 3 / d ** 0.5).cuda()
+    h = handle(wq, ws, rows, base, span)
+    lse, sl = torch.empty(rows, device="cuda"), torch.empty(rows, span, device="cuda")
+    fr.fr_i8_lse(h, xq, xs, lse, sl if span else None)
+    assert fr.fr_i8_status(h) == fr.FR_OK
+    y = _product(xq, xs, wq, ws)
+    want = torch.logsumexp(y, 1)
+    big = y.abs().amax(1)
+    bound = 3.1 * 2.0 ** -24 * big + (256 + N / 8192 + 8) * 2.0 ** -24 + 2.0 ** -22 + 2.0 ** -23 * (want.abs() + 3 * big)
+    assert torch.all((lse.double().cpu() - want).abs() <= bound)
+    assert torch.all((sl.double().cpu() - y[:, base:base + span]).abs() <= 3.1 * 2.0 ** -24 * y[:, base:base + span].abs())
