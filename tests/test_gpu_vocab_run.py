@@ -212,3 +212,30 @@ def test_an_error_of_a_run_right_after_init(which):
             assert status(h) == (want if wrong else fr.FR_OK), wrong
         finally:
             destroy(h)
+
+
+def test_every_call_refuses_tensors_on_the_cpu():
+    rows, V, d = 4, 32, 16
+    em, ce = fr.fr_embed_init(V, d, rows), fr.fr_ce_init(V, d, rows)
+    wq, ws = torch.ones(V, d, dtype=torch.int8, device="cuda"), torch.ones(V, device="cuda")
+    i8 = fr.fr_i8_init(wq, ws, rows, 0, 8)
+    table, h = torch.zeros(V, d, dtype=BF16, device="cuda"), torch.zeros(rows, d, dtype=BF16, device="cuda")
+    tok, f = torch.zeros(rows, dtype=torch.int32, device="cuda"), torch.zeros(rows, device="cuda")
+    xq, out, sl = torch.zeros(rows, d, dtype=torch.int8, device="cuda"), torch.zeros(rows, V, device="cuda"), torch.zeros(rows, 8, device="cuda")
+    calls = [
+        (fr.fr_embed_lookup, em, (table, tok, h)), (fr.fr_embed_grad, em, (h, tok, table)),
+        (fr.fr_ce_loss, ce, (h, table, tok, f, f)), (fr.fr_ce_grad, ce, (h, table, tok, f, f, h, table)),
+        (fr.fr_i8_quantize, None, (h, xq, f)), (fr.fr_i8_init, None, (wq, ws)),
+        (fr.fr_i8_matmul, i8, (xq, f, out)), (fr.fr_i8_lse, i8, (xq, f, f, sl)),
+    ]
+    try:
+        for call, handle, args in calls:
+            for k in range(len(args)):
+                moved = [a.cpu() if j == k else a for j, a in enumerate(args)]
+                tail = (rows,) if call is fr.fr_i8_init else ()
+                with pytest.raises(ValueError, match="CUDA"):
+                    call(*(() if handle is None else (handle,)), *moved, *tail)
+    finally:
+        fr.fr_embed_destroy(em)
+        fr.fr_ce_destroy(ce)
+        fr.fr_i8_destroy(i8)
