@@ -403,8 +403,8 @@ void fr_ce_destroy(fr_ce* ce);
  *
  * fr_i8_matmul:  out[r][n] = (sum_j xq[r][j] * wq[n][j]) * xscale[r] * wscale[n]
  *   into out [rows, ldo] of FR_F32 or FR_BF16, ldo >= N: with the lm_head as the
- *   weight, logits rows for fr_beam_step.  Exact int32 sums, two fp32 products,
- *   one rounding to the output type.
+ *   weight, logits rows for fr_beam_step.  Exact int32 sums, converted to fp32
+ *   (rounded above 2^24), two fp32 products, one rounding to the output type.
  * fr_i8_lse:  the same product reduced to lse [rows] and the SID slice
  *   [rows, sid_span] for fr_beam_step_lse, without writing the [rows, N]
  *   product; a row whose lse is not finite is recorded as FR_ERR_NAN_LOGIT.

@@ -31,7 +31,8 @@
 // multiplies the fp32 sums.  So the entries at the targets, which carry most of
 // a gradient whose probabilities are spread, are p - 1 times a power of two,
 // without g's own rounding, when all rows have the same g (a mean), and a small
-// or large g neither underflows nor overflows.
+// or large g neither underflows nor overflows.  A probability below 2^-126 counts
+// as 0 (the exponential flushes).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -51,8 +52,8 @@ namespace {
 
 // Tokens per piece of the gradient: at least CE_PIECE_MIN, and as many as keep
 // a piece of G within CE_PIECE_BYTES.  Every launch costs its start and its
-// uneven end: pieces of 128, 256 and 512 MB took 12.70, 12.48 and 12.31 ms on
-// 8,192 rows (d 2,048, V 151,936).
+// uneven end: pieces of 128, 256 and 512 MB took 11.62, 11.49 and 11.39 ms for
+// the gradients of 8,192 rows (d 2,048, V 151,936).
 constexpr int CE_PIECE_MIN = 4096;
 constexpr int64_t CE_PIECE_BYTES = 512 << 20;
 constexpr int64_t CE_PARTIALS_MORE = 1 << 16;  // for narrow tiles of small calls
@@ -215,7 +216,7 @@ __device__ __forceinline__ void ce_load_b_mn(const CUtensorMap* map, uint8_t* b,
 }
 
 // BN: tokens of a tile, known to the compiler (256) or not (0: narrow_bn).  Known,
-// 2,048 rows x 151,936 tokens x 2,048 values took 959 us instead of 1,016.
+// 2,048 rows x 151,936 tokens x 2,048 values took 915 us instead of 950.
 template <bool PAIR_, int BN>
 struct CeLoss {
     static constexpr bool I8 = false, STAGED = false, DYNAMIC = false, PAIR = PAIR_;
@@ -420,8 +421,8 @@ struct CeGrad {
         return true;
     }
     // Columns of a dh or dW tile: in the small calls' kernels those that are there,
-    // rounded up to a multiple of 32; else all (8,192 rows x 151,936 tokens: 15.0 ms, and
-    // 16.1 with a width that the compiler does not know).
+    // rounded up to a multiple of 32; else all (gradients of 8,192 rows x 151,936 tokens:
+    // 11.4 ms, and 12.6 with a width that the compiler does not know).
     __device__ __forceinline__ int width(const Tile& t) const { return BN ? GM_TILE : min((d - t.n0 + 31) & ~31, GM_TILE); }
     __device__ __forceinline__ uint32_t stage_bytes(const Tile& t) const {
         constexpr int CTAS = PAIR ? 2 : 1;
