@@ -303,9 +303,9 @@ void fr_beam_destroy(fr_beam* beam);
  * stream; when they return, the handle can be used on any stream.  Its workspace
  * is shared by all its runs, so runs of one handle (captured graphs included) must
  * be ordered one after another, by one stream or by events; use one handle per
- * stream for runs that may overlap.  Runs allocate nothing, never synchronise and can be captured into a
- * CUDA graph.  Inputs, outputs and workspace may not overlap, except where an
- * output is said to be added to.  The status calls are as fr_beam_status:
+ * stream for runs that may overlap.  Runs allocate nothing, never synchronise and
+ * can be captured into a CUDA graph.  Inputs, outputs and workspace may not
+ * overlap, except where an output is said to be added to.  The status calls are as fr_beam_status:
  * sticky, first error first, read with a synchronisation of the last run's
  * stream (not while that stream is being captured). */
 

@@ -75,8 +75,8 @@ struct CeRows {
 // finite |g| of a counted row: that value times a power of two (so an entry p - 1 of
 // equal g's still carries no rounding of g), below 2 unless it is above 2^65.  A
 // quotient by the value itself would push the small g's of a mixed batch below 2^-126
-// (beside 1e30, a g of 1e-10 lost all but a bit or two).  What is kept is at most 2^64, so no sum
-// of the products overflows before its result does.
+// (beside 1e30, a g of 1e-10 lost all but a bit or two).  What is kept is at most
+// 2^64, so no sum of the products overflows before its result does.
 __device__ __forceinline__ float ce_scale(float largest) {
     if (largest == 0.f) return 1.f;
     return largest < 2.f ? largest : scalbnf(largest, -min(ilogbf(largest), 64));
